@@ -93,7 +93,8 @@ typedef enum {
   MLA_ERR_CUDA = -4,        /* a CUDA runtime/driver call or a kernel launch failed */
   MLA_ERR_TIMEOUT = -5,     /* device only: a bounded wait inside a kernel gave up */
   MLA_ERR_BAD_INDEX = -6,   /* device only: a block id outside [0, num_blocks) or a bad position */
-  MLA_ERR_STATIC_WS = -7    /* the shape needs more scratch than mla_decode_noalloc's built-in buffer */
+  MLA_ERR_STATIC_WS = -7,   /* the shape needs more scratch than mla_decode_noalloc's built-in buffer */
+  MLA_ERR_NO_BLOCKS = -8    /* device only: mla_plan_step found too few free blocks */
 } mla_status;
 
 typedef enum { MLA_F32 = 0, MLA_BF16 = 1 } mla_dtype;
@@ -388,6 +389,118 @@ MLA_API int mla_decode_sparse(const mla_dims *dims, int B, int n_q, const void *
                               int num_blocks, const int32_t *seqlens, int max_seqlen, const int32_t *topk_idx,
                               int topk, const void *w_uk, const void *w_uv, void *out, float *lse, void *workspace,
                               size_t ws_bytes, int *dev_status, mla_stream_t stream);
+
+/*
+ * mla_decode_shared_workspace_size / mla_decode_shared — the decode of mla_decode
+ *   for a batch whose sequences share the first tokens of the cache in groups
+ *   (a common prompt, several samples of one request): the shared keys of a
+ *   group are attended to once, by the query rows of all its sequences
+ *   together, the rest of every sequence by its own rows, and the two partial
+ *   results are merged by their log-sum-exps (exact, as in mla_merge_partials).
+ *   "Transformer升级之路：21、MLA好在哪里?（下）", section 双重投影, decoding
+ *   column: every head attends to the same cached rows, so the heads and the
+ *   sequences of a group are alike to the kernel: rows of one product.
+ *   group_offsets [num_groups + 1] (int32, device): group g is the sequences
+ *   group_offsets[g] .. group_offsets[g+1] - 1; the offsets rise from 0 to B.
+ *   prefix_lens [num_groups] (int32, device, >= 0): how many first tokens the
+ *   group's sequences have in common.  They are read through the block table
+ *   row of the group's first sequence; the table rows of the others must name
+ *   the same blocks for the whole blocks among these tokens (not checked; the
+ *   tokens of a block that is only partly shared are read through each
+ *   sequence's own row).  prefix_lens may exceed what the sequences hold or
+ *   see: the common part ends at the first query token of the group's
+ *   shortest sequence.  num_groups == 0: nothing is shared, and both arrays may
+ *   be NULL.  On the device, offsets that do not rise from 0 to B or a negative
+ *   prefix length report MLA_ERR_BAD_INDEX, and then nothing is shared.
+ *   block_table is required.  w_uv == NULL writes o_lat [B, n_q, H, d_c], as
+ *   mla_decode_latent.  The other arguments, outputs and errors as mla_decode.
+ *   Shapes of the tensor-core path (mla_decode_path) share; other shapes run
+ *   every sequence by itself, with the same results.
+ *   Workspace: >= mla_decode_shared_workspace_size bytes, 256-byte aligned.
+ */
+MLA_API int mla_decode_shared_workspace_size(const mla_dims *dims, int B, int n_q, int max_seqlen, int num_groups,
+                                             size_t *bytes);
+MLA_API int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *q_nope, const void *q_pe,
+                              const void *c_kv, const void *k_pe, const int32_t *block_table, int max_blocks_per_seq,
+                              int num_blocks, const int32_t *seqlens, int max_seqlen, int num_groups,
+                              const int32_t *group_offsets, const int32_t *prefix_lens, const void *w_uk,
+                              const void *w_uv, void *out, float *lse, void *workspace, size_t ws_bytes,
+                              int *dev_status, mla_stream_t stream);
+
+/*
+ * mla_plan_step — the bookkeeping of one step over the paged cache, on the GPU:
+ *   block tables, sequence lengths and slot maps from the requests' lengths.
+ *   The source pages have no counterpart (they do not page the cache); its
+ *   outputs are the index arguments of mla_append_latent, mla_decode,
+ *   mla_decode_shared and mla_prefill.
+ *   Request b holds cached_lens[b] tokens and receives new_lens[b] >= 0 more.
+ *   All arrays are int32 device memory unless said otherwise.
+ *   - cu_seqlens [B + 1]: prefix sums of new_lens; token t of the step belongs
+ *     to the request whose range holds t.
+ *   - New blocks are taken from the end of free_list [free_capacity], of which
+ *     the first *free_count entries are free: the k-th new block of the step
+ *     (requests in order, each request's blocks in order) is
+ *     free_list[*free_count - 1 - k], and goes to
+ *     block_table[b, ceil(cached_lens[b] / block_size) ..].  *free_count_out is
+ *     what is left; free_list is not written.
+ *   - Groups of requests may share the first blocks of the cache: group_offsets
+ *     and prefix_lens as in mla_decode_shared, prefix_lens[g] a multiple of
+ *     block_size, whose blocks are prefix_table[g, 0 ..]
+ *     ([num_groups, max_prefix_blocks]).  The prefix counts as cached: a request
+ *     joins with cached_lens[b] == prefix_lens[g], and then the group's blocks
+ *     are written to the start of its table row.  num_groups == 0: the three
+ *     arrays may be NULL.
+ *   - seqlens [B] = cached_lens + new_lens; seq_idx, pos [max_tokens] and slots
+ *     [max_tokens] (int64, may be NULL): request, 0-based position and pool row
+ *     of every token of the step.  Entries behind the last token are left as
+ *     they were.
+ *   - A request that cannot be served is left as it is: seqlens[b] =
+ *     max(cached_lens[b], 0), its table row is not written, it takes no
+ *     blocks, and its tokens have seq_idx = pos = slots = -1
+ *     (mla_append_latent skips and reports such rows).  Requests are served in
+ *     order; the first whose new blocks do not fit *free_count is refused with
+ *     all later ones that need a block (MLA_ERR_NO_BLOCKS).  Refused with
+ *     MLA_ERR_BAD_INDEX: a negative length, new_lens[b] > max_tokens (these two
+ *     have no tokens in cu_seqlens), a total beyond the table row or 2^31 - 1,
+ *     tokens that do not all fit max_tokens, cached_lens[b] below the group's
+ *     prefix, and a prefix that is negative, not whole blocks, or longer than
+ *     prefix_table.  Free ids outside [0, num_blocks) report MLA_ERR_BAD_INDEX;
+ *     the table gets -1 there, and so do the tokens.  Group offsets that do not
+ *     rise from 0 to B report MLA_ERR_BAD_INDEX, and no request has a prefix.
+ *   seqlens may be cached_lens itself and free_count_out may be free_count
+ *   itself: the state of a loop, or of a replayed graph, is updated in place.
+ *   The other outputs overlap nothing.  dims: block_size and the checks of
+ *   every call.  B <= 8192 (else MLA_ERR_UNSUPPORTED); one kernel, no workspace.
+ */
+MLA_API int mla_plan_step(const mla_dims *dims, int B, const int32_t *cached_lens, const int32_t *new_lens,
+                          int num_groups, const int32_t *group_offsets, const int32_t *prefix_lens,
+                          const int32_t *prefix_table, int max_prefix_blocks, const int32_t *free_list,
+                          int free_capacity, const int32_t *free_count, int32_t *block_table, int max_blocks_per_seq,
+                          int num_blocks, int max_tokens, int32_t *seqlens, int32_t *cu_seqlens, int32_t *seq_idx,
+                          int32_t *pos, int64_t *slots, int32_t *free_count_out, int *dev_status,
+                          mla_stream_t stream);
+
+/*
+ * mla_release_blocks — the blocks of finished requests go back to the free list.
+ *   For every request with done[b] != 0, in order, the blocks of its own tokens
+ *   (block_table[b, prefix_lens[g] / block_size .. ceil(seqlens[b] / block_size) - 1],
+ *   in order; all of them without groups) are appended to free_list at
+ *   *free_count, and seqlens_out[b] = 0; other requests keep seqlens[b].  The
+ *   blocks of a shared prefix belong to no request and are not returned; the
+ *   table is not written.  *free_count_out is the new number of free blocks.
+ *   group_offsets, prefix_lens as in mla_plan_step.  A request whose blocks do
+ *   not fit free_capacity, and every later one with blocks to return, keeps
+ *   them and its length (MLA_ERR_BAD_INDEX); so does one whose length is
+ *   negative or beyond the table row, or whose prefix is not whole blocks.
+ *   Block ids outside [0, num_blocks) are reported (MLA_ERR_BAD_INDEX) and
+ *   returned as they are.  seqlens_out may be seqlens and free_count_out may be
+ *   free_count.  B <= 8192 (else MLA_ERR_UNSUPPORTED); one kernel, no workspace.
+ */
+MLA_API int mla_release_blocks(const mla_dims *dims, int B, const int32_t *done, const int32_t *seqlens,
+                               int num_groups, const int32_t *group_offsets, const int32_t *prefix_lens,
+                               const int32_t *block_table, int max_blocks_per_seq, int num_blocks, int32_t *free_list,
+                               int free_capacity, const int32_t *free_count, int32_t *seqlens_out,
+                               int32_t *free_count_out, int *dev_status, mla_stream_t stream);
 
 /*
  * mla_prefill_workspace_size — scratch bytes of mla_prefill for total_tokens

@@ -22,7 +22,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 MLA_F32, MLA_BF16 = 0, 1
 MLA_CACHE_ROWS, MLA_CACHE_TILED = 0, 1
 STATUS = {0: "MLA_OK", -1: "MLA_ERR_INVALID_ARG", -2: "MLA_ERR_UNSUPPORTED", -3: "MLA_ERR_WORKSPACE",
-          -4: "MLA_ERR_CUDA", -5: "MLA_ERR_TIMEOUT", -6: "MLA_ERR_BAD_INDEX", -7: "MLA_ERR_STATIC_WS"}
+          -4: "MLA_ERR_CUDA", -5: "MLA_ERR_TIMEOUT", -6: "MLA_ERR_BAD_INDEX", -7: "MLA_ERR_STATIC_WS",
+          -8: "MLA_ERR_NO_BLOCKS"}
 NOALLOC_SCRATCH_BYTES = 16 << 20   # MLA_NOALLOC_SCRATCH_BYTES in include/mla.h
 
 
@@ -79,6 +80,11 @@ _sigs = {
     "mla_merge_partials": [_D, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "mla_decode_sparse": [_D, _I, _I, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P,
                           ctypes.c_size_t, _P, _P],
+    "mla_decode_shared_workspace_size": [_D, _I, _I, _I, _I, _SZ],
+    "mla_decode_shared": [_D, _I, _I, _P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P,
+                          ctypes.c_size_t, _P, _P],
+    "mla_plan_step": [_D, _I, _P, _P, _I, _P, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P],
+    "mla_release_blocks": [_D, _I, _P, _P, _I, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P, _P, _P],
     "mla_decode_launches": [_D, _I, ctypes.POINTER(ctypes.c_int)],
     "mla_decode_path": [_D, _I, ctypes.POINTER(ctypes.c_int)],
     "mla_cache_pack": [_D, _P, _P, ctypes.c_int64, _P],
@@ -368,6 +374,135 @@ def mla_decode_sparse(dims, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_pe
                                 ctypes.c_size_t(workspace.numel() * workspace.element_size()),
                                 _ptr(dev_status, torch.int32, "dev_status", True), _stream(stream))
     _check("mla_decode_sparse", rc)
+
+
+def mla_decode_shared_workspace_size(dims, B, n_q, max_seqlen, num_groups) -> int:
+    n = ctypes.c_size_t(0)
+    _check("mla_decode_shared_workspace_size",
+           _lib.mla_decode_shared_workspace_size(ctypes.byref(dims), int(B), int(n_q), int(max_seqlen),
+                                                 int(num_groups), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _group_args(B, group_offsets, prefix_lens):
+    """(num_groups, group_offsets, prefix_lens) as the C calls take them; both None: no groups."""
+    if (group_offsets is None) != (prefix_lens is None):
+        raise ValueError("group_offsets and prefix_lens go together")
+    if group_offsets is None:
+        return 0, None, None
+    _same_shape(prefix_lens, (group_offsets.numel() - 1,), "prefix_lens")
+    if not 0 < prefix_lens.numel() <= B:
+        raise ValueError("there must be 1 .. B groups")
+    return (prefix_lens.numel(), _ptr(_dense(group_offsets, "group_offsets"), torch.int32, "group_offsets"),
+            _ptr(_dense(prefix_lens, "prefix_lens"), torch.int32, "prefix_lens"))
+
+
+def _same_shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _on_current_device(*tensors):
+    """The kernels run on the current device: tensors of another one are refused."""
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def mla_decode_shared(dims, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,
+                      max_seqlen, group_offsets, prefix_lens, w_uk, w_uv, out, lse, workspace, dev_status=None,
+                      stream=None):
+    """mla_decode for groups of sequences that share their first tokens: group_offsets [G + 1] and prefix_lens [G]
+    (int32, device); the shared tokens of a group are attended to once for all its sequences.  w_uv None: out is
+    o_lat [B, n_q, H, d_c]."""
+    et = _elem_dtype(dims)
+    B, n_q = q_nope.shape[0], q_nope.shape[1]
+    for n, t in (("q_nope", q_nope), ("q_pe", q_pe), ("block_table", block_table), ("seqlens", seqlens),
+                 ("w_uk", w_uk), ("w_uv", w_uv), ("out", out), ("lse", lse)):
+        _dense(t, n)
+    H, dv = dims.n_heads, dims.d_v if w_uv is not None else dims.d_c
+    for n, t, shape in (("q_nope", q_nope, (B, n_q, H, dims.d_nope)), ("q_pe", q_pe, (B, n_q, H, dims.d_rope)),
+                        ("seqlens", seqlens, (B,)), ("block_table", block_table, (B, max_blocks_per_seq)),
+                        ("w_uk", w_uk, (H, dims.d_c, dims.d_nope)), ("w_uv", w_uv, (H, dims.d_c, dims.d_v)),
+                        ("out", out, (B, n_q, H, dv)), ("lse", lse, (B, n_q, H))):
+        if t is not None:
+            _same_shape(t, shape, n)
+    _on_current_device(q_nope, q_pe, c_kv, k_pe, block_table, seqlens, group_offsets, prefix_lens, w_uk, w_uv, out, lse,
+                       workspace, dev_status)
+    G, offs, lens = _group_args(B, group_offsets, prefix_lens)
+    rc = _lib.mla_decode_shared(ctypes.byref(dims), B, n_q, _ptr(q_nope, et, "q_nope"), _ptr(q_pe, et, "q_pe"),
+                                _ptr(c_kv, et, "c_kv"), _ptr(k_pe, et, "k_pe", True),
+                                _ptr(block_table, torch.int32, "block_table"), int(max_blocks_per_seq),
+                                int(num_blocks), _ptr(seqlens, torch.int32, "seqlens"), int(max_seqlen), G, offs, lens,
+                                _ptr(w_uk, et, "w_uk"), _ptr(w_uv, et, "w_uv", True), _ptr(out, et, "out"),
+                                _ptr(lse, torch.float32, "lse", True), _ptr(workspace, None, "workspace"),
+                                ctypes.c_size_t(workspace.numel() * workspace.element_size()),
+                                _ptr(dev_status, torch.int32, "dev_status", True), _stream(stream))
+    _check("mla_decode_shared", rc)
+
+
+def mla_plan_step(dims, cached_lens, new_lens, group_offsets, prefix_lens, prefix_table, free_list, free_count,
+                  block_table, num_blocks, seqlens, cu_seqlens, seq_idx, pos, slots, free_count_out, dev_status=None,
+                  stream=None):
+    """Block tables, lengths and slot maps of a step from the requests' lengths.  block_table [B, max_blocks] is
+    updated in place; seqlens [B], cu_seqlens [B + 1], seq_idx and pos [max_tokens], slots [max_tokens] (int64, or
+    None) and free_count_out [1] are written.  seqlens may be cached_lens and free_count_out may be free_count.
+    group_offsets, prefix_lens and prefix_table [G, max_prefix_blocks] are None without shared prefixes."""
+    i32 = torch.int32
+    B = cached_lens.numel()
+    for n, t in (("cached_lens", cached_lens), ("new_lens", new_lens), ("prefix_table", prefix_table),
+                 ("free_list", free_list), ("block_table", block_table), ("seqlens", seqlens),
+                 ("cu_seqlens", cu_seqlens), ("seq_idx", seq_idx), ("pos", pos), ("slots", slots)):
+        _dense(t, n)
+    for n, t, shape in (("new_lens", new_lens, (B,)), ("seqlens", seqlens, (B,)), ("cu_seqlens", cu_seqlens, (B + 1,)),
+                        ("pos", pos, tuple(seq_idx.shape)), ("free_count", free_count, (1,)),
+                        ("free_count_out", free_count_out, (1,))):
+        _same_shape(t, shape, n)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks_per_seq]")
+    if slots is not None:
+        _same_shape(slots, seq_idx.shape, "slots")
+    _on_current_device(cached_lens, new_lens, group_offsets, prefix_lens, prefix_table, free_list, free_count,
+                       block_table, seqlens, cu_seqlens, seq_idx, pos, slots, free_count_out, dev_status)
+    G, offs, lens = _group_args(B, group_offsets, prefix_lens)
+    if G and (prefix_table is None or prefix_table.dim() != 2 or prefix_table.shape[0] != G):
+        raise ValueError("prefix_table must be [num_groups, max_prefix_blocks]")
+    rc = _lib.mla_plan_step(ctypes.byref(dims), B, _ptr(cached_lens, i32, "cached_lens"),
+                            _ptr(new_lens, i32, "new_lens"), G, offs, lens,
+                            _ptr(prefix_table, i32, "prefix_table", True), int(prefix_table.shape[1]) if G else 0,
+                            _ptr(free_list, i32, "free_list"), free_list.numel(), _ptr(free_count, i32, "free_count"),
+                            _ptr(block_table, i32, "block_table"), int(block_table.shape[1]), int(num_blocks),
+                            seq_idx.numel(), _ptr(seqlens, i32, "seqlens"), _ptr(cu_seqlens, i32, "cu_seqlens"),
+                            _ptr(seq_idx, i32, "seq_idx"), _ptr(pos, i32, "pos"),
+                            _ptr(slots, torch.int64, "slots", True), _ptr(free_count_out, i32, "free_count_out"),
+                            _ptr(dev_status, i32, "dev_status", True), _stream(stream))
+    _check("mla_plan_step", rc)
+
+
+def mla_release_blocks(dims, done, seqlens, group_offsets, prefix_lens, block_table, num_blocks, free_list,
+                       free_count, seqlens_out, free_count_out, dev_status=None, stream=None):
+    """The own blocks of every request with done[b] != 0 are appended to free_list; its length becomes 0.
+    seqlens_out may be seqlens and free_count_out may be free_count."""
+    i32 = torch.int32
+    B = seqlens.numel()
+    for n, t in (("done", done), ("seqlens", seqlens), ("block_table", block_table), ("free_list", free_list),
+                 ("seqlens_out", seqlens_out)):
+        _dense(t, n)
+    for n, t, shape in (("done", done, (B,)), ("seqlens_out", seqlens_out, (B,)), ("free_count", free_count, (1,)),
+                        ("free_count_out", free_count_out, (1,))):
+        _same_shape(t, shape, n)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks_per_seq]")
+    _on_current_device(done, seqlens, group_offsets, prefix_lens, block_table, free_list, free_count, seqlens_out,
+                       free_count_out, dev_status)
+    G, offs, lens = _group_args(B, group_offsets, prefix_lens)
+    rc = _lib.mla_release_blocks(ctypes.byref(dims), B, _ptr(done, i32, "done"), _ptr(seqlens, i32, "seqlens"), G,
+                                 offs, lens, _ptr(block_table, i32, "block_table"), int(block_table.shape[1]),
+                                 int(num_blocks), _ptr(free_list, i32, "free_list"), free_list.numel(),
+                                 _ptr(free_count, i32, "free_count"), _ptr(seqlens_out, i32, "seqlens_out"),
+                                 _ptr(free_count_out, i32, "free_count_out"), _ptr(dev_status, i32, "dev_status", True),
+                                 _stream(stream))
+    _check("mla_release_blocks", rc)
 
 
 def mla_decode_latent(dims, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,

@@ -377,8 +377,80 @@ const char *mla_status_string(int s) {
     case MLA_ERR_TIMEOUT: return "device wait timed out";
     case MLA_ERR_BAD_INDEX: return "block id, sequence index or position out of range";
     case MLA_ERR_STATIC_WS: return "shape needs more scratch than the built-in no-allocation buffer";
+    case MLA_ERR_NO_BLOCKS: return "too few free cache blocks";
     default: return "unknown status";
   }
+}
+
+int mla_decode_shared_workspace_size(const mla_dims *dims, int B, int n_q, int max_seqlen, int num_groups,
+                                     size_t *bytes) {
+  if (!dims_ok(dims) || B <= 0 || n_q <= 0 || max_seqlen < n_q || num_groups < 0 || num_groups > B || !bytes)
+    return MLA_ERR_INVALID_ARG;
+  if (n_q * dims->n_heads > 256) return MLA_ERR_UNSUPPORTED;
+  *bytes = decode_layout(dims, B, n_q, max_seqlen).total;
+  return MLA_OK;
+}
+
+int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *q_nope, const void *q_pe, const void *c_kv,
+                      const void *k_pe, const int32_t *block_table, int max_blocks_per_seq, int num_blocks,
+                      const int32_t *seqlens, int max_seqlen, int num_groups, const int32_t *group_offsets,
+                      const int32_t *prefix_lens, const void *w_uk, const void *w_uv, void *out, float *lse,
+                      void *workspace, size_t ws_bytes, int *dev_status, mla_stream_t stream) {
+  if (num_groups < 0 || num_groups > B || !block_table || (num_groups > 0 && (!group_offsets || !prefix_lens)))
+    return MLA_ERR_INVALID_ARG;
+  return decode_impl(dims, B, n_q, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,
+                     max_seqlen, w_uk, w_uv, out, lse, workspace, ws_bytes, dev_status,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+// What the two bookkeeping calls check alike.
+static int check_book_args(const mla_dims *dims, int B, int num_groups, const int32_t *group_offsets,
+                           const int32_t *prefix_lens, const int32_t *block_table, int max_blocks_per_seq,
+                           int num_blocks, const int32_t *free_list, int free_capacity, const int32_t *free_count,
+                           const int32_t *free_count_out) {
+  if (!dims_ok(dims) || B <= 0 || num_groups < 0 || num_groups > B || max_blocks_per_seq <= 0 || num_blocks <= 0 ||
+      free_capacity < 0)
+    return MLA_ERR_INVALID_ARG;
+  if ((num_groups > 0 && (!group_offsets || !prefix_lens)) || !block_table || (!free_list && free_capacity > 0) ||
+      !free_count || !free_count_out)
+    return MLA_ERR_INVALID_ARG;
+  return B > kPlanMaxRequests ? MLA_ERR_UNSUPPORTED : MLA_OK;
+}
+
+int mla_plan_step(const mla_dims *dims, int B, const int32_t *cached_lens, const int32_t *new_lens, int num_groups,
+                  const int32_t *group_offsets, const int32_t *prefix_lens, const int32_t *prefix_table,
+                  int max_prefix_blocks, const int32_t *free_list, int free_capacity, const int32_t *free_count,
+                  int32_t *block_table, int max_blocks_per_seq, int num_blocks, int max_tokens, int32_t *seqlens,
+                  int32_t *cu_seqlens, int32_t *seq_idx, int32_t *pos, int64_t *slots, int32_t *free_count_out,
+                  int *dev_status, mla_stream_t stream) {
+  const int rc = check_book_args(dims, B, num_groups, group_offsets, prefix_lens, block_table, max_blocks_per_seq,
+                                 num_blocks, free_list, free_capacity, free_count, free_count_out);
+  if (rc) return rc;
+  if (!cached_lens || !new_lens || !seqlens || !cu_seqlens || max_prefix_blocks < 0 || max_tokens < 0 ||
+      (num_groups > 0 && max_prefix_blocks > 0 && !prefix_table) || (max_tokens > 0 && (!seq_idx || !pos)))
+    return MLA_ERR_INVALID_ARG;
+  const uintptr_t low = reinterpret_cast<uintptr_t>(seq_idx) | reinterpret_cast<uintptr_t>(pos) |
+                        reinterpret_cast<uintptr_t>(slots);
+  const StepPlanArgs a{B, num_groups, dims->block_size, max_blocks_per_seq, num_blocks, max_prefix_blocks,
+                       free_capacity, max_tokens, cached_lens, new_lens, group_offsets, prefix_lens, prefix_table,
+                       free_list, free_count, block_table, seqlens, cu_seqlens, seq_idx, pos, slots, free_count_out,
+                       dev_status, (low & 15) == 0};
+  return launch_step_plan(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mla_release_blocks(const mla_dims *dims, int B, const int32_t *done, const int32_t *seqlens, int num_groups,
+                       const int32_t *group_offsets, const int32_t *prefix_lens, const int32_t *block_table,
+                       int max_blocks_per_seq, int num_blocks, int32_t *free_list, int free_capacity,
+                       const int32_t *free_count, int32_t *seqlens_out, int32_t *free_count_out, int *dev_status,
+                       mla_stream_t stream) {
+  const int rc = check_book_args(dims, B, num_groups, group_offsets, prefix_lens, block_table, max_blocks_per_seq,
+                                 num_blocks, free_list, free_capacity, free_count, free_count_out);
+  if (rc) return rc;
+  if (!done || !seqlens || !seqlens_out) return MLA_ERR_INVALID_ARG;
+  const ReleaseArgs a{B, num_groups, dims->block_size, max_blocks_per_seq, num_blocks, free_capacity, done, seqlens,
+                      group_offsets, prefix_lens, block_table, free_list, free_count, seqlens_out, free_count_out,
+                      dev_status};
+  return launch_release(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 static AppendArgs append_args(const mla_dims *dims, int T, const void *h, const void *w_dkv, const void *w_kr,

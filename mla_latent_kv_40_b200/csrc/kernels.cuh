@@ -140,6 +140,33 @@ inline size_t prefill_tiled_bytes(int B, int H, int max_seqlen) {
   return ((q + 255) & ~size_t(255)) + (size_t)H * B * 2 * nqt * kPfKVTileBytes;
 }
 
+// Bookkeeping of a step: block tables, lengths and slot maps from the requests' lengths.
+struct StepPlanArgs {
+  int B, num_groups, block_size, max_blocks_per_seq, num_blocks, max_prefix_blocks, free_capacity, max_tokens;
+  const int32_t *cached_lens, *new_lens;              // [B]
+  const int32_t *group_offsets, *prefix_lens;         // [num_groups + 1], [num_groups]
+  const int32_t *prefix_table;                        // [num_groups, max_prefix_blocks]
+  const int32_t *free_list, *free_count;
+  int32_t *block_table, *seqlens, *cu_seqlens, *seq_idx, *pos;
+  int64_t *slots;                                     // or NULL
+  int32_t *free_count_out;
+  int *dev_status;
+  int vec;                                            // seq_idx, pos and slots are 16-byte aligned
+};
+// Return of finished requests' blocks to the free list.
+struct ReleaseArgs {
+  int B, num_groups, block_size, max_blocks_per_seq, num_blocks, free_capacity;
+  const int32_t *done, *seqlens;                      // [B]
+  const int32_t *group_offsets, *prefix_lens, *block_table;
+  int32_t *free_list;
+  const int32_t *free_count;
+  int32_t *seqlens_out, *free_count_out;
+  int *dev_status;
+};
+constexpr int kPlanMaxRequests = 8192;                // four words of shared memory per request
+int launch_step_plan(const StepPlanArgs &a, cudaStream_t st);
+int launch_release(const ReleaseArgs &a, cudaStream_t st);
+
 int launch_append(const AppendArgs &a, bool bf16, cudaStream_t st);
 int launch_absorb(const AbsorbArgs &a, bool bf16, cudaStream_t st);
 int launch_attn_simt(const AttnArgs &a, bool bf16, cudaStream_t st);

@@ -1,0 +1,402 @@
+// Bookkeeping of the paged latent cache on the GPU: the block tables, lengths and slot maps of a step
+// from the requests' lengths (mla_plan_step), and the return of finished requests' blocks
+// (mla_release_blocks).
+//
+// Mathematics.  With block size s, request b holding c_b tokens and receiving n_b:
+//   need_b = ceil((c_b + n_b) / s) - ceil(c_b / s),   N_b = need_0 + .. + need_b,
+//   b is served iff need_b = 0 or N_b <= F (F free blocks),
+//   its i-th new block is free_list[F - 1 - (N_b - need_b + i)],
+//   token t of the step belongs to the request whose range of the prefix sums of n holds t.
+// All of it is two prefix sums over the requests and one search per four tokens (or ids).
+//
+// Shape.  One cluster of kCtas CTAs does the whole call in one launch: every CTA loads the lengths and
+// forms the prefix sums in its own shared memory (redundantly: they are a few KB and the alternative is
+// a second launch), then the table entries and tokens are dealt out over all threads of the cluster.
+// The outputs that may alias inputs (lengths, free count) are written after a cluster barrier that every
+// CTA enters once it has read them, so the state of a serving loop can be updated in place, also in a
+// replayed graph.  No atomics: the result does not depend on timing.  The call is bound by latency (the
+// dependent loads of the scan and of the search), not by its bytes.
+#include "kernels.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int kCtas = 8;          // the largest portable cluster
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kPer = 4;           // consecutive tokens (or block ids) per thread and search
+
+// Inclusive block-wide prefix sum of one value per thread.  `part` holds kWarps values; the caller
+// synchronises before it is used again.
+__device__ __forceinline__ long long block_scan(long long v, long long *part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  long long w = part[lane];      // kWarps == 32: every warp scans the warps' totals
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  const long long before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  __syncthreads();
+  return v + (warp > 0 ? before : 0);
+}
+static_assert(kWarps == 32, "block_scan reads one total per lane");
+
+// Exclusive prefix sums of in[0..n) into out[0..n], thread i owning items i * per .. (i + 1) * per - 1;
+// values are clamped to `most` on the way out.  Returns the total to every thread.
+template <typename F>
+__device__ __forceinline__ long long scan_items(int n, int per, long long most, int32_t *out, long long *part, F item) {
+  const int lo = min(n, (int)threadIdx.x * per), hi = min(n, lo + per);
+  long long sum = 0;
+  for (int i = lo; i < hi; ++i) sum += item(i);
+  const long long inc = block_scan(sum, part);
+  long long at = inc - sum;
+  for (int i = lo; i < hi; ++i) {
+    const long long v = item(i);
+    out[i] = (int32_t)min(at, most);
+    at += v;
+  }
+  if (threadIdx.x == kThreads - 1) {
+    out[n] = (int32_t)min(inc, most);
+    part[0] = inc;
+  }
+  __syncthreads();
+  const long long total = part[0];
+  __syncthreads();
+  return total;
+}
+
+// Last i with a[i] <= v, for a[0] <= v and a ascending over [0, n).
+__device__ __forceinline__ int last_le(const int32_t *a, int n, int32_t v) {
+  int lo = 0, hi = n;             // a[lo] <= v < a[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= v) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Group of every request (-1: none).  Offsets that do not rise from 0 to B leave every request without one.
+__device__ __forceinline__ void fill_groups(int B, int G, const int32_t *offsets, int32_t *gid, int *dev_status) {
+  int bad = 0;
+  for (int g = threadIdx.x; g < G; g += kThreads) {
+    const int lo = offsets[g], hi = offsets[g + 1];
+    bad |= lo < 0 || lo > hi || hi > B || (g == 0 && lo != 0) || (g == G - 1 && hi != B);
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && threadIdx.x == 0) report(dev_status, MLA_ERR_BAD_INDEX);
+  if (bad || G == 0) {
+    for (int b = threadIdx.x; b < B; b += kThreads) gid[b] = -1;
+  } else {
+    for (int g = threadIdx.x >> 5; g < G; g += kWarps)
+      for (int b = offsets[g] + (threadIdx.x & 31); b < offsets[g + 1]; b += 32) gid[b] = g;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ int blocks_of(int tokens, int bs) { return tokens / bs + (tokens % bs != 0); }
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) step_plan_kernel(const StepPlanArgs a) {
+  extern __shared__ int32_t sm[];
+  __shared__ long long part[kWarps];
+  __shared__ int s_taken;
+  const int B = a.B, bs = a.block_size, tid = threadIdx.x;
+  int32_t *cu = sm;                    // [B + 1] first token of each request
+  int32_t *cum = cu + B + 1;           // [B + 1] first new block of each request
+  int32_t *held = cum + B + 1;         // [B] cached tokens; ~cached where the request is refused
+  int32_t *gid = held + B;             // [B] group; then, where the request joins its prefix, still the group, else -1
+  const int rank = (int)cluster_ctarank();
+  const int gtid = rank * kThreads + tid;
+  const int per = (B + kThreads - 1) / kThreads;
+
+  fill_groups(B, a.num_groups, a.group_offsets, gid, rank == 0 ? a.dev_status : nullptr);
+  int free = *a.free_count;
+  if (free < 0 || free > a.free_capacity) {
+    if (gtid == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+    free = free < 0 ? 0 : a.free_capacity;
+  }
+  // Lengths and refusals that do not depend on the other requests.
+  const int64_t room = min((int64_t)a.max_blocks_per_seq * bs, (int64_t)0x7fffffff);
+  for (int b = tid; b < B; b += kThreads) {
+    const int c = a.cached_lens[b], g = gid[b];
+    int n = a.new_lens[b];
+    const int P = g >= 0 ? a.prefix_lens[g] : 0;
+    bool bad = n < 0 || n > a.max_tokens;
+    if (bad) n = 0;
+    bad |= c < 0 || (int64_t)c + n > room || P < 0 || P % bs != 0 || P / bs > a.max_prefix_blocks || c < P;
+    cu[b] = n;
+    held[b] = bad ? ~max(c, 0) : c;
+    if (bad || P <= 0 || c != P) gid[b] = -1;
+    if (bad && rank == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+  }
+  __syncthreads();
+  // First tokens.  cum holds the token counts meanwhile.
+  for (int b = tid; b < B; b += kThreads) cum[b] = cu[b];
+  __syncthreads();
+  const long long tokens = scan_items(B, per, a.max_tokens, cu, part, [&](int b) { return (long long)cum[b]; });
+  // A request whose tokens do not all fit the token arrays is refused.
+  if (tokens > a.max_tokens) {
+    for (int b = tid; b < B; b += kThreads)
+      if (held[b] >= 0 && cum[b] > 0 && (long long)cu[b] + cum[b] > a.max_tokens) {
+        held[b] = ~held[b];
+        gid[b] = -1;
+        if (rank == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+      }
+    __syncthreads();
+  }
+  for (int b = tid; b < B; b += kThreads) {
+    const int n = cum[b];
+    cum[b] = held[b] >= 0 ? blocks_of(held[b] + n, bs) - blocks_of(held[b], bs) : 0;
+  }
+  __syncthreads();
+  // First new blocks, in place: every item is read by the thread that overwrites it, after its own reads.
+  {
+    const int lo = min(B, tid * per), hi = min(B, lo + per);
+    long long sum = 0;
+    for (int b = lo; b < hi; ++b) sum += cum[b];
+    const long long inc = block_scan(sum, part);
+    long long at = inc - sum;
+    int taken = 0;
+    for (int b = lo; b < hi; ++b) {
+      const int need = cum[b];
+      cum[b] = (int32_t)min(at, (long long)free);
+      at += need;
+      if (need > 0) {
+        if (at <= free) {
+          taken = (int)at;
+        } else {                   // the free list ends here: this request and every later one that needs a block
+          held[b] = ~held[b];
+          gid[b] = -1;
+          if (rank == 0) report(a.dev_status, MLA_ERR_NO_BLOCKS);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
+    if ((tid & 31) == 0) part[tid >> 5] = taken;
+    __syncthreads();
+    if (tid < 32) {
+      int t = (int)part[tid];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+      if (tid == 0) s_taken = t;
+    }
+    __syncthreads();
+  }
+  const int taken = s_taken;
+  // Every CTA has read the lengths and the free count.
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+
+  // New table entries.
+  for (int k0 = gtid * kPer; k0 < taken; k0 += kCtas * kThreads * kPer) {
+    int b = last_le(cum, B, k0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int k = k0 + i;
+      if (k >= taken) break;
+      while (b + 1 < B && cum[b + 1] <= k) ++b;
+      int id = a.free_list[free - 1 - k];
+      if (id < 0 || id >= a.num_blocks) {
+        report(a.dev_status, MLA_ERR_BAD_INDEX);
+        id = -1;
+      }
+      a.block_table[(int64_t)b * a.max_blocks_per_seq + blocks_of(held[b], bs) + (k - cum[b])] = id;
+    }
+  }
+  // The shared blocks of requests that join their group's prefix.
+  for (int b = gtid >> 5; b < B; b += kCtas * kWarps) {
+    const int g = gid[b];
+    if (g < 0) continue;
+    const int np = held[b] / bs;
+    const int32_t *src = a.prefix_table + (int64_t)g * a.max_prefix_blocks;
+    int32_t *dst = a.block_table + (int64_t)b * a.max_blocks_per_seq;
+    for (int i = tid & 31; i < np; i += 32) dst[i] = src[i];
+  }
+  // Tokens: request, position and pool row.
+  const int T = cu[B];
+  for (int t0 = gtid * kPer; t0 < T; t0 += kCtas * kThreads * kPer) {
+    int b = last_le(cu, B, t0);
+    int32_t sq[kPer], ps[kPer];
+    int64_t sl[kPer];
+    int at_b = -1, at_l = -1;
+    int32_t blk = -1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = t0 + i;
+      sq[i] = ps[i] = -1;
+      sl[i] = -1;
+      if (t < T) {
+        while (b + 1 < B && cu[b + 1] <= t) ++b;
+        const int c = held[b];
+        if (c >= 0) {
+          const int p = c + (t - cu[b]), l = p / bs, have = blocks_of(c, bs);
+          if (b != at_b || l != at_l) {
+            blk = l < have ? a.block_table[(int64_t)b * a.max_blocks_per_seq + l]
+                           : a.free_list[free - 1 - (cum[b] + l - have)];
+            if (blk < 0 || blk >= a.num_blocks) {
+              report(a.dev_status, MLA_ERR_BAD_INDEX);
+              blk = -1;
+            }
+            at_b = b;
+            at_l = l;
+          }
+          if (blk >= 0) {
+            sq[i] = b;
+            ps[i] = p;
+            sl[i] = (int64_t)blk * bs + p % bs;
+          }
+        }
+      }
+    }
+    if (a.vec && t0 + kPer <= T) {
+      *reinterpret_cast<int4 *>(a.seq_idx + t0) = make_int4(sq[0], sq[1], sq[2], sq[3]);
+      *reinterpret_cast<int4 *>(a.pos + t0) = make_int4(ps[0], ps[1], ps[2], ps[3]);
+      if (a.slots) {
+        *reinterpret_cast<longlong2 *>(a.slots + t0) = make_longlong2(sl[0], sl[1]);
+        *reinterpret_cast<longlong2 *>(a.slots + t0 + 2) = make_longlong2(sl[2], sl[3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (t0 + i < T) {
+          a.seq_idx[t0 + i] = sq[i];
+          a.pos[t0 + i] = ps[i];
+          if (a.slots) a.slots[t0 + i] = sl[i];
+        }
+    }
+  }
+  for (int b = gtid; b <= B; b += kCtas * kThreads) a.cu_seqlens[b] = cu[b];
+  // In-place outputs.  new = cu[b + 1] - cu[b] for a served request (refused ones keep what they held).
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int b = gtid; b < B; b += kCtas * kThreads) {
+    const int c = held[b];
+    a.seqlens[b] = c >= 0 ? c + (cu[b + 1] - cu[b]) : ~c;
+  }
+  if (gtid == 0) *a.free_count_out = free - taken;
+}
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) {
+  extern __shared__ int32_t sm[];
+  __shared__ long long part[kWarps];
+  __shared__ int s_put;
+  const int B = a.B, bs = a.block_size, tid = threadIdx.x;
+  int32_t *cum = sm;                   // [B + 1] first returned block of each request
+  int32_t *first = cum + B + 1;        // [B] first own table entry
+  int32_t *left = first + B;           // [B] length after the call
+  int32_t *gid = left + B;             // [B] group
+  const int rank = (int)cluster_ctarank();
+  const int gtid = rank * kThreads + tid;
+  const int per = (B + kThreads - 1) / kThreads;
+
+  fill_groups(B, a.num_groups, a.group_offsets, gid, rank == 0 ? a.dev_status : nullptr);
+  int free = *a.free_count;
+  if (free < 0 || free > a.free_capacity) {
+    if (gtid == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+    free = free < 0 ? 0 : a.free_capacity;
+  }
+  for (int b = tid; b < B; b += kThreads) {
+    const int n = a.seqlens[b], g = gid[b];
+    const int P = g >= 0 ? a.prefix_lens[g] : 0;
+    int own = 0;
+    left[b] = n;
+    first[b] = 0;
+    if (a.done[b]) {
+      if (n < 0 || P < 0 || P % bs != 0 || blocks_of(n, bs) > a.max_blocks_per_seq) {
+        if (rank == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+      } else {
+        own = max(0, blocks_of(n, bs) - P / bs);
+        first[b] = P / bs;
+        left[b] = 0;
+      }
+    }
+    cum[b] = own;
+  }
+  __syncthreads();
+  const long long most = a.free_capacity - free;
+  {
+    const int lo = min(B, tid * per), hi = min(B, lo + per);
+    long long sum = 0;
+    for (int b = lo; b < hi; ++b) sum += cum[b];
+    const long long inc = block_scan(sum, part);
+    long long at = inc - sum;
+    int put = 0;
+    for (int b = lo; b < hi; ++b) {
+      const int own = cum[b];
+      cum[b] = (int32_t)min(at, most);
+      at += own;
+      if (own > 0) {
+        if (at <= most) {
+          put = (int)at;
+        } else {                   // the list is full: this request and every later one keeps its blocks
+          left[b] = a.seqlens[b];
+          if (rank == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) put = max(put, __shfl_xor_sync(0xffffffffu, put, o));
+    if ((tid & 31) == 0) part[tid >> 5] = put;
+    __syncthreads();
+    if (tid < 32) {
+      int t = (int)part[tid];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+      if (tid == 0) s_put = t;
+    }
+    __syncthreads();
+  }
+  const int put = s_put;
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  for (int k0 = gtid * kPer; k0 < put; k0 += kCtas * kThreads * kPer) {
+    int b = last_le(cum, B, k0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int k = k0 + i;
+      if (k >= put) break;
+      while (b + 1 < B && cum[b + 1] <= k) ++b;
+      const int id = a.block_table[(int64_t)b * a.max_blocks_per_seq + first[b] + (k - cum[b])];
+      if (id < 0 || id >= a.num_blocks) report(a.dev_status, MLA_ERR_BAD_INDEX);
+      a.free_list[free + k] = id;
+    }
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int b = gtid; b < B; b += kCtas * kThreads) a.seqlens_out[b] = left[b];
+  if (gtid == 0) *a.free_count_out = free + put;
+}
+
+template <typename Args>
+int launch_cluster(void (*kernel)(Args), const Args &a, size_t smem, std::atomic<int> (&cache)[kSmemCacheDevs],
+                   cudaStream_t st) {
+  if (smem_limit(kernel, smem, cache) != cudaSuccess) return MLA_ERR_CUDA;
+  kernel<<<kCtas, kThreads, smem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_step_plan(const StepPlanArgs &a, cudaStream_t st) {
+  static std::atomic<int> cache[kSmemCacheDevs];
+  return launch_cluster(step_plan_kernel, a, (size_t)(4 * a.B + 2) * sizeof(int32_t), cache, st);
+}
+
+int launch_release(const ReleaseArgs &a, cudaStream_t st) {
+  static std::atomic<int> cache[kSmemCacheDevs];
+  return launch_cluster(release_kernel, a, (size_t)(4 * a.B + 1) * sizeof(int32_t), cache, st);
+}
+
+}  // namespace mla
