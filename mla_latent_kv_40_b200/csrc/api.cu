@@ -5,6 +5,7 @@
 
 #include "decode_tc.cuh"
 #include "kernels.cuh"
+#include "shared_tc.cuh"
 
 using namespace mla;
 
@@ -214,6 +215,42 @@ AbsorbedLayout absorbed_layout(const mla_dims *d, int d_cq, int B, int n_q, int 
   return L;
 }
 
+// Decode over shared prefixes (tensor-core shapes): the absorbed queries, the plan, and the partials of the sequences'
+// own keys followed by those of the shared ones.
+struct SharedLayout {
+  size_t q_off, head_off, cluster_off, units_off, segs_off, begin_off, seq_off, pages_off, info_off, o_off, lse_off, total;
+  int shared_segs;
+};
+
+SharedLayout shared_layout(const mla_dims *d, int B, int n_q, int num_groups) {
+  SharedLayout L{};
+  const int R = n_q * d->n_heads;
+  const int units = shared_max_units(B, R, num_groups);
+  const int C = shared_clusters_for_device();
+  const int clusters = C > 0 ? C : kSharedMaxClusters;
+  L.shared_segs = units + clusters;
+  const size_t rows = (size_t)tc_own_segments(*d, B, n_q) * 128 + (size_t)L.shared_segs * 256;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  L.q_off = take((size_t)B * R * (d->d_c + d->d_rope) * 2);
+  L.head_off = take(16);
+  L.cluster_off = take((size_t)clusters * sizeof(int));
+  L.units_off = take((size_t)units * sizeof(SharedUnit));
+  L.segs_off = take((size_t)units * sizeof(int2));
+  L.begin_off = take((size_t)B * sizeof(int));
+  L.seq_off = take((size_t)B * sizeof(int2));
+  L.pages_off = take((size_t)num_groups * sizeof(int));
+  L.info_off = take(tc_seg_info_bytes(*d, B, n_q));
+  L.o_off = take(rows * d->d_c * 2);
+  L.lse_off = take(rows * sizeof(float));
+  L.total = off;
+  return L;
+}
+
 // Sequence and position of each new token of a decode step: token t = b n_q + j sits at
 // seqlens[b] - n_q + j.
 __global__ void step_positions_kernel(int B, int n_q, const int32_t *seqlens, int32_t *seq_idx, int32_t *pos) {
@@ -387,7 +424,9 @@ int mla_decode_shared_workspace_size(const mla_dims *dims, int B, int n_q, int m
   if (!dims_ok(dims) || B <= 0 || n_q <= 0 || max_seqlen < n_q || num_groups < 0 || num_groups > B || !bytes)
     return MLA_ERR_INVALID_ARG;
   if (n_q * dims->n_heads > 256) return MLA_ERR_UNSUPPORTED;
-  *bytes = decode_layout(dims, B, n_q, max_seqlen).total;
+  const size_t alone = decode_layout(dims, B, n_q, max_seqlen).total;
+  const size_t shared = num_groups > 0 && tc_decode_supported(*dims, n_q) ? shared_layout(dims, B, n_q, num_groups).total : 0;
+  *bytes = shared > alone ? shared : alone;
   return MLA_OK;
 }
 
@@ -396,11 +435,47 @@ int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *q_nope, 
                       const int32_t *seqlens, int max_seqlen, int num_groups, const int32_t *group_offsets,
                       const int32_t *prefix_lens, const void *w_uk, const void *w_uv, void *out, float *lse,
                       void *workspace, size_t ws_bytes, int *dev_status, mla_stream_t stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int rc = check_decode_args(dims, B, n_q, c_kv, k_pe, max_blocks_per_seq, num_blocks, seqlens, max_seqlen);
+  if (rc) return rc;
   if (num_groups < 0 || num_groups > B || !block_table || (num_groups > 0 && (!group_offsets || !prefix_lens)))
     return MLA_ERR_INVALID_ARG;
-  return decode_impl(dims, B, n_q, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,
-                     max_seqlen, w_uk, w_uv, out, lse, workspace, ws_bytes, dev_status,
-                     reinterpret_cast<cudaStream_t>(stream));
+  // Nothing to share, or a shape that the tensor cores do not take: every sequence by itself.
+  if (num_groups == 0 || !tc_decode_supported(*dims, n_q))
+    return decode_impl(dims, B, n_q, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,
+                       max_seqlen, w_uk, w_uv, out, lse, workspace, ws_bytes, dev_status, st);
+  if (!q_nope || (!q_pe && dims->d_rope) || !w_uk || !out) return MLA_ERR_INVALID_ARG;
+  const SharedLayout L = shared_layout(dims, B, n_q, num_groups);
+  if (!workspace || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MLA_ERR_WORKSPACE;
+  const bool tiled = dims->cache_layout == MLA_CACHE_TILED;
+  if ((reinterpret_cast<uintptr_t>(c_kv) & 15) || (!tiled && (reinterpret_cast<uintptr_t>(k_pe) & 15)))
+    return MLA_ERR_INVALID_ARG;
+  char *ws = static_cast<char *>(workspace);
+  void *qbuf = ws + L.q_off;
+  const int own_segs = tc_own_segments(*dims, B, n_q);
+  const SharedPlan pl{reinterpret_cast<int *>(ws + L.head_off), reinterpret_cast<int *>(ws + L.cluster_off),
+                      reinterpret_cast<SharedUnit *>(ws + L.units_off), reinterpret_cast<int2 *>(ws + L.segs_off),
+                      reinterpret_cast<int *>(ws + L.begin_off), reinterpret_cast<int2 *>(ws + L.seq_off),
+                      reinterpret_cast<int *>(ws + L.pages_off)};
+  const TcBuffers buf{reinterpret_cast<int *>(ws + L.info_off), reinterpret_cast<__nv_bfloat16 *>(ws + L.o_off),
+                      reinterpret_cast<float *>(ws + L.lse_off)};
+  const CacheView cv{c_kv, k_pe, dims->ckv_stride, dims->kpe_stride, block_table, max_blocks_per_seq, num_blocks,
+                     dims->block_size, dims->cache_layout, dims->d_c, dims->d_c + dims->d_rope};
+  // (1) Who shares what, (2) the latent queries, (3) the shared keys for all rows of a group, (4) every sequence's
+  // own keys, (5) the merge and W_UV.
+  if ((rc = launch_shared_plan(pl, B, n_q, dims->n_heads, max_seqlen, dims->block_size, num_groups, group_offsets, prefix_lens,
+                               seqlens, dev_status, st)))
+    return rc;
+  const AbsorbArgs ab{B, n_q, dims->n_heads, dims->d_c, dims->d_rope, dims->d_nope,
+                      q_nope, q_pe, w_uk, seqlens, qbuf, dims->rope_base};
+  if ((rc = absorb_dispatch(ab, true, dev_status, st))) return rc;
+  if ((rc = launch_shared_attention(*dims, pl, qbuf, cv, buf.o_part + (size_t)own_segs * 128 * dims->d_c,
+                                    buf.lse_part + (size_t)own_segs * 128, dev_status, st)))
+    return rc;
+  if ((rc = launch_tc_attention_own(*dims, B, n_q, qbuf, cv, seqlens, max_seqlen, pl.own_begin, buf, dev_status, st)))
+    return rc;
+  return launch_tc_combine_shared(*dims, B, n_q, buf, pl.seq_unit, pl.unit_segs, L.shared_segs, w_uv, out, lse, dev_status,
+                                  st);
 }
 
 // What the two bookkeeping calls check alike.

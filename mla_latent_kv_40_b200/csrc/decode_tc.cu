@@ -163,6 +163,15 @@ struct TcParams {
   const unsigned char *tiled;        // tiled page pool (pages move by bulk copy), or NULL: row pool via TMA maps
   const unsigned char *row_pool;     // row pool base (c_kv) for L2 prefetch
   int rows_contig;                   // row pool with fused 576-wide rows: a page is 73728 contiguous bytes
+  static constexpr bool kOwn = false;
+  __device__ __forceinline__ int begin(int) const { return kv_begin; }
+};
+
+// Every sequence begins at its own key (a multiple of 64): the keys before it are attended to elsewhere.
+struct TcOwnParams : TcParams {
+  const int *own_begin;              // [B], written by an earlier kernel on the stream
+  static constexpr bool kOwn = true;
+  __device__ __forceinline__ int begin(int b) const { return own_begin[b]; }
 };
 
 __device__ __forceinline__ int seq_len_clamped(const TcParams &p, int b) {
@@ -176,9 +185,10 @@ __device__ __forceinline__ int key_end(const TcParams &p, int b) {
   return S < p.kv_end ? S : p.kv_end;
 }
 
-// Tiles (64-key pages) of a unit inside the key range; tile t holds keys kv_begin + 64 t ...
-__device__ __forceinline__ int unit_tiles(const TcParams &p, int u) {
-  const int e = key_end(p, u / p.n_rb) - p.kv_begin;
+// Tiles (64-key pages) of a unit inside the key range; tile t holds keys begin + 64 t ...
+template <typename P>
+__device__ __forceinline__ int unit_tiles(const P &p, int u) {
+  const int e = key_end(p, u / p.n_rb) - p.begin(u / p.n_rb);
   return e > 0 ? (e + kTileKeys - 1) / kTileKeys : 0;
 }
 
@@ -203,7 +213,8 @@ __device__ __forceinline__ int cluster_of(long long t, int k, const Split &sp) {
 
 // Warp-level plan: total tiles and cost, this cluster's tile range, its first unit and the tile,
 // non-empty-unit and segment prefixes of that unit.  Every CTA computes the same values.
-__device__ __forceinline__ void make_plan(const TcParams &p, SmemB &sb, int cid, int C) {
+template <typename P>
+__device__ __forceinline__ void make_plan(const P &p, SmemB &sb, int cid, int C) {
   const int lane = threadIdx.x & 31;
   long long total = 0;
   int une = 0;
@@ -308,7 +319,8 @@ struct SegIter {
   int u, prefix, seg_prefix, k;   // k: non-empty units before u
   long long pos, end;
   Split sp;
-  __device__ __forceinline__ bool next(const TcParams &p, int cid, int &b, int &rb, int &t0, int &t1, int &segid, bool &first_of_unit,
+  template <typename P>
+  __device__ __forceinline__ bool next(const P &p, int cid, int &b, int &rb, int &t0, int &t1, int &segid, bool &first_of_unit,
                        int &nseg_unit) {
     while (pos < end && u < p.U) {
       const int nt = unit_tiles(p, u);
@@ -387,8 +399,9 @@ __device__ __forceinline__ bool warp_wait(SmemB &sb, uint32_t bar, uint32_t pari
   return ok != 0;
 }
 
-__device__ __forceinline__ int64_t tile_row(const TcParams &p, int b, int t) {
-  const int key = p.kv_begin + t * kTileKeys;
+template <typename P>
+__device__ __forceinline__ int64_t tile_row(const P &p, int b, int t) {
+  const int key = p.begin(b) + t * kTileKeys;
   const int lb = key / p.block_size;
   if (lb >= p.max_blocks_per_seq) return -1;
   const int blk = p.block_table ? p.block_table[(int64_t)b * p.max_blocks_per_seq + lb]
@@ -403,12 +416,14 @@ __device__ __forceinline__ int64_t tile_row(const TcParams &p, int b, int t) {
 struct PageRows {
   int b = -1, base = 0;
   int64_t r0 = -1, r1 = -1;
-  __device__ __forceinline__ void load(const TcParams &p) {
+  template <typename P>
+  __device__ __forceinline__ void load(const P &p) {
     const int lane = threadIdx.x & 31;
     r0 = tile_row(p, b, base + lane);
     r1 = tile_row(p, b, base + 32 + lane);
   }
-  __device__ __forceinline__ int64_t get(const TcParams &p, int seq, int page) {
+  template <typename P>
+  __device__ __forceinline__ int64_t get(const P &p, int seq, int page) {
     if (seq != b || page < base || page >= base + 96) {
       b = seq;
       base = page;
@@ -423,9 +438,10 @@ struct PageRows {
   }
 };
 
+template <typename P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_pe,
-                     const __grid_constant__ TcParams p) {
+                     const __grid_constant__ P p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   SmemB &sb = *reinterpret_cast<SmemB *>(tiles + kRegionA);
@@ -463,6 +479,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
     tmem_alloc(smem_u32(&sb.tmem_base), 512);
     tmem_relinquish();
   }
+  if (P::kOwn) grid_dep_wait();   // the plan needs own_begin
   if (warp == 0) make_plan(p, sb, cid, C);
   if (threadIdx.x == 32 && !p.tiled) {
     tma_prefetch_desc(&map_c);
@@ -664,7 +681,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
       bool ok = true;
       while (ok && it.next(p, cid, b, rb, t0, t1, segid, first_u, nseg)) {
         if (uc > 0 && !wait_or_abort(sb, bar(B_OFREE), (uc - 1) & 1, p.dev_status, false, p.timeout_rec, __LINE__)) break;
-        const int S = seq_len_clamped(p, b);
+        const int S = seq_len_clamped(p, b), kb = p.begin(b);
         for (int t = t0; t < t1; ++t, n += 2, ++np) {
           sb.prog[warp] = (int)n;
           const int pb = np % kPSlots;
@@ -674,7 +691,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
             ok = false;
             break;
           }
-          const bool tail = p.kv_begin + (t + 1) * kTileKeys > S;
+          const bool tail = kb + (t + 1) * kTileKeys > S;
           const uint32_t fa = slot_factors(smem_u32(tiles), pb);
           const bool resc = t != t0 && (ld_shared_u32(fa + 4 * 32) | ld_shared_u32(fa + 4 * (kPaWords + 32)) |
                                         ld_shared_u32(fa + 4 * (2 * kPaWords + 32)) |
@@ -689,7 +706,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
             // halves: the slot's P.V barrier counts both issuers) must have completed.
             if (resc && !wait_or_abort(sb, bar(B_PVDONE + (np - 1) % kPSlots), ((np - 1) / kPSlots) & 1, p.dev_status,
                                        false, p.timeout_rec, __LINE__)) { ok = false; break; }
-            sb.req[hv] = Req{0, sv, pb, S - p.kv_begin - t * kTileKeys, tail ? 1 : 0, resc ? 1 : 0, 0, 0, 0};
+            sb.req[hv] = Req{0, sv, pb, S - kb - t * kTileKeys, tail ? 1 : 0, resc ? 1 : 0, 0, 0, 0};
             mbar_arrive(bar(B_REQ + hv));
             if (!wait_or_abort(sb, bar(B_REQDONE + hv), nfix & 1, p.dev_status, false, p.timeout_rec, __LINE__)) { ok = false; break; }
             ++nfix;
@@ -822,7 +839,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
         const int S = seq_len_clamped(p, b);
         const int j = real ? gr / p.H : 0;
         // Keys this row may see, counted from the key range's first key.
-        const int vis_end = (real ? min(S - p.n_q + j + 1, p.kv_end) : 0) - p.kv_begin;
+        const int vis_end = (real ? min(S - p.n_q + j + 1, p.kv_end) : 0) - p.begin(b);
         float m_ref = -CUDART_INF_F, l = 0.f;
         for (int T = t0; T < t1; T += kSuper, ++ns) {
           if (lane == 0) sb.prog[warp] = (int)np;
@@ -1050,7 +1067,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
 
 // ------------------------------------------------------------ merge of the split partials
 // One warp merges the ns pieces of one (query row, head) by their log-sum-exps: piece k is the bf16
-// row part[k * part_stride][0 .. 512) with log-sum-exp lse[k * lse_stride].  It writes the merged
+// row part[row(k)][0 .. 512) with log-sum-exp lse[row(k)].  It writes the merged
 // row (bf16) and, if lse_dst is non-null, the log of the summed exp (-inf, with a zero row, where no
 // piece saw a key).  Each lane owns 16 latent columns (8 in each half of the row), and the loads of
 // up to kMergeUnroll pieces are in flight together, so a row cut into a few pieces costs one round
@@ -1059,16 +1076,16 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeUnroll = 4;
 constexpr int kMaxSegPerUnit = kMaxClusters + 1;
 
-__device__ __forceinline__ void merge_row(int lane, int ns, const __nv_bfloat16 *part, int64_t part_stride,
-                                          const float *lse, int64_t lse_stride, __nv_bfloat16 *dst,
-                                          float *lse_dst) {
+template <typename Row>
+__device__ __forceinline__ void merge_row(int lane, int ns, const __nv_bfloat16 *part, const float *lse, Row row,
+                                          __nv_bfloat16 *dst, float *lse_dst) {
   float m = -CUDART_INF_F;
-  for (int k = lane; k < ns; k += 32) m = fmaxf(m, lse[(int64_t)k * lse_stride]);
+  for (int k = lane; k < ns; k += 32) m = fmaxf(m, lse[row(k)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float sum = 0.f;
   if (m != -CUDART_INF_F)
-    for (int k = lane; k < ns; k += 32) sum += __expf(lse[(int64_t)k * lse_stride] - m);
+    for (int k = lane; k < ns; k += 32) sum += __expf(lse[row(k)] - m);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -1082,10 +1099,10 @@ __device__ __forceinline__ void merge_row(int lane, int ns, const __nv_bfloat16 
     for (int i = 0; i < kMergeUnroll; ++i) {
       const int k = k0 + i;
       const bool have = k < ns;
-      const __nv_bfloat16 *src = part + (int64_t)(have ? k : 0) * part_stride + 8 * lane;
+      const __nv_bfloat16 *src = part + row(have ? k : 0) * kDc + 8 * lane;
       x[i][0] = have ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
       x[i][1] = have ? *reinterpret_cast<const uint4 *>(src + 256) : make_uint4(0, 0, 0, 0);
-      wk[i] = have && m != -CUDART_INF_F ? __expf(lse[(int64_t)k * lse_stride] - m) * inv : 0.f;
+      wk[i] = have && m != -CUDART_INF_F ? __expf(lse[row(k)] - m) * inv : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < kMergeUnroll; ++i)
@@ -1132,8 +1149,8 @@ tc_merge_kernel(int B, int n_q, int H, int n_rb, int max_segs, const int *seg_in
     s0 = 0;
     ns = 0;
   }
-  merge_row(lane, ns, o_part + ((int64_t)s0 * kRows + lr) * kDc, (int64_t)kRows * kDc,
-            lse_part + (int64_t)s0 * kRows + lr, kRows, o_lat + item * kDc, lse_out ? lse_out + item : nullptr);
+  merge_row(lane, ns, o_part, lse_part, [&](int k) { return (int64_t)(s0 + k) * kRows + lr; }, o_lat + item * kDc,
+            lse_out ? lse_out + item : nullptr);
 }
 
 // One warp per row r = ((b, j), s) of n_parts stacked partials (one per key range, e.g. gathered
@@ -1147,7 +1164,7 @@ parts_merge_kernel(int64_t rows, int n_parts, const __nv_bfloat16 *o_parts, cons
   const int lane = threadIdx.x & 31;
   const int64_t r = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
   if (r >= rows) return;
-  merge_row(lane, n_parts, o_parts + r * kDc, rows * kDc, lse_parts + r, rows, o_lat + r * kDc,
+  merge_row(lane, n_parts, o_parts, lse_parts, [&](int k) { return k * rows + r; }, o_lat + r * kDc,
             lse_out ? lse_out + r : nullptr);
 }
 
@@ -1160,24 +1177,74 @@ struct Pieces {
   const float *lse;            // one log-sum-exp per row of `part`
   const int *seg_info;         // [units][2], or NULL for stacked partials
   int n_q, H, n_rb, max_segs, n_parts;
+  static constexpr bool kShared = false;
 };
 
-// Number of pieces of row (g, s) and the index of its first piece row; pieces are `stride` rows apart.
-__device__ __forceinline__ int piece_rows(const Pieces &pc, int rows, int g, int s, int64_t &first, int64_t &stride) {
+// With the pieces of a shared prefix behind those of the sequence's own keys: the group's rows are cut into units of
+// 256, unit u's pieces are the segments unit_segs[u] = (first, count) of 256 rows each, from row `shared_row` on.
+struct SharedPieces : Pieces {
+  const int2 *seq_unit;        // [B]: first unit of the sequence's group (-1: none), the group's first query row
+  const int2 *unit_segs;
+  int64_t shared_row;
+  int max_shared_segs;
+  static constexpr bool kShared = true;
+};
+constexpr int kSharedRows = 256;
+
+// The pieces of one output row: `own` rows from `first` on, `stride` apart, then rows from `first2` on, 256 apart.
+struct PieceRows {
+  int ns = 0, own = 0;
+  int64_t first = 0, stride = 0, first2 = 0;
+  template <bool kShared>
+  __device__ __forceinline__ int64_t at(int k) const {
+    if (kShared && k >= own) return first2 + (int64_t)(k - own) * kSharedRows;
+    return first + k * stride;
+  }
+};
+
+template <typename P>
+__device__ __forceinline__ PieceRows piece_rows(const P &pc, int rows, int g, int s) {
+  PieceRows r;
   if (!pc.seg_info) {
-    first = (int64_t)g * pc.H + s;
-    stride = (int64_t)rows * pc.H;
-    return pc.n_parts;
+    r.first = (int64_t)g * pc.H + s;
+    r.stride = (int64_t)rows * pc.H;
+    r.ns = r.own = pc.n_parts;
+    return r;
   }
   const int b = g / pc.n_q, j = g % pc.n_q;
   const int gr = j * pc.H + s;
   const int u = b * pc.n_rb + gr / kRows;
   int s0 = pc.seg_info[2 * u], ns = pc.seg_info[2 * u + 1];
   ns = ns < 0 ? 0 : (ns > kMaxSegPerUnit ? kMaxSegPerUnit : ns);
-  if (s0 < 0 || s0 + ns > pc.max_segs) return 0;
-  first = (int64_t)s0 * kRows + gr % kRows;
-  stride = kRows;
-  return ns;
+  if (s0 >= 0 && s0 + ns <= pc.max_segs) {
+    r.first = (int64_t)s0 * kRows + gr % kRows;
+    r.stride = kRows;
+    r.ns = r.own = ns;
+  }
+  if constexpr (P::kShared) {
+    const int2 su = pc.seq_unit[b];
+    if (su.x >= 0) {
+      const int q = g * pc.H + s - su.y;   // row within the group
+      const int2 sg = pc.unit_segs[su.x + q / kSharedRows];
+      if (sg.x >= 0 && sg.y > 0 && sg.x + sg.y <= pc.max_shared_segs) {
+        r.first2 = pc.shared_row + (int64_t)sg.x * kSharedRows + q % kSharedRows;
+        r.ns += sg.y;
+      }
+    }
+  }
+  return r;
+}
+
+// As tc_merge_kernel, with the pieces of a shared prefix.
+__global__ void __launch_bounds__(kMergeThreads)
+shared_merge_kernel(const SharedPieces pc, int rows, __nv_bfloat16 *o_lat, float *lse_out) {
+  sm100::grid_dep_launch();
+  sm100::grid_dep_wait();
+  const int64_t item = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  if (item >= (int64_t)rows * pc.H) return;
+  const PieceRows pr = piece_rows(pc, rows, (int)(item / pc.H), (int)(item % pc.H));
+  merge_row(threadIdx.x & 31, pr.ns, pc.part, pc.lse, [&](int k) { return pr.at<true>(k); }, o_lat + item * kDc,
+            lse_out ? lse_out + item : nullptr);
 }
 
 // CTA = (head s, 64 query rows (b, j)): the rows' pieces are merged by their log-sum-exps straight
@@ -1195,8 +1262,9 @@ constexpr uint32_t kOlBytes = kCombRows * kDc * 2;         // o_lat: [8 K-chunks
 constexpr uint32_t kWuvBytes = kDc * kDv * 2;              // W_UV^T: [8 K-chunks][2 M-chunks][64 K rows][128 B]
 static_assert(kCombThreads == 4 * kCombRows, "four merging threads per row");
 
+template <typename P>
 __global__ void __launch_bounds__(kCombThreads)
-tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const Pieces pc, int rows, float *lse_out,
+tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int rows, float *lse_out,
                   __nv_bfloat16 *out, int *dev_status) {
   extern __shared__ unsigned char csm_raw[];
   unsigned char *csm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(csm_raw) + 1023) & ~uintptr_t(1023));
@@ -1229,13 +1297,13 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const Pieces pc, in
   {
     // Merge of row rr (output row g = g0 + rr); rows past the end become zero rows of the tile.
     const int rr = tid >> 2, q = tid & 3, g = g0 + rr;
-    int64_t first = 0, stride = 0;
-    const int ns = g < rows ? piece_rows(pc, rows, g, s, first, stride) : 0;
+    const PieceRows pr = g < rows ? piece_rows(pc, rows, g, s) : PieceRows();
+    const int ns = pr.ns;
     float m = -CUDART_INF_F;
-    for (int k = 0; k < ns; ++k) m = fmaxf(m, pc.lse[first + k * stride]);
+    for (int k = 0; k < ns; ++k) m = fmaxf(m, pc.lse[pr.at<P::kShared>(k)]);
     float sum = 0.f;
     if (m != -CUDART_INF_F)
-      for (int k = 0; k < ns; ++k) sum += __expf(pc.lse[first + k * stride] - m);
+      for (int k = 0; k < ns; ++k) sum += __expf(pc.lse[pr.at<P::kShared>(k)] - m);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
     for (int hh = 0; hh < 2; ++hh) {
@@ -1251,11 +1319,12 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const Pieces pc, in
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
           const bool have = k0 + kk < ns;
-          const __nv_bfloat16 *src = pc.part + (first + (int64_t)(have ? k0 + kk : 0) * stride) * kDc;
+          const int64_t prow = pr.at<P::kShared>(have ? k0 + kk : 0);
+          const __nv_bfloat16 *src = pc.part + prow * kDc;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             x[kk][i] = have ? *reinterpret_cast<const uint4 *>(src + 8 * (4 * (8 * hh + i) + q)) : make_uint4(0, 0, 0, 0);
-          wk[kk] = have && m != -CUDART_INF_F ? __expf(pc.lse[first + (int64_t)(k0 + kk) * stride] - m) * inv : 0.f;
+          wk[kk] = have && m != -CUDART_INF_F ? __expf(pc.lse[prow] - m) * inv : 0.f;
         }
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
@@ -1408,11 +1477,13 @@ int clusters_for_device() {
   if (const int c = cached[dev].load(std::memory_order_acquire)) return c;
   std::lock_guard<std::mutex> lock(mu);
   if (const int c = cached[dev].load(std::memory_order_acquire)) return c;
-  if (cudaFuncSetAttribute(mla_decode_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes))
+  const auto kernel = mla_decode_tc_kernel<TcParams>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) ||
+      cudaFuncSetAttribute(mla_decode_tc_kernel<TcOwnParams>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes))
     return 0;
   // One CTA of kThreads per SM needs at most kLaunchRegs registers per thread.
   cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, mla_decode_tc_kernel) != cudaSuccess || fa.numRegs > kLaunchRegs) return 0;
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs > kLaunchRegs) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * kMaxClusters);
   cfg.blockDim = dim3(kThreads);
@@ -1425,7 +1496,7 @@ int clusters_for_device() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, mla_decode_tc_kernel, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     int sms = 0;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1451,17 +1522,18 @@ size_t tc_decode_workspace_bytes(const mla_dims &d, int B, int n_q) {
   return ws_layout(B, n_rb).total;
 }
 
-int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
-                        const int32_t *seqlens, int max_seqlen, void *ws, int *dev_status, cudaStream_t st,
-                        int kv_begin, int kv_end) {
+namespace {
+
+// The attention over [begin, kv_end) of every sequence: begin = kv_begin, or own_begin[b] when given.
+int launch_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
+                     const int32_t *seqlens, int max_seqlen, const TcBuffers &buf, int *dev_status, cudaStream_t st,
+                     int kv_begin, int kv_end, const int *own_begin) {
   if (kv_begin < 0 || kv_begin % kTileKeys) return MLA_ERR_INVALID_ARG;
   const bool tiled = cache.layout == MLA_CACHE_TILED;
   if ((reinterpret_cast<uintptr_t>(cache.c_kv) & 15) || (!tiled && (reinterpret_cast<uintptr_t>(cache.k_pe) & 15)) ||
       (reinterpret_cast<uintptr_t>(q_abs) & 15))
     return MLA_ERR_INVALID_ARG;
   const int n_rb = (n_q * d.n_heads + kRows - 1) / kRows;
-  const WsLayout L = ws_layout(B, n_rb);
-  char *w = static_cast<char *>(ws);
   CUtensorMap mc, mpe;
   memset(&mc, 0, sizeof(mc));
   memset(&mpe, 0, sizeof(mpe));
@@ -1473,7 +1545,7 @@ int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, co
   }
   const int C = clusters_for_device();
   if (C <= 0) return MLA_ERR_CUDA;
-  TcParams p;
+  TcOwnParams p;
   p.B = B;
   p.n_q = n_q;
   p.H = d.n_heads;
@@ -1491,13 +1563,14 @@ int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, co
   p.row_pool = static_cast<const unsigned char *>(cache.c_kv);
   p.rows_contig = !tiled && cache.ckv_stride == kW && cache.kpe_stride == kW &&
                   static_cast<const char *>(cache.k_pe) == static_cast<const char *>(cache.c_kv) + 2 * kDc;
-  p.o_part = reinterpret_cast<__nv_bfloat16 *>(w + L.o_part);
-  p.lse_part = reinterpret_cast<float *>(w + L.lse_part);
-  p.seg_info = reinterpret_cast<int *>(w + L.seg_info);
+  p.o_part = buf.o_part;
+  p.lse_part = buf.lse_part;
+  p.seg_info = buf.seg_info;
   p.timeout_rec = p.seg_info + 2 * p.U;
   p.dev_status = dev_status;
   p.kv_begin = kv_begin;
   p.kv_end = kv_end;
+  p.own_begin = own_begin;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * C);
   cfg.blockDim = dim3(kThreads);
@@ -1508,15 +1581,45 @@ int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, co
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, mla_decode_tc_kernel, mc, mpe, p) != cudaSuccess) return MLA_ERR_CUDA;
-  return MLA_OK;
+  const cudaError_t e = own_begin ? cudaLaunchKernelEx(&cfg, mla_decode_tc_kernel<TcOwnParams>, mc, mpe, p)
+                                  : cudaLaunchKernelEx(&cfg, mla_decode_tc_kernel<TcParams>, mc, mpe,
+                                                       static_cast<const TcParams &>(p));
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
+                        const int32_t *seqlens, int max_seqlen, void *ws, int *dev_status, cudaStream_t st,
+                        int kv_begin, int kv_end) {
+  const WsLayout L = ws_layout(B, (n_q * d.n_heads + kRows - 1) / kRows);
+  char *w = static_cast<char *>(ws);
+  const TcBuffers buf{reinterpret_cast<int *>(w + L.seg_info), reinterpret_cast<__nv_bfloat16 *>(w + L.o_part),
+                      reinterpret_cast<float *>(w + L.lse_part)};
+  return launch_attention(d, B, n_q, q_abs, cache, seqlens, max_seqlen, buf, dev_status, st, kv_begin, kv_end, nullptr);
+}
+
+int tc_own_segments(const mla_dims &d, int B, int n_q) {
+  const int C = clusters_for_device();
+  return B * ((n_q * d.n_heads + kRows - 1) / kRows) + (C > 0 ? C : kMaxClusters);
+}
+
+size_t tc_seg_info_bytes(const mla_dims &d, int B, int n_q) {
+  return ((size_t)B * ((n_q * d.n_heads + kRows - 1) / kRows) * 2 + kTimeoutRecInts) * sizeof(int);
+}
+
+int launch_tc_attention_own(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
+                            const int32_t *seqlens, int max_seqlen, const int *own_begin, const TcBuffers &buf,
+                            int *dev_status, cudaStream_t st) {
+  return launch_attention(d, B, n_q, q_abs, cache, seqlens, max_seqlen, buf, dev_status, st, 0, 0x7fffffff, own_begin);
 }
 
 namespace {
 
 // out [rows][H][128] = (pieces of each row, merged) . W_UV^(s) per head s, on the tensor cores;
 // lse (if non-null) gets the merged log-sum-exps.
-int launch_merge_wuv(const mla_dims &d, int rows, const Pieces &pc, const void *w_uv, void *out, float *lse,
+template <typename P>
+int launch_merge_wuv(const mla_dims &d, int rows, const P &pc, const void *w_uv, void *out, float *lse,
                      int *dev_status, cudaStream_t st) {
   // W_UV as [H * 512 rows][128] (boxes of 64 rows x 64 columns).
   CUtensorMap mw;
@@ -1524,10 +1627,10 @@ int launch_merge_wuv(const mla_dims &d, int rows, const Pieces &pc, const void *
   if (rc) return rc;
   const size_t smem = 1024 + kOlBytes + kWuvBytes;
   static std::atomic<int> smem_set[kSmemCacheDevs];
-  if (smem_limit(tc_combine_kernel, smem, smem_set) != cudaSuccess)
+  if (smem_limit(tc_combine_kernel<P>, smem, smem_set) != cudaSuccess)
     return MLA_ERR_CUDA;
   const dim3 grid(d.n_heads, (rows + kCombRows - 1) / kCombRows);
-  return launch_pdl(tc_combine_kernel, grid, dim3(kCombThreads), smem, st, mw, pc, rows, lse,
+  return launch_pdl(tc_combine_kernel<P>, grid, dim3(kCombThreads), smem, st, mw, pc, rows, lse,
                     static_cast<__nv_bfloat16 *>(out), dev_status) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
@@ -1556,6 +1659,27 @@ int launch_tc_combine(const mla_dims &d, int B, int n_q, const int32_t *seqlens,
   return launch_pdl(tc_merge_kernel, mgrid, dim3(kMergeThreads), 0, st, B, n_q, d.n_heads, n_rb, max_segs,
                     reinterpret_cast<const int *>(w + L.seg_info), reinterpret_cast<const __nv_bfloat16 *>(w + L.o_part),
                     reinterpret_cast<const float *>(w + L.lse_part), static_cast<__nv_bfloat16 *>(out), lse) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+int launch_tc_combine_shared(const mla_dims &d, int B, int n_q, const TcBuffers &buf, const int2 *seq_unit,
+                             const int2 *unit_segs, int max_shared_segs, const void *w_uv, void *out, float *lse,
+                             int *dev_status, cudaStream_t st) {
+  if (w_uv && (d.d_v != kDv || (reinterpret_cast<uintptr_t>(w_uv) & 15))) return MLA_ERR_UNSUPPORTED;
+  const int rows = B * n_q, max_segs = tc_own_segments(d, B, n_q);
+  SharedPieces pc;
+  static_cast<Pieces &>(pc) = Pieces{buf.o_part, buf.lse_part, buf.seg_info, n_q, d.n_heads,
+                                     (n_q * d.n_heads + kRows - 1) / kRows, max_segs, 0};
+  pc.seq_unit = seq_unit;
+  pc.unit_segs = unit_segs;
+  pc.shared_row = (int64_t)max_segs * kRows;
+  pc.max_shared_segs = max_shared_segs;
+  if (w_uv) return launch_merge_wuv(d, rows, pc, w_uv, out, lse, dev_status, st);
+  const int64_t warps = (int64_t)rows * d.n_heads;
+  const dim3 mgrid((unsigned)((warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32)));
+  return launch_pdl(shared_merge_kernel, mgrid, dim3(kMergeThreads), 0, st, pc, rows, static_cast<__nv_bfloat16 *>(out),
+                    lse) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }

@@ -1,0 +1,925 @@
+// Attention of a group's query rows over the keys that its sequences share, on tcgen05 (sm_100a).
+//
+// In the absorbed form every head of every sequence attends to the same cached rows [c_i | kpe_i], so over a shared
+// prefix the rows of all sequences of a group are rows of one product,
+//   S = Q [rows x 576] . K^T [576 x keys],   O += P [rows x keys] . C [keys x 512],
+// with no mask (the shared keys end before every query).  2176 FLOPs per (row, key) against 1152 bytes per key and
+// 256 rows: bound by the tensor cores.
+//
+// Shape.  A unit is 256 rows.  A cluster of four CTAs works on one unit at a time, as two pairs that issue M = 256
+// MMAs (cta_group::2: each CTA holds 128 of the rows and half of the B operand, so each SM pulls half the bytes that
+// a 128-row tile of its own would need; at 128 rows the L2 -> SM path, not the tensor pipe, sets the pace):
+//   * ranks 0, 1 (score pair): Q_lat of the CTA's 128 rows in tensor memory (A operand), Q_rope in shared memory; a
+//     tile is 128 keys, and CTA r streams its page r (64 keys, contiguous in the tiled pool) as two half-page stages;
+//     rank 0 issues S [256 x 128] into one of two tensor-memory buffers; eight warps per CTA run the online softmax
+//     of its 128 rows and send each page of P (bf16) to the value CTA of the same rows by one shared-to-shared copy;
+//   * ranks 2, 3 (value pair): O of the CTA's 128 rows in all 512 tensor-memory columns; CTA r streams the latent
+//     dims 256 (r - 2) .. of every page (32 KB, contiguous); rank 2 issues O += P . C as two N = 256 MMAs per 16 keys.
+// Per 128 keys the score pair has 36 MMAs of 64 cycles, the value pair 16 of 128: 2304 and 2048 cycles.
+//
+// The issuing warps run whole, and each MMA is issued by the elected lane: with warp-uniform descriptors the issue
+// keeps up with the pipe from one warp.  Reference maximum, row sums, rounding of P and of the partials as in the
+// per-sequence kernel (decode_tc.cu): lazy maximum in log2 units, sums of P in fp32 before its rounding, O / l in
+// bf16 per segment.  The (unit, tile) list is cut into equal runs, one per cluster; a unit cut between clusters
+// leaves one partial per piece, merged with the sequences' own partials by the combine.
+// Every wait is bounded; on expiry the kernel reports MLA_ERR_TIMEOUT, drains its copies, frees its tensor memory
+// and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math_constants.h>
+
+#include <atomic>
+#include <cstring>
+#include <mutex>
+
+#include "shared_tc.cuh"
+#include "sm100.cuh"
+#include "tmap.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int kPage = 64;                          // keys of a page
+constexpr int kDc = 512, kDr = 64, kW = kDc + kDr;
+constexpr int kRows = 128;                         // query rows per CTA
+constexpr int kUnitRows = 256;
+constexpr int kThreads = 384;
+constexpr int kSoftWarps = 8;
+constexpr uint32_t kChunkBytes = kPage * 128;      // [64 keys x 64 dims] bf16, 128-byte swizzled
+constexpr int kKStages = 4;                        // half pages: chunks 0-3, then 4-8
+__host__ __device__ constexpr int half_chunks(int half) { return half ? 5 : 4; }
+constexpr uint32_t kKStageBytes = 5 * kChunkBytes;
+constexpr int kVStages = 4;                        // a page's 256 latent dims of this CTA
+constexpr uint32_t kVStageBytes = 4 * kChunkBytes;
+constexpr uint32_t kPBytes = kRows * kPage * 2;
+constexpr int kPSlots = 5;
+// A page of P travels with its rows' rescale factors: per writer warp 32 factors, a flag word, padding.
+constexpr uint32_t kPaWords = 36;
+constexpr uint32_t kPTxBytes = kPBytes + 4 * kPaWords * 4;
+constexpr uint32_t kPSlotBytes = ((kPTxBytes + 1023) / 1024) * 1024;
+constexpr uint32_t kQpeOff = 0;
+constexpr uint32_t kKOff = kRows * 128;
+constexpr uint32_t kStgOff = kKOff + kKStages * kKStageBytes;
+constexpr uint32_t kPOff = kVStages * kVStageBytes;
+constexpr uint32_t kScoreEnd = kStgOff + 2 * kPSlotBytes, kValueEnd = kPOff + kPSlots * kPSlotBytes;
+constexpr uint32_t kRegion = ((kScoreEnd > kValueEnd ? kScoreEnd : kValueEnd) + 1023) & ~1023u;
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s per wait
+
+constexpr uint32_t kQCol = 0, kSCol = 256;         // score CTA's tensor memory; the value CTA's is all O
+constexpr uint16_t kScorePair = 0x3, kValuePair = 0xc;
+
+// Barrier slots, alike in all four CTAs.
+enum Bar {
+  B_KFULL = 0,                          // score: own stage has landed
+  B_KPEER = B_KFULL + kKStages,         // rank 0: rank 1's stage has landed
+  B_KEMPTY = B_KPEER + kKStages,        // score: the MMAs have read the stage (both CTAs, one commit)
+  B_SFULL = B_KEMPTY + kKStages,        // score: S of a tile is complete (both CTAs)
+  B_SEMPTY = B_SFULL + 2,               // rank 0: both CTAs' softmax warps have read S
+  B_QREADY = B_SEMPTY + 2,              // rank 0: both CTAs' queries are in place
+  B_PEMPTY = B_QREADY + 1,              // score: the value CTA's P slot may be written
+  B_STATSEMPTY = B_PEMPTY + kPSlots,    // score: the value CTA has read the row statistics
+  B_VFULL = B_STATSEMPTY + 1,           // value: own stage has landed
+  B_VEMPTY = B_VFULL + kVStages,        // value: the MMAs have read the stage (both CTAs)
+  B_PFULL = B_VEMPTY + kVStages,        // value: a page of P has landed
+  B_READY = B_PFULL + kPSlots,          // rank 2: rank 3 has P, C and (where due) its O rescaled
+  B_PVDONE = B_READY + kPSlots,         // value: the page's MMAs are complete (both CTAs)
+  B_REQ = B_PVDONE + kPSlots,           // value: request to the epilogue warps
+  B_REQDONE = B_REQ + 1,
+  B_STATSFULL = B_REQDONE + 1,          // value: row statistics of a finished unit
+  B_OFREE = B_STATSFULL + 1,            // value: both CTAs' O has been read (both CTAs)
+  B_COUNT = B_OFREE + 1
+};
+
+struct Req {
+  int kind;      // 0: rescale O before a page's MMAs, 1: the unit's epilogue
+  int slot, segid, last_slot, last_parity;
+};
+
+struct Small {                          // behind the tiles
+  float stat_l[kRows], stat_m[kRows];
+  float xmax[2][2][kRows];
+  float xl[2][kRows];
+  uint64_t bars[B_COUNT];
+  Req req;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kSmemBytes = 1024 + kRegion + sizeof(Small);
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+struct Params {
+  const int *head, *cluster_unit;
+  const SharedUnit *units;
+  const __nv_bfloat16 *q;
+  const int32_t *block_table;
+  int max_blocks_per_seq, num_blocks, block_size;
+  float scale_log2;
+  __nv_bfloat16 *o_part;
+  float *lse_part;
+  int *dev_status;
+  const unsigned char *tiled;           // tiled pool, or NULL: row pool through the tensor maps
+};
+
+// ------------------------------------------------------------ cta_group::2 forms
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// The whole warp calls these; one elected lane (always the same one) issues.
+__device__ __forceinline__ void mma2_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// Arrival on the barrier at this offset in every CTA of `mask` once the elected lane's MMAs so far are complete.
+__device__ __forceinline__ void commit2(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+
+// ------------------------------------------------------------ waits
+__device__ __noinline__ bool timed_out(Small &sm, int *dev_status) {
+  *(volatile int *)&sm.abort = 1;
+  report(dev_status, MLA_ERR_TIMEOUT);
+  return false;
+}
+// One thread's bounded wait; false once any wait of the CTA has given up.
+__device__ __forceinline__ bool wait1(Small &sm, uint32_t bar, uint32_t parity, int *dev_status) {
+  if (*(volatile int *)&sm.abort) return false;
+  if (mbar_wait(bar, parity, kWaitNs, true)) return true;
+  return timed_out(sm, dev_status);
+}
+// Whole-warp wait with one verdict: lane 0 waits, then every lane observes the completed phase (which cannot move on
+// before this warp's own arrival).
+__device__ __forceinline__ bool waitw(Small &sm, uint32_t bar, uint32_t parity, int *dev_status) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = wait1(sm, bar, parity, dev_status) ? 1 : 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  if (ok) mbar_wait(bar, parity, kWaitNs, true);
+  __syncwarp();
+  return ok != 0;
+}
+
+// ------------------------------------------------------------ work list
+// The (unit, tile) runs of one cluster.
+struct Runs {
+  int u, pos, end, cid;
+  SharedUnit un;
+  int t0, t1;       // tiles of the unit in this run
+  __device__ __forceinline__ Runs(const Params &p, int cid_) : u(0), pos(0), end(0), cid(cid_) {
+    const int N = p.head[0], C = p.head[1];
+    if (cid < C) {
+      pos = (int)((int64_t)cid * N / C);
+      end = (int)((int64_t)(cid + 1) * N / C);
+      u = p.cluster_unit[cid];
+    }
+  }
+  __device__ __forceinline__ bool next(const Params &p) {
+    if (pos >= end) return false;
+    const int4 *src = reinterpret_cast<const int4 *>(p.units + u);
+    const int4 a = src[0], b = src[1];
+    un.tile0 = a.x; un.tiles = a.y; un.pages = a.z; un.seq = a.w;
+    un.row0 = b.x; un.rows = b.y;
+    t0 = pos - un.tile0;
+    t1 = min(end - un.tile0, un.tiles);
+    pos = un.tile0 + t1;
+    ++u;
+    return true;
+  }
+  __device__ __forceinline__ int seg() const { return u - 1 + cid; }   // u and cid only rise along the list
+  __device__ __forceinline__ int pages_end() const { return min(2 * t1, un.pages); }
+};
+
+__device__ __forceinline__ int64_t page_row(const Params &p, int seq, int page) {
+  const int key = page * kPage;
+  const int lb = key / p.block_size;
+  if (lb >= p.max_blocks_per_seq) return -1;
+  const int blk = p.block_table[(int64_t)seq * p.max_blocks_per_seq + lb];
+  if (blk < 0 || blk >= p.num_blocks) return -1;
+  return (int64_t)blk * p.block_size + key % p.block_size;
+}
+
+// Pool rows of a run's pages, looked up a warp-load at a time, one load ahead.
+struct PageRows {
+  int seq = -1, base = 0;
+  int64_t r0 = -1, r1 = -1;
+  __device__ __forceinline__ void start(const Params &p, int seq_, int page) {
+    const int lane = threadIdx.x & 31;
+    seq = seq_;
+    base = page;
+    r0 = page_row(p, seq, base + lane);
+    r1 = page_row(p, seq, base + 32 + lane);
+  }
+  // Pages must be asked for in ascending order from the start page on.
+  __device__ __forceinline__ int64_t get(const Params &p, int page) {
+    while (page >= base + 32) {
+      base += 32;
+      r0 = r1;
+      r1 = page_row(p, seq, base + 32 + (threadIdx.x & 31));
+    }
+    return __shfl_sync(0xffffffffu, r0, page - base);
+  }
+};
+
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
+shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_pe,
+                   const __grid_constant__ Params p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Small &sm = *reinterpret_cast<Small *>(tiles + kRegion);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank(), side = rank & 1;   // side: which 128 rows
+  const bool score = rank < 2, lead = side == 0;
+  const int cid = (int)cluster_id_x();
+  auto bar = [&](int i) { return smem_u32(&sm.bars[i]); };
+
+  grid_dep_launch();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < B_COUNT; ++i) {
+      uint32_t n = 1;
+      if ((i >= B_SEMPTY && i < B_SEMPTY + 2) || i == B_QREADY || i == B_OFREE) n = 2 * kSoftWarps;
+      if (i == B_STATSEMPTY || i == B_REQDONE) n = kSoftWarps;
+      if (i == B_STATSFULL) n = kRows;
+      mbar_init(bar(i), n);
+    }
+    if (!score)
+      for (int i = 0; i < kPSlots; ++i) mbar_expect_tx(bar(B_PFULL + i), kPTxBytes);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 3) {
+    tmem_alloc2(smem_u32(&sm.tmem_base), 512);
+    tmem_relinquish2();
+  }
+  if (threadIdx.x == 32 && !p.tiled) {
+    tma_prefetch_desc(&map_c);
+    tma_prefetch_desc(&map_pe);
+  }
+  tc_fence_before();
+  cluster_sync();   // barriers ready in all CTAs before any remote arrival
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+  grid_dep_wait();  // the plan and the queries come from earlier kernels, whose reads of the partials are over too
+
+  Runs it(p, cid);
+  if (warp < 4) {
+    if (score) {
+      if (warp == 0) {
+        // ---- keys: page `side` of every tile as two stages; a tile without that page passes its stages on empty.
+        uint32_t n = 0;
+        PageRows pr;
+        int ok = 1;
+        while (ok && it.next(p)) {
+          pr.start(p, it.un.seq, 2 * it.t0);
+          for (int t = it.t0; ok && t < it.t1; ++t) {
+            const int page = 2 * t + (int)side;
+            const bool have = page < it.un.pages;
+            int64_t row = pr.get(p, have ? page : 2 * t);
+            if (row < 0) {
+              if (lane == 0) report(p.dev_status, MLA_ERR_BAD_INDEX);
+              row = 0;
+            }
+            if (lane == 0)
+              for (int half = 0; half < 2; ++half, ++n) {
+                const int s = n % kKStages;
+                if (n >= kKStages && !wait1(sm, bar(B_KEMPTY + s), (n / kKStages - 1) & 1, p.dev_status)) {
+                  ok = 0;
+                  break;
+                }
+                if (!have) {
+                  mbar_arrive(bar(B_KFULL + s));
+                  continue;
+                }
+                const uint32_t dst = smem_u32(tiles + kKOff + s * kKStageBytes);
+                const int c0 = 4 * half, nc = half_chunks(half);
+                mbar_expect_tx(bar(B_KFULL + s), nc * kChunkBytes);
+                if (p.tiled)
+                  bulk_load(dst, p.tiled + (row / kPage) * (9 * kChunkBytes) + c0 * kChunkBytes, nc * kChunkBytes,
+                            bar(B_KFULL + s));
+                else
+                  for (int c = 0; c < nc; ++c) {
+                    if (c0 + c < 8) tma_load_2d(dst + c * kChunkBytes, &map_c, 64 * (c0 + c), (int32_t)row, bar(B_KFULL + s));
+                    else tma_load_2d(dst + c * kChunkBytes, &map_pe, 0, (int32_t)row, bar(B_KFULL + s));
+                  }
+              }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+          }
+        }
+        // Drain: what was loaded last into each stage has landed before the CTA may exit.
+        if (lane == 0)
+          for (uint32_t i = n > kKStages ? n - kKStages : 0; i < n; ++i)
+            mbar_wait(bar(B_KFULL + i % kKStages), (i / kKStages) & 1, kWaitNs);
+      } else if (warp == 1 && lead) {
+        // ---- S [256 x 128] = Q . K^T, the tile's two pages being the two CTAs' halves of B.
+        const uint32_t idesc = idesc_bf16_f32(kUnitRows, 2 * kPage, false, false);
+        const uint64_t qpe = smem_desc_sw128(smem_u32(tiles + kQpeOff), 16, 1024);
+        uint32_t n = 0, ns = 0, uc = 0;
+        bool ok = true;
+        while (ok && it.next(p)) {
+          ok = waitw(sm, bar(B_QREADY), uc & 1, p.dev_status);
+          ++uc;
+          for (int t = it.t0; ok && t < it.t1; ++t, ++ns) {
+            const uint32_t sbuf = ns & 1, dcol = tbase + kSCol + 128 * sbuf;
+            if (ns >= 2 && !(ok = waitw(sm, bar(B_SEMPTY + sbuf), (ns / 2 - 1) & 1, p.dev_status))) break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half, ++n) {
+              const int s = n % kKStages;
+              const uint32_t par = (n / kKStages) & 1;
+              ok = ok && waitw(sm, bar(B_KFULL + s), par, p.dev_status) && waitw(sm, bar(B_KPEER + s), par, p.dev_status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t kd = smem_desc_sw128(smem_u32(tiles + kKOff + s * kKStageBytes), 16, 1024);
+#pragma unroll
+              for (int c = 0; c < half_chunks(half); ++c) {
+                const int j = 4 * half + c;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint64_t bd = kd + ((c * kChunkBytes + kk * 32) >> 4);
+                  if (j < 8) mma2_ts(dcol, tbase + kQCol + 32 * j + 8 * kk, bd, idesc, (j | kk) ? 1u : 0u);
+                  else mma2_ss(dcol, qpe + ((kk * 32) >> 4), bd, idesc, 1u);
+                }
+              }
+              commit2(bar(B_KEMPTY + s), kScorePair);
+            }
+            if (ok) commit2(bar(B_SFULL + sbuf), kScorePair);
+          }
+        }
+      } else if (warp == 1 && lane == 0) {
+        // ---- rank 1: tells rank 0 about its stages.
+        const uint32_t kpeer = mapa(bar(B_KPEER), 0);
+        uint32_t n = 0;
+        bool ok = true;
+        while (ok && it.next(p))
+          for (int i = 2 * it.t0; ok && i < 2 * it.t1; ++i, ++n) {
+            const int s = n % kKStages;
+            ok = wait1(sm, bar(B_KFULL + s), (n / kKStages) & 1, p.dev_status);
+            if (ok) mbar_arrive_cluster(kpeer + 8 * s);
+          }
+      }
+    } else {
+      if (warp == 0) {
+        // ---- latents: dims 256 side .. of every page, one stage each.
+        uint32_t n = 0;
+        PageRows pr;
+        int ok = 1;
+        while (ok && it.next(p)) {
+          pr.start(p, it.un.seq, 2 * it.t0);
+          for (int g = 2 * it.t0; ok && g < it.pages_end(); ++g, ++n) {
+            int64_t row = pr.get(p, g);
+            if (row < 0) row = 0;   // reported by the score pair
+            const int s = n % kVStages;
+            if (lane == 0) {
+              if (n >= kVStages && !wait1(sm, bar(B_VEMPTY + s), (n / kVStages - 1) & 1, p.dev_status)) ok = 0;
+              if (ok) {
+                const uint32_t dst = smem_u32(tiles + s * kVStageBytes);
+                mbar_expect_tx(bar(B_VFULL + s), kVStageBytes);
+                if (p.tiled)
+                  bulk_load(dst, p.tiled + (row / kPage) * (9 * kChunkBytes) + side * kVStageBytes, kVStageBytes,
+                            bar(B_VFULL + s));
+                else
+                  for (int c = 0; c < 4; ++c)
+                    tma_load_2d(dst + c * kChunkBytes, &map_c, 256 * (int)side + 64 * c, (int32_t)row, bar(B_VFULL + s));
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+          }
+        }
+        if (lane == 0)
+          for (uint32_t i = n > kVStages ? n - kVStages : 0; i < n; ++i)
+            mbar_wait(bar(B_VFULL + i % kVStages), (i / kVStages) & 1, kWaitNs);
+      } else if (warp == 1) {
+        // ---- O += P . C.  Both CTAs walk the pages alike: P has landed, O rescaled where the page asks for it, C has
+        // landed; rank 3 then reports to rank 2, which issues for both.
+        const uint32_t idesc = idesc_bf16_f32(kUnitRows, 256, false, true);
+        const uint32_t ready = mapa(bar(B_READY), 2);
+        uint32_t np = 0, uc = 0, nfix = 0;
+        bool ok = true;
+        while (ok && it.next(p)) {
+          if (uc > 0 && !(ok = waitw(sm, bar(B_OFREE), (uc - 1) & 1, p.dev_status))) break;
+          for (int g = 2 * it.t0; g < it.pages_end(); ++g, ++np) {
+            const int pb = np % kPSlots, sv = np % kVStages;
+            const uint32_t ppar = (np / kPSlots) & 1;
+            if (!(ok = waitw(sm, bar(B_PFULL + pb), ppar, p.dev_status))) break;
+            const uint32_t slot = smem_u32(tiles + kPOff + pb * kPSlotBytes);
+            const bool first = g == 2 * it.t0;
+            if (!first) {
+              uint32_t moved = 0;
+              const float *pa = reinterpret_cast<const float *>(tiles + kPOff + pb * kPSlotBytes + kPBytes);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) moved |= reinterpret_cast<const uint32_t *>(pa + w * kPaWords)[32];
+              if (moved) {
+                // O is read back: the previous page's MMAs must be complete.
+                if (!(ok = waitw(sm, bar(B_PVDONE + (np - 1) % kPSlots), ((np - 1) / kPSlots) & 1, p.dev_status))) break;
+                if (lane == 0) {
+                  sm.req = Req{0, pb, 0, 0, 0};
+                  mbar_arrive(bar(B_REQ));
+                }
+                if (!(ok = waitw(sm, bar(B_REQDONE), nfix & 1, p.dev_status))) break;
+                tc_fence_after();
+                ++nfix;
+              }
+            }
+            if (!(ok = waitw(sm, bar(B_VFULL + sv), (np / kVStages) & 1, p.dev_status))) break;
+            if (!lead) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(ready + 8 * pb);
+              continue;
+            }
+            if (!(ok = waitw(sm, bar(B_READY + pb), ppar, p.dev_status))) break;
+            tc_fence_after();
+            const uint64_t ad = smem_desc_sw128(slot, 16, 1024);
+            const uint64_t bd = smem_desc_sw128(smem_u32(tiles + sv * kVStageBytes), kChunkBytes, 1024);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma2_ss(tbase + 256 * h, ad + ((ks * 32) >> 4), bd + ((h * 2 * kChunkBytes + ks * 2048) >> 4), idesc,
+                        (first && ks == 0) ? 0u : 1u);
+            commit2(bar(B_VEMPTY + sv), kValuePair);
+            commit2(bar(B_PVDONE + pb), kValuePair);
+          }
+          if (!ok) break;
+          const uint32_t last = np - 1;
+          if (lane == 0) {
+            sm.req = Req{1, 0, it.seg(), (int)(last % kPSlots), (int)((last / kPSlots) & 1)};
+            mbar_arrive(bar(B_REQ));
+          }
+          __syncwarp();
+          ++uc;
+        }
+      } else if (warp == 2 && lane == 0) {
+        // ---- a P slot may be written again once the MMAs that read it are complete.
+        const uint32_t pempty = mapa(bar(B_PEMPTY), side);
+        uint32_t np = 0;
+        bool ok = true;
+        while (ok && it.next(p))
+          for (int g = 2 * it.t0; g < it.pages_end(); ++g, ++np) {
+            const int pb = np % kPSlots;
+            if (!(ok = wait1(sm, bar(B_PVDONE + pb), (np / kPSlots) & 1, p.dev_status))) break;
+            mbar_expect_tx(bar(B_PFULL + pb), kPTxBytes);
+            mbar_arrive_cluster(pempty + 8 * pb);
+          }
+      }
+    }
+  } else if (score) {
+    // ---- softmax: warp (quadrant q4, half h) owns rows 32 q4 .. and page h of every tile.  No early exit: the warps
+    // meet at named barriers, and after a timeout every wait returns at once.
+    const int q4 = warp & 3, h = (warp - 4) >> 2;
+    const int r = q4 * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const uint32_t mate = 2 + side;                       // the value CTA of these rows
+    const uint32_t pslot_remote = mapa(smem_u32(tiles + kPOff), mate), pfull_remote = mapa(bar(B_PFULL), mate);
+    const uint32_t statl_remote = mapa(smem_u32(&sm.stat_l[0]), mate), statm_remote = mapa(smem_u32(&sm.stat_m[0]), mate);
+    const uint32_t statsfull_remote = mapa(bar(B_STATSFULL), mate);
+    const uint32_t sempty = mapa(bar(B_SEMPTY), 0), qready = mapa(bar(B_QREADY), 0);
+    unsigned char *stgp = tiles + kStgOff + h * kPSlotBytes;
+    unsigned char *stga = stgp + kPBytes;
+    uint32_t ns = 0, np = 0, uc = 0;
+    while (it.next(p)) {
+      // Queries of the unit: latent dims 256 h .. of the warp's rows into tensor memory, coalesced through the warp's
+      // part of the P staging tile (whose last copy must have been read); half 0 also stages the RoPE dims.  The last
+      // S of the previous unit has been read, so its MMAs are complete.
+      {
+        if (q4 == 0 && lane == 0) bulk_wait_read_all();
+        asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
+        unsigned char *stg_w = stgp + q4 * 4096;
+        const int j = lane & 7;
+        const uint4 *rowp[8];
+        bool live[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int g = kRows * (int)side + q4 * 32 + 4 * k + (lane >> 3);
+          live[k] = g < it.un.rows;
+          rowp[k] = reinterpret_cast<const uint4 *>(p.q + (int64_t)(it.un.row0 + (live[k] ? g : 0)) * kW);
+        }
+#pragma unroll 1
+        for (int cb = 0; cb < 4; cb += 2) {
+          uint4 x[2][8];
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              x[rr][k] = live[k] ? __ldg(rowp[k] + h * 32 + (cb + rr) * 8 + j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int lr = 4 * k + (lane >> 3);
+              *reinterpret_cast<uint4 *>(stg_w + (lr >> 3) * 1024 + (lr & 7) * 128 + ((j ^ (lr & 7)) << 4)) = x[rr][k];
+            }
+            __syncwarp();
+            uint32_t v[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 y = *reinterpret_cast<const uint4 *>(stg_w + (lane >> 3) * 1024 + (lane & 7) * 128 + ((i ^ (lane & 7)) << 4));
+              v[4 * i] = y.x; v[4 * i + 1] = y.y; v[4 * i + 2] = y.z; v[4 * i + 3] = y.w;
+            }
+            tmem_st32(tbase + lane_off + kQCol + 128 * h + 32 * (cb + rr), v);
+            __syncwarp();
+          }
+        }
+        if (h == 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rq = q4 * 32 + 4 * k + (lane >> 3);
+            *reinterpret_cast<uint4 *>(tiles + kQpeOff + (rq >> 3) * 1024 + (rq & 7) * 128 + ((j ^ (rq & 7)) << 4)) =
+                live[k] ? __ldg(rowp[k] + 64 + j) : make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(qready);
+      }
+      float m_ref = -CUDART_INF_F, l = 0.f;
+      for (int t = it.t0; t < it.t1; ++t, ++ns) {
+        const int npg = min(2, it.un.pages - 2 * t);
+        const uint32_t sbuf = ns & 1;
+        waitw(sm, bar(B_SFULL + sbuf), (ns >> 1) & 1, p.dev_status);
+        tc_fence_after();
+        const uint32_t scol = tbase + lane_off + kSCol + 128 * sbuf + 64 * h;
+        auto release_s = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(sempty + 8 * sbuf);
+        };
+        float mx = -CUDART_INF_F;
+        if (h < npg) {
+#pragma unroll 1
+          for (int c2 = 0; c2 < 2; ++c2) {
+            uint32_t v[32];
+            tmem_ld32(scol + 32 * c2, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) mx = max3f(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+          }
+        } else {
+          release_s();   // no page here
+        }
+        mx *= p.scale_log2;
+        sm.xmax[ns & 1][h][r] = mx;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        mx = fmaxf(mx, sm.xmax[ns & 1][h ^ 1][r]);
+        float alpha = 1.f;
+        const bool need = mx > m_ref + kRescaleLog2;
+        if (need) {
+          alpha = exp2f(m_ref - mx);
+          l *= alpha;
+          m_ref = mx;
+        }
+        if (h < npg) {
+          const uint32_t pn = np + h;
+          const int pb = pn % kPSlots;
+          const bool sender = q4 == 0 && lane == 0;
+          if (sender) bulk_wait_read_all();   // the staging tile's previous copy has been read
+          asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
+          unsigned char *prow = stgp + 4096 * q4 + (lane >> 3) * 1024 + (lane & 7) * 128;
+          float psum0 = 0.f, psum1 = 0.f;
+#pragma unroll 1
+          for (int c2 = 0; c2 < 2; ++c2) {
+            uint32_t v[32];
+            tmem_ld32(scol + 32 * c2, v);
+            tmem_wait_ld();
+            if (c2 == 1) release_s();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int k = 8 * c + 2 * e;
+                const float p0 = exp2f(__uint_as_float(v[k]) * p.scale_log2 - m_ref);
+                const float p1 = exp2f(__uint_as_float(v[k + 1]) * p.scale_log2 - m_ref);
+                pk[e] = pack_bf16x2(p0, p1);
+                psum0 += p0;
+                psum1 += p1;
+              }
+              *reinterpret_cast<uint4 *>(prow + (((4 * c2 + c) ^ (lane & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          }
+          l += psum0 + psum1;
+          // The first page of a tile carries its rows' rescale factors.
+          float *pa = reinterpret_cast<float *>(stga) + q4 * kPaWords;
+          pa[lane] = h == 0 ? alpha : 1.f;
+          const unsigned moved = __ballot_sync(0xffffffffu, need && h == 0 && t != it.t0);
+          if (lane < 4) reinterpret_cast<uint32_t *>(pa + 32)[lane] = (lane == 0 && moved) ? 1u : 0u;
+          fence_proxy_async_smem();
+          asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
+          if (sender && (pn < kPSlots || wait1(sm, bar(B_PEMPTY + pb), ((pn / kPSlots) - 1) & 1, p.dev_status))) {
+            bulk_copy_to_peer(pslot_remote + pb * kPSlotBytes, smem_u32(stgp), kPTxBytes, pfull_remote + 8 * pb);
+            bulk_commit();
+          }
+        }
+        np += npg;
+      }
+      sm.xl[h][r] = l;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (h == 0) {
+        l += sm.xl[1][r];
+        if (uc > 0) waitw(sm, bar(B_STATSEMPTY), (uc - 1) & 1, p.dev_status);
+        st_cluster_f32(statl_remote + r * 4, l);
+        st_cluster_f32(statm_remote + r * 4, m_ref);
+        mbar_arrive_cluster(statsfull_remote);
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");   // xl may be used again
+      ++uc;
+    }
+    if (lane == 0) bulk_wait_all();
+  } else {
+    // ---- epilogue warps: group g owns O columns 256 g ..; warp w owns rows 32 (w & 3) ...
+    const int g = (warp - 4) >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ocol = 256 * g;
+    const uint32_t statsempty_remote = mapa(bar(B_STATSEMPTY), side);
+    const uint32_t ofree2 = mapa(bar(B_OFREE), 2), ofree3 = mapa(bar(B_OFREE), 3);
+    uint32_t nreq = 0, uc = 0;
+    bool ok = true;
+    while (ok && it.next(p)) {
+      for (;;) {
+        if (!(ok = waitw(sm, bar(B_REQ), nreq & 1, p.dev_status))) break;
+        ++nreq;
+        const Req q = sm.req;
+        if (q.kind == 0) {
+          tc_fence_after();
+          const float a = reinterpret_cast<const float *>(tiles + kPOff + q.slot * kPSlotBytes + kPBytes)[(r >> 5) * kPaWords + (r & 31)];
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[32];
+            tmem_ld32(tbase + lane_off + ocol + 32 * c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+            tmem_st32(tbase + lane_off + ocol + 32 * c, v);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_REQDONE));
+          continue;
+        }
+        if (!(ok = waitw(sm, bar(B_PVDONE + q.last_slot), q.last_parity, p.dev_status) &&
+                   waitw(sm, bar(B_STATSFULL), uc & 1, p.dev_status)))
+          break;
+        tc_fence_after();
+        const float l = sm.stat_l[r], m = sm.stat_m[r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(statsempty_remote);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int64_t prow = (int64_t)q.segid * kUnitRows + kRows * side + r;
+        const bool live = kRows * (int)side + r < it.un.rows;
+        __nv_bfloat16 *dst = p.o_part + prow * kDc;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tbase + lane_off + ocol + 32 * c, v);
+          tmem_wait_ld();
+          // Columns 256 g .. are rank 2's dims 128 g .. 128 g + 127, then rank 3's, 256 further on.
+          const int dim = 256 * (c >> 2) + 128 * g + 32 * (c & 3);
+          if (live)
+#pragma unroll
+            for (int i = 0; i < 32; i += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(v[i + 2 * e]) * inv, __uint_as_float(v[i + 2 * e + 1]) * inv);
+              st_global_v8(dst + dim + i, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+            }
+        }
+        if (g == 0 && live) p.lse_part[prow] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster(ofree2);
+          mbar_arrive_cluster(ofree3);
+        }
+        ++uc;
+        break;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the pair frees its tensor memory together, after both CTAs' last access
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc2(tbase, 512);
+  }
+  cluster_sync();   // no CTA leaves while another may still reach its shared memory
+}
+
+// ------------------------------------------------------------ plan
+// One CTA.  Shared keys of a group: the whole blocks among its first min(prefix_lens[g], shortest visible run) keys,
+// where the first query token of sequence b sees seqlens[b] - n_q + 1 keys.
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+
+__device__ __forceinline__ int cluster_of(int64_t t, int N, int C) { return (int)(((t + 1) * C + N - 1) / N - 1); }
+
+__global__ void __launch_bounds__(kPlanThreads)
+shared_plan_kernel(SharedPlan pl, int B, int n_q, int R, int max_seqlen, int block_size, int G, int clusters,
+                   const int32_t *offsets,
+                   const int32_t *prefix_lens, const int32_t *seqlens, int *dev_status) {
+  __shared__ int64_t part[kPlanWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_launch();
+  grid_dep_wait();   // earlier calls may still read the plan that is overwritten here
+  int bad = 0;
+  for (int g = tid; g < G; g += kPlanThreads) {
+    const int lo = offsets[g], hi = offsets[g + 1];
+    bad |= lo < 0 || lo > hi || hi > B || (g == 0 && lo != 0) || (g == G - 1 && hi != B) || prefix_lens[g] < 0;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) report(dev_status, MLA_ERR_BAD_INDEX);
+  if (bad) G = 0;
+  if (G == 0)
+    for (int b = tid; b < B; b += kPlanThreads) {
+      pl.own_begin[b] = 0;
+      pl.seq_unit[b] = make_int2(-1, 0);
+    }
+  // Pages of every group.
+  for (int g = warp; g < G; g += kPlanWarps) {
+    const int lo = offsets[g], hi = offsets[g + 1];
+    int common = prefix_lens[g];
+    for (int b = lo + lane; b < hi; b += 32) {
+      const int S = min(seqlens[b], max_seqlen);
+      common = min(common, max(S - n_q + 1, 0));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) common = min(common, __shfl_xor_sync(0xffffffffu, common, o));
+    // A sequence alone shares nothing.
+    if (lane == 0) pl.group_pages[g] = hi - lo > 1 ? common / block_size * (block_size / kPage) : 0;
+  }
+  __syncthreads();
+  // First unit and first tile of every group (their sums packed: units low, tiles high), a slab of groups at a time.
+  // The totals are needed first (clusters are dealt out over all tiles), so there are two passes.
+  for (int pass = 0; pass < 2; ++pass) {
+    __shared__ int64_t s_total;
+    int64_t carry = 0;
+    const int64_t total = pass ? s_total : 0;
+    const int N = (int)(total >> 32), U = (int)(total & 0xffffffff);
+    const int C = N < clusters ? N : clusters;
+    for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
+      const int g = g0 + tid;
+      int64_t v = 0;
+      if (g < G) {
+        const int pages = pl.group_pages[g];
+        const int units = pages ? (int)(((int64_t)(offsets[g + 1] - offsets[g]) * R + kUnitRows - 1) / kUnitRows) : 0;
+        v = (int64_t)units | ((int64_t)units * ((pages + 1) / 2) << 32);
+      }
+      int64_t inc = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t w = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += w;
+      }
+      __syncthreads();
+      if (lane == 31) part[warp] = inc;
+      __syncthreads();
+      int64_t w = part[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+      }
+      const int64_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+      const int64_t slab = __shfl_sync(0xffffffffu, w, 31);
+      const int64_t exc = carry + (warp ? before : 0) + inc - v;
+      carry += slab;
+      if (pass) {
+        // The warp writes its 32 groups one after another.
+        for (int k = 0; k < 32; ++k) {
+          const int gg = g0 + warp * 32 + k;
+          if (gg >= G) break;
+          const int64_t e = __shfl_sync(0xffffffffu, exc, k);
+          const int u0 = (int)(e & 0xffffffff), tile0 = (int)(e >> 32);
+          const int lo = offsets[gg], hi = offsets[gg + 1], pages = pl.group_pages[gg];
+          const int rows = (hi - lo) * R, tiles = (pages + 1) / 2;
+          const int units = pages ? (rows + kUnitRows - 1) / kUnitRows : 0;
+          for (int b = lo + lane; b < hi; b += 32) {
+            pl.own_begin[b] = pages * kPage;
+            pl.seq_unit[b] = make_int2(pages ? u0 : -1, lo * R);
+          }
+          for (int i = lane; i < units; i += 32) {
+            const int u = u0 + i, ut = tile0 + i * tiles;
+            const int4 a = make_int4(ut, tiles, pages, lo);
+            const int4 c = make_int4(lo * R + i * kUnitRows, min(kUnitRows, rows - i * kUnitRows), 0, 0);
+            reinterpret_cast<int4 *>(pl.units + u)[0] = a;
+            reinterpret_cast<int4 *>(pl.units + u)[1] = c;
+            const int c0 = cluster_of(ut, N, C), c1 = cluster_of((int64_t)ut + tiles - 1, N, C);
+            pl.unit_segs[u] = make_int2(u + c0, c1 - c0 + 1);
+            // Clusters whose first tile lies in this unit.
+            for (int x = c0; x <= c1; ++x)
+              if ((int64_t)x * N / C >= ut) pl.cluster_unit[x] = u;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (!pass && tid == 0) s_total = carry;
+    __syncthreads();
+    if (pass && tid == 0) *reinterpret_cast<int4 *>(pl.head) = make_int4(N, C, U, 0);
+  }
+}
+
+}  // namespace
+
+int shared_clusters_for_device() {
+  static std::atomic<int> cached[128];
+  static std::mutex mu;
+  int dev = 0, ndev = 0;
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev <= 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
+  if (const int c = cached[dev].load(std::memory_order_acquire)) return c;
+  std::lock_guard<std::mutex> lock(mu);
+  if (const int c = cached[dev].load(std::memory_order_acquire)) return c;
+  if (cudaFuncSetAttribute(shared_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes)) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4 * kSharedMaxClusters);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 4;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, shared_attn_kernel, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (n > kSharedMaxClusters) n = kSharedMaxClusters;
+  cached[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+int launch_shared_plan(const SharedPlan &pl, int B, int n_q, int H, int max_seqlen, int block_size, int num_groups,
+                       const int32_t *group_offsets, const int32_t *prefix_lens, const int32_t *seqlens,
+                       int *dev_status, cudaStream_t st) {
+  const int C = shared_clusters_for_device();
+  if (C <= 0) return MLA_ERR_CUDA;
+  return launch_pdl(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, pl, B, n_q, n_q * H, max_seqlen, block_size,
+                    num_groups, C, group_offsets, prefix_lens, seqlens, dev_status) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+int launch_shared_attention(const mla_dims &d, const SharedPlan &pl, const void *q_abs, const CacheView &cache,
+                            __nv_bfloat16 *o_part, float *lse_part, int *dev_status, cudaStream_t st) {
+  const bool tiled = cache.layout == MLA_CACHE_TILED;
+  CUtensorMap mc, mpe;
+  memset(&mc, 0, sizeof(mc));
+  memset(&mpe, 0, sizeof(mpe));
+  if (!tiled) {
+    const uint64_t rows = (uint64_t)cache.num_blocks * cache.block_size;
+    if (!make_tmap_bf16(&mc, cache.c_kv, kDc, rows, (uint64_t)cache.ckv_stride * 2, kPage) ||
+        !make_tmap_bf16(&mpe, cache.k_pe, kDr, rows, (uint64_t)cache.kpe_stride * 2, kPage))
+      return MLA_ERR_CUDA;
+  }
+  const int C = shared_clusters_for_device();
+  if (C <= 0) return MLA_ERR_CUDA;
+  Params p;
+  p.head = pl.head;
+  p.cluster_unit = pl.cluster_unit;
+  p.units = pl.units;
+  p.q = static_cast<const __nv_bfloat16 *>(q_abs);
+  p.block_table = cache.block_table;
+  p.max_blocks_per_seq = cache.max_blocks_per_seq;
+  p.num_blocks = cache.num_blocks;
+  p.block_size = cache.block_size;
+  p.scale_log2 = default_scale(d) * 1.4426950408889634f;
+  p.o_part = o_part;
+  p.lse_part = lse_part;
+  p.dev_status = dev_status;
+  p.tiled = tiled ? static_cast<const unsigned char *>(cache.c_kv) : nullptr;
+  return launch_pdl(shared_attn_kernel, dim3(4 * C), dim3(kThreads), kSmemBytes, st, mc, mpe, p) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+}  // namespace mla
