@@ -161,21 +161,19 @@ __device__ __noinline__ bool timed_out(Small &sm, int *dev_status) {
   report(dev_status, MLA_ERR_TIMEOUT);
   return false;
 }
-// One thread's bounded wait; false once any wait of the CTA has given up.
-__device__ __forceinline__ bool wait1(Small &sm, uint32_t bar, uint32_t parity, int *dev_status) {
+// One thread's bounded wait; false once any wait of the CTA has given up.  `remote`: what is waited for was written
+// by another CTA's threads (not by copies or MMAs).
+__device__ __forceinline__ bool wait1(Small &sm, uint32_t bar, uint32_t parity, int *dev_status, bool remote = false) {
+  if (remote ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
   if (*(volatile int *)&sm.abort) return false;
-  if (mbar_wait(bar, parity, kWaitNs, true)) return true;
+  if (mbar_wait(bar, parity, kWaitNs, remote)) return true;
   return timed_out(sm, dev_status);
 }
-// Whole-warp wait with one verdict: lane 0 waits, then every lane observes the completed phase (which cannot move on
-// before this warp's own arrival).
-__device__ __forceinline__ bool waitw(Small &sm, uint32_t bar, uint32_t parity, int *dev_status) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = wait1(sm, bar, parity, dev_status) ? 1 : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  if (ok) mbar_wait(bar, parity, kWaitNs, true);
-  __syncwarp();
-  return ok != 0;
+// The same for a whole warp, with one verdict.
+__device__ __forceinline__ bool waitw(Small &sm, uint32_t bar, uint32_t parity, int *dev_status, bool remote = false) {
+  const bool ok = remote ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return __all_sync(0xffffffffu, wait1(sm, bar, parity, dev_status, remote));
 }
 
 // ------------------------------------------------------------ work list
@@ -334,7 +332,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         uint32_t n = 0, ns = 0, uc = 0;
         bool ok = true;
         while (ok && it.next(p)) {
-          ok = waitw(sm, bar(B_QREADY), uc & 1, p.dev_status);
+          ok = waitw(sm, bar(B_QREADY), uc & 1, p.dev_status, true);
           ++uc;
           for (int t = it.t0; ok && t < it.t1; ++t, ++ns) {
             const uint32_t sbuf = ns & 1, dcol = tbase + kSCol + 128 * sbuf;
@@ -371,7 +369,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
           for (int i = 2 * it.t0; ok && i < 2 * it.t1; ++i, ++n) {
             const int s = n % kKStages;
             ok = wait1(sm, bar(B_KFULL + s), (n / kKStages) & 1, p.dev_status);
-            if (ok) mbar_arrive_cluster(kpeer + 8 * s);
+            if (ok) mbar_arrive_cluster_light(kpeer + 8 * s);
           }
       }
     } else {
@@ -442,7 +440,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             if (!lead) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(ready + 8 * pb);
+              if (lane == 0) mbar_arrive_cluster_light(ready + 8 * pb);
               continue;
             }
             if (!(ok = waitw(sm, bar(B_READY + pb), ppar, p.dev_status))) break;
@@ -477,7 +475,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             const int pb = np % kPSlots;
             if (!(ok = wait1(sm, bar(B_PVDONE + pb), (np / kPSlots) & 1, p.dev_status))) break;
             mbar_expect_tx(bar(B_PFULL + pb), kPTxBytes);
-            mbar_arrive_cluster(pempty + 8 * pb);
+            mbar_arrive_cluster_light(pempty + 8 * pb);
           }
       }
     }
@@ -562,7 +560,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         auto release_s = [&]() {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(sempty + 8 * sbuf);
+          if (lane == 0) mbar_arrive_cluster_light(sempty + 8 * sbuf);
         };
         float mx = -CUDART_INF_F;
         if (h < npg) {
@@ -679,7 +677,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
           continue;
         }
         if (!(ok = waitw(sm, bar(B_PVDONE + q.last_slot), q.last_parity, p.dev_status) &&
-                   waitw(sm, bar(B_STATSFULL), uc & 1, p.dev_status)))
+                   waitw(sm, bar(B_STATSFULL), uc & 1, p.dev_status, true)))
           break;
         tc_fence_after();
         const float l = sm.stat_l[r], m = sm.stat_m[r];

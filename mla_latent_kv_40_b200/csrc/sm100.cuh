@@ -108,6 +108,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 
+// The same arrival without ordering this thread's writes for the other CTA.  The cluster-scope release costs a few
+// hundred cycles where the thread has writes in flight; arrivals that only pass on tensor-memory reads (ordered by
+// tcgen05.fence) or copies of the async proxy (ordered by their own barrier) do without it.
+__device__ __forceinline__ void mbar_arrive_cluster_light(uint32_t remote_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
