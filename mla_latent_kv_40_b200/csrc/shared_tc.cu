@@ -73,19 +73,19 @@ constexpr uint16_t kScorePair = 0x3, kValuePair = 0xc;
 
 // Barrier slots, alike in all four CTAs.
 enum Bar {
-  B_KFULL = 0,                          // score: own stage has landed
-  B_KPEER = B_KFULL + kKStages,         // rank 0: rank 1's stage has landed
-  B_KEMPTY = B_KPEER + kKStages,        // score: the MMAs have read the stage (both CTAs, one commit)
+  B_KFULL = 0,                          // score: own stage has landed; at rank 0 rank 1's as well
+  B_KEMPTY = B_KFULL + kKStages,        // score: the MMAs have read the stage (both CTAs, one commit)
   B_SFULL = B_KEMPTY + kKStages,        // score: S of a tile is complete (both CTAs)
   B_SEMPTY = B_SFULL + 2,               // rank 0: both CTAs' softmax warps have read S
   B_QREADY = B_SEMPTY + 2,              // rank 0: both CTAs' queries are in place
   B_PEMPTY = B_QREADY + 1,              // score: the value CTA's P slot may be written
   B_STATSEMPTY = B_PEMPTY + kPSlots,    // score: the value CTA has read the row statistics
-  B_VFULL = B_STATSEMPTY + 1,           // value: own stage has landed
+  B_STGFULL = B_STATSEMPTY + 1,         // score: a page of P is staged, per softmax group
+  B_STGEMPTY = B_STGFULL + 2,           // score: its copy has read the staging tile
+  B_VFULL = B_STGEMPTY + 2,              // value: own stage has landed; at rank 2 also: rank 3 has P, C and its O rescaled
   B_VEMPTY = B_VFULL + kVStages,        // value: the MMAs have read the stage (both CTAs)
   B_PFULL = B_VEMPTY + kVStages,        // value: a page of P has landed
-  B_READY = B_PFULL + kPSlots,          // rank 2: rank 3 has P, C and (where due) its O rescaled
-  B_PVDONE = B_READY + kPSlots,         // value: the page's MMAs are complete (both CTAs)
+  B_PVDONE = B_PFULL + kPSlots,         // value: the page's MMAs are complete (both CTAs)
   B_REQ = B_PVDONE + kPSlots,           // value: request to the epilogue warps
   B_REQDONE = B_REQ + 1,
   B_STATSFULL = B_REQDONE + 1,          // value: row statistics of a finished unit
@@ -100,8 +100,8 @@ struct Req {
 
 struct Small {                          // behind the tiles
   float stat_l[kRows], stat_m[kRows];
-  float xmax[2][2][kRows];
-  float xl[2][kRows];
+  float m_sh[2][kRows];                 // score: reference maximum after a tile, per group
+  float xl[kRows];
   uint64_t bars[B_COUNT];
   Req req;
   uint32_t tmem_base;
@@ -253,8 +253,11 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
       uint32_t n = 1;
-      if ((i >= B_SEMPTY && i < B_SEMPTY + 2) || i == B_QREADY || i == B_OFREE) n = 2 * kSoftWarps;
+      if (i == B_QREADY || i == B_OFREE) n = 2 * kSoftWarps;
+      if (i >= B_SEMPTY && i < B_SEMPTY + 2) n = kSoftWarps;   // four warps of each CTA
+      if (lead && ((i >= B_KFULL && i < B_KFULL + kKStages) || (i >= B_VFULL && i < B_VFULL + kVStages))) n = 2;
       if (i == B_STATSEMPTY || i == B_REQDONE) n = kSoftWarps;
+      if (i >= B_STGFULL && i < B_STGFULL + 2) n = 4;
       if (i == B_STATSFULL) n = kRows;
       mbar_init(bar(i), n);
     }
@@ -341,7 +344,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             for (int half = 0; half < 2; ++half, ++n) {
               const int s = n % kKStages;
               const uint32_t par = (n / kKStages) & 1;
-              ok = ok && waitw(sm, bar(B_KFULL + s), par, p.dev_status) && waitw(sm, bar(B_KPEER + s), par, p.dev_status);
+              ok = ok && waitw(sm, bar(B_KFULL + s), par, p.dev_status);
               if (!ok) break;
               tc_fence_after();
               const uint64_t kd = smem_desc_sw128(smem_u32(tiles + kKOff + s * kKStageBytes), 16, 1024);
@@ -362,7 +365,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         }
       } else if (warp == 1 && lane == 0) {
         // ---- rank 1: tells rank 0 about its stages.
-        const uint32_t kpeer = mapa(bar(B_KPEER), 0);
+        const uint32_t kpeer = mapa(bar(B_KFULL), 0);
         uint32_t n = 0;
         bool ok = true;
         while (ok && it.next(p))
@@ -371,6 +374,32 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             ok = wait1(sm, bar(B_KFULL + s), (n / kKStages) & 1, p.dev_status);
             if (ok) mbar_arrive_cluster_light(kpeer + 8 * s);
           }
+      } else if (warp >= 2 && lane == 0) {
+        // ---- sender of softmax group h = warp - 2: every staged page goes to the value CTA of these rows, into the slot
+        // of its place in the unit's pages, once the MMAs that read the slot before are complete.
+        const int h = warp - 2;
+        const uint32_t mate = 2 + side;
+        const uint32_t pslot_remote = mapa(smem_u32(tiles + kPOff), mate), pfull_remote = mapa(bar(B_PFULL), mate);
+        const uint32_t stg = smem_u32(tiles + kStgOff + h * kPSlotBytes);
+        uint32_t ns = 0, np = 0, nst = 0;
+        bool ok = true;
+        while (ok && it.next(p))
+          for (int t = it.t0; ok && t < it.t1; ++t, ++ns) {
+            const int npg = min(2, it.un.pages - 2 * t);
+            if ((int)(ns & 1) == h)
+              for (int pg = 0; ok && pg < npg; ++pg, ++nst) {
+                const uint32_t pn = np + pg, pb = pn % kPSlots;
+                ok = wait1(sm, bar(B_STGFULL + h), nst & 1, p.dev_status) &&
+                     (pn < kPSlots || wait1(sm, bar(B_PEMPTY + pb), (pn / kPSlots - 1) & 1, p.dev_status));
+                if (!ok) break;
+                bulk_copy_to_peer(pslot_remote + pb * kPSlotBytes, stg, kPTxBytes, pfull_remote + 8 * pb);
+                bulk_commit();
+                bulk_wait_read_all();
+                mbar_arrive(bar(B_STGEMPTY + h));
+              }
+            np += npg;
+          }
+        bulk_wait_all();   // the copies have landed before the CTA may exit
       }
     } else {
       if (warp == 0) {
@@ -408,7 +437,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         // ---- O += P . C.  Both CTAs walk the pages alike: P has landed, O rescaled where the page asks for it, C has
         // landed; rank 3 then reports to rank 2, which issues for both.
         const uint32_t idesc = idesc_bf16_f32(kUnitRows, 256, false, true);
-        const uint32_t ready = mapa(bar(B_READY), 2);
+        const uint32_t ready = mapa(bar(B_VFULL), 2);
         uint32_t np = 0, uc = 0, nfix = 0;
         bool ok = true;
         while (ok && it.next(p)) {
@@ -440,10 +469,9 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             if (!lead) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_light(ready + 8 * pb);
+              if (lane == 0) mbar_arrive_cluster_light(ready + 8 * sv);
               continue;
             }
-            if (!(ok = waitw(sm, bar(B_READY + pb), ppar, p.dev_status))) break;
             tc_fence_after();
             const uint64_t ad = smem_desc_sw128(slot, 16, 1024);
             const uint64_t bd = smem_desc_sw128(smem_u32(tiles + sv * kVStageBytes), kChunkBytes, 1024);
@@ -480,26 +508,31 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
       }
     }
   } else if (score) {
-    // ---- softmax: warp (quadrant q4, half h) owns rows 32 q4 .. and page h of every tile.  No early exit: the warps
-    // meet at named barriers, and after a timeout every wait returns at once.
+    // ---- softmax: two groups of four warps take the tiles in turn, group h those of S buffer h; warp (quadrant q4)
+    // owns rows 32 q4 .. of both pages.  While one group waits for tensor memory, barriers or its copy, the other has
+    // the SM's exponentials.  The reference maximum passes from tile to tile, so from group to group, through
+    // m_sh and a pair of named barriers.  No early exit: after a timeout every wait returns at once.
     const int q4 = warp & 3, h = (warp - 4) >> 2;
     const int r = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t mate = 2 + side;                       // the value CTA of these rows
-    const uint32_t pslot_remote = mapa(smem_u32(tiles + kPOff), mate), pfull_remote = mapa(bar(B_PFULL), mate);
     const uint32_t statl_remote = mapa(smem_u32(&sm.stat_l[0]), mate), statm_remote = mapa(smem_u32(&sm.stat_m[0]), mate);
     const uint32_t statsfull_remote = mapa(bar(B_STATSFULL), mate);
     const uint32_t sempty = mapa(bar(B_SEMPTY), 0), qready = mapa(bar(B_QREADY), 0);
     unsigned char *stgp = tiles + kStgOff + h * kPSlotBytes;
     unsigned char *stga = stgp + kPBytes;
-    uint32_t ns = 0, np = 0, uc = 0;
+    unsigned char *prow = stgp + 4096 * q4 + (lane >> 3) * 1024 + (lane & 7) * 128;
+    uint32_t ns = 0, nst = 0, uc = 0;                     // nst: pages staged by this group
+    // This warp's part of the staging tile may be written once the previous copy out of it has been read.
+    auto staging_free = [&]() {
+      if (nst > 0) waitw(sm, bar(B_STGEMPTY + h), (nst - 1) & 1, p.dev_status);
+    };
     while (it.next(p)) {
       // Queries of the unit: latent dims 256 h .. of the warp's rows into tensor memory, coalesced through the warp's
-      // part of the P staging tile (whose last copy must have been read); half 0 also stages the RoPE dims.  The last
-      // S of the previous unit has been read, so its MMAs are complete.
+      // part of the P staging tile (whose last copy must have been read); half 0 also stages the RoPE dims.  Both
+      // groups have read the last S of the previous unit, so its MMAs are complete.
       {
-        if (q4 == 0 && lane == 0) bulk_wait_read_all();
-        asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
+        staging_free();
         unsigned char *stg_w = stgp + q4 * 4096;
         const int j = lane & 7;
         const uint4 *rowp[8];
@@ -550,99 +583,116 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(qready);
       }
-      float m_ref = -CUDART_INF_F, l = 0.f;
+      float m_mine = -CUDART_INF_F, l = 0.f;   // l: this group's row sum, relative to m_mine
+      const uint32_t ns_end = ns + (uint32_t)(it.t1 - it.t0);
       for (int t = it.t0; t < it.t1; ++t, ++ns) {
+        if ((int)(ns & 1) != h) continue;   // the other group's
         const int npg = min(2, it.un.pages - 2 * t);
-        const uint32_t sbuf = ns & 1;
-        waitw(sm, bar(B_SFULL + sbuf), (ns >> 1) & 1, p.dev_status);
+        waitw(sm, bar(B_SFULL + h), (ns >> 1) & 1, p.dev_status);
         tc_fence_after();
-        const uint32_t scol = tbase + lane_off + kSCol + 128 * sbuf + 64 * h;
-        auto release_s = [&]() {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_light(sempty + 8 * sbuf);
-        };
+        const uint32_t scol = tbase + lane_off + kSCol + 128 * h;
+        uint32_t v[2][32];            // 64 scores of this row: one page
         float mx = -CUDART_INF_F;
-        if (h < npg) {
-#pragma unroll 1
-          for (int c2 = 0; c2 < 2; ++c2) {
-            uint32_t v[32];
-            tmem_ld32(scol + 32 * c2, v);
-            tmem_wait_ld();
+        auto load_page = [&](int pg) {
+          tmem_ld32(scol + 64 * pg, v[0]);
+          tmem_ld32(scol + 64 * pg + 32, v[1]);
+        };
+        auto page_max = [&]() {
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) mx = max3f(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+          for (int k = 0; k < 32; k += 2) {
+            mx = max3f(mx, __uint_as_float(v[0][k]), __uint_as_float(v[0][k + 1]));
+            mx = max3f(mx, __uint_as_float(v[1][k]), __uint_as_float(v[1][k + 1]));
           }
-        } else {
-          release_s();   // no page here
+        };
+        // The second page only for its maximum (it is read again below), the first one to stay.
+        if (npg == 2) {
+          load_page(1);
+          tmem_wait_ld();
+          page_max();
         }
+        load_page(0);
+        tmem_wait_ld();
+        page_max();
         mx *= p.scale_log2;
-        sm.xmax[ns & 1][h][r] = mx;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        mx = fmaxf(mx, sm.xmax[ns & 1][h ^ 1][r]);
-        float alpha = 1.f;
-        const bool need = mx > m_ref + kRescaleLog2;
-        if (need) {
-          alpha = exp2f(m_ref - mx);
-          l *= alpha;
-          m_ref = mx;
+        // The reference after the previous tile, and this tile's for the next one.
+        float m_prev = -CUDART_INF_F;
+        if (t != it.t0) {
+          asm volatile("bar.sync %0, 256;" ::"r"(5 - h) : "memory");
+          m_prev = sm.m_sh[h ^ 1][r];
         }
-        if (h < npg) {
-          const uint32_t pn = np + h;
-          const int pb = pn % kPSlots;
-          const bool sender = q4 == 0 && lane == 0;
-          if (sender) bulk_wait_read_all();   // the staging tile's previous copy has been read
-          asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
-          unsigned char *prow = stgp + 4096 * q4 + (lane >> 3) * 1024 + (lane & 7) * 128;
-          float psum0 = 0.f, psum1 = 0.f;
-#pragma unroll 1
-          for (int c2 = 0; c2 < 2; ++c2) {
-            uint32_t v[32];
-            tmem_ld32(scol + 32 * c2, v);
-            tmem_wait_ld();
-            if (c2 == 1) release_s();
+        const bool need = mx > m_prev + kRescaleLog2;
+        const float m_ref = need ? mx : m_prev;
+        const float alpha = need ? exp2f(m_prev - mx) : 1.f;
+        sm.m_sh[h][r] = m_ref;
+        asm volatile("bar.arrive %0, 256;" ::"r"(4 + h) : "memory");
+        if (m_mine != m_ref) {
+          l *= exp2f(m_mine - m_ref);   // m_mine = -inf: l is 0
+          m_mine = m_ref;
+        }
+        const unsigned moved = __ballot_sync(0xffffffffu, need && t != it.t0);
+        float psum0 = 0.f, psum1 = 0.f;
+        uint32_t pk[32];              // this row's 64 P values of a page
+        auto page_p = [&]() {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t pk[4];
+          for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int k = 8 * c + 2 * e;
-                const float p0 = exp2f(__uint_as_float(v[k]) * p.scale_log2 - m_ref);
-                const float p1 = exp2f(__uint_as_float(v[k + 1]) * p.scale_log2 - m_ref);
-                pk[e] = pack_bf16x2(p0, p1);
-                psum0 += p0;
-                psum1 += p1;
-              }
-              *reinterpret_cast<uint4 *>(prow + (((4 * c2 + c) ^ (lane & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = exp2f(__uint_as_float(v[c2][2 * e]) * p.scale_log2 - m_ref);
+              const float p1 = exp2f(__uint_as_float(v[c2][2 * e + 1]) * p.scale_log2 - m_ref);
+              pk[16 * c2 + e] = pack_bf16x2(p0, p1);
+              psum0 += p0;
+              psum1 += p1;
             }
-          }
-          l += psum0 + psum1;
-          // The first page of a tile carries its rows' rescale factors.
+        };
+        // The first page of a tile carries its rows' rescale factors.
+        auto stage = [&](float factor, bool flag) {
+          staging_free();
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4 *>(prow + ((c ^ (lane & 7)) << 4)) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
           float *pa = reinterpret_cast<float *>(stga) + q4 * kPaWords;
-          pa[lane] = h == 0 ? alpha : 1.f;
-          const unsigned moved = __ballot_sync(0xffffffffu, need && h == 0 && t != it.t0);
-          if (lane < 4) reinterpret_cast<uint32_t *>(pa + 32)[lane] = (lane == 0 && moved) ? 1u : 0u;
+          pa[lane] = factor;
+          if (lane < 4) reinterpret_cast<uint32_t *>(pa + 32)[lane] = (lane == 0 && flag) ? 1u : 0u;
           fence_proxy_async_smem();
-          asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
-          if (sender && (pn < kPSlots || wait1(sm, bar(B_PEMPTY + pb), ((pn / kPSlots) - 1) & 1, p.dev_status))) {
-            bulk_copy_to_peer(pslot_remote + pb * kPSlotBytes, smem_u32(stgp), kPTxBytes, pfull_remote + 8 * pb);
-            bulk_commit();
-          }
+          ++nst;
+        };
+        page_p();
+        load_page(1);                 // in flight while the first page is staged (unused columns where there is no page)
+        stage(alpha, moved != 0);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(B_STGFULL + h));
+          mbar_arrive_cluster_light(sempty + 8 * h);   // the last read of this S is done
         }
-        np += npg;
+        if (npg == 2) {
+          page_p();
+          stage(1.f, false);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_STGFULL + h));
+        }
+        l += psum0 + psum1;
       }
-      sm.xl[h][r] = l;
+      // Row statistics of the run: the group that did not have the last tile passes its sum on, relative to the final
+      // reference; the other one sends the total.
+      const bool last = (int)((ns_end - 1) & 1) == h;
+      if (!last) {
+        asm volatile("bar.sync %0, 256;" ::"r"(5 - h) : "memory");
+        const float m_end = sm.m_sh[h ^ 1][r];
+        sm.xl[r] = l > 0.f ? l * exp2f(m_mine - m_end) : 0.f;
+      }
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (h == 0) {
-        l += sm.xl[1][r];
+      if (last) {
+        l += sm.xl[r];
         if (uc > 0) waitw(sm, bar(B_STATSEMPTY), (uc - 1) & 1, p.dev_status);
         st_cluster_f32(statl_remote + r * 4, l);
-        st_cluster_f32(statm_remote + r * 4, m_ref);
+        st_cluster_f32(statm_remote + r * 4, m_mine);
         mbar_arrive_cluster(statsfull_remote);
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");   // xl may be used again
+      asm volatile("bar.sync 1, 256;" ::: "memory");   // xl and m_sh may be used again
       ++uc;
     }
-    if (lane == 0) bulk_wait_all();
   } else {
     // ---- epilogue warps: group g owns O columns 256 g ..; warp w owns rows 32 (w & 3) ...
     const int g = (warp - 4) >> 2;
