@@ -218,18 +218,17 @@ AbsorbedLayout absorbed_layout(const mla_dims *d, int d_cq, int B, int n_q, int 
 // Decode over shared prefixes (tensor-core shapes): the absorbed queries, the plan, and the partials of the sequences'
 // own keys followed by those of the shared ones.
 struct SharedLayout {
-  size_t q_off, head_off, cluster_off, units_off, segs_off, begin_off, seq_off, pages_off, info_off, o_off, lse_off, total;
-  int shared_segs;
+  size_t q_off, head_off, cluster_off, units_off, parts_off, seq_off, begin_off, pages_off, o_off, lse_off, total;
 };
 
 SharedLayout shared_layout(const mla_dims *d, int B, int n_q, int num_groups) {
   SharedLayout L{};
   const int R = n_q * d->n_heads;
-  const int units = shared_max_units(B, R, num_groups);
+  const int shared = shared_max_units(B, R, num_groups);
   const int C = shared_clusters_for_device();
   const int clusters = C > 0 ? C : kSharedMaxClusters;
-  L.shared_segs = units + clusters;
-  const size_t rows = (size_t)tc_own_segments(*d, B, n_q) * 128 + (size_t)L.shared_segs * 256;
+  // A list of n units cut at most clusters - 1 times leaves at most n + clusters - 1 partials.
+  const size_t rows = (size_t)(B + clusters) * R + (size_t)(shared + clusters) * kSharedUnitRows;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -239,12 +238,11 @@ SharedLayout shared_layout(const mla_dims *d, int B, int n_q, int num_groups) {
   L.q_off = take((size_t)B * R * (d->d_c + d->d_rope) * 2);
   L.head_off = take(16);
   L.cluster_off = take((size_t)clusters * sizeof(int));
-  L.units_off = take((size_t)units * sizeof(SharedUnit));
-  L.segs_off = take((size_t)units * sizeof(int2));
-  L.begin_off = take((size_t)B * sizeof(int));
+  L.units_off = take((size_t)(B + shared) * sizeof(SharedUnit));
+  L.parts_off = take((size_t)(B + shared) * sizeof(int2));
   L.seq_off = take((size_t)B * sizeof(int2));
+  L.begin_off = take((size_t)B * sizeof(int));
   L.pages_off = take((size_t)num_groups * sizeof(int));
-  L.info_off = take(tc_seg_info_bytes(*d, B, n_q));
   L.o_off = take(rows * d->d_c * 2);
   L.lse_off = take(rows * sizeof(float));
   L.total = off;
@@ -452,30 +450,25 @@ int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *q_nope, 
     return MLA_ERR_INVALID_ARG;
   char *ws = static_cast<char *>(workspace);
   void *qbuf = ws + L.q_off;
-  const int own_segs = tc_own_segments(*dims, B, n_q);
   const SharedPlan pl{reinterpret_cast<int *>(ws + L.head_off), reinterpret_cast<int *>(ws + L.cluster_off),
-                      reinterpret_cast<SharedUnit *>(ws + L.units_off), reinterpret_cast<int2 *>(ws + L.segs_off),
-                      reinterpret_cast<int *>(ws + L.begin_off), reinterpret_cast<int2 *>(ws + L.seq_off),
+                      reinterpret_cast<SharedUnit *>(ws + L.units_off), reinterpret_cast<int2 *>(ws + L.parts_off),
+                      reinterpret_cast<int2 *>(ws + L.seq_off), reinterpret_cast<int *>(ws + L.begin_off),
                       reinterpret_cast<int *>(ws + L.pages_off)};
-  const TcBuffers buf{reinterpret_cast<int *>(ws + L.info_off), reinterpret_cast<__nv_bfloat16 *>(ws + L.o_off),
-                      reinterpret_cast<float *>(ws + L.lse_off)};
+  __nv_bfloat16 *o_part = reinterpret_cast<__nv_bfloat16 *>(ws + L.o_off);
+  float *lse_part = reinterpret_cast<float *>(ws + L.lse_off);
   const CacheView cv{c_kv, k_pe, dims->ckv_stride, dims->kpe_stride, block_table, max_blocks_per_seq, num_blocks,
                      dims->block_size, dims->cache_layout, dims->d_c, dims->d_c + dims->d_rope};
-  // (1) Who shares what, (2) the latent queries, (3) the shared keys for all rows of a group, (4) every sequence's
-  // own keys, (5) the merge and W_UV.
-  if ((rc = launch_shared_plan(pl, B, n_q, dims->n_heads, max_seqlen, dims->block_size, num_groups, group_offsets, prefix_lens,
-                               seqlens, dev_status, st)))
+  // (1) Who shares what and which cluster does what, (2) the latent queries, (3) the shared keys for all rows of a
+  // group and every sequence's own keys, (4) the merge of the partials and W_UV.
+  if ((rc = launch_shared_plan(pl, B, n_q, dims->n_heads, max_seqlen, dims->block_size, num_groups, group_offsets,
+                               prefix_lens, seqlens, dev_status, st)))
     return rc;
   const AbsorbArgs ab{B, n_q, dims->n_heads, dims->d_c, dims->d_rope, dims->d_nope,
                       q_nope, q_pe, w_uk, seqlens, qbuf, dims->rope_base};
   if ((rc = absorb_dispatch(ab, true, dev_status, st))) return rc;
-  if ((rc = launch_shared_attention(*dims, pl, qbuf, cv, buf.o_part + (size_t)own_segs * 128 * dims->d_c,
-                                    buf.lse_part + (size_t)own_segs * 128, dev_status, st)))
-    return rc;
-  if ((rc = launch_tc_attention_own(*dims, B, n_q, qbuf, cv, seqlens, max_seqlen, pl.own_begin, buf, dev_status, st)))
-    return rc;
-  return launch_tc_combine_shared(*dims, B, n_q, buf, pl.seq_unit, pl.unit_segs, L.shared_segs, w_uv, out, lse, dev_status,
-                                  st);
+  if ((rc = launch_shared_attention(*dims, pl, qbuf, cv, o_part, lse_part, dev_status, st))) return rc;
+  const SharedPieces pc{o_part, lse_part, pl.unit_parts, pl.seq_group, n_q, dims->n_heads};
+  return launch_tc_combine_shared(*dims, B, n_q, pc, w_uv, out, lse, dev_status, st);
 }
 
 // What the two bookkeeping calls check alike.

@@ -163,15 +163,6 @@ struct TcParams {
   const unsigned char *tiled;        // tiled page pool (pages move by bulk copy), or NULL: row pool via TMA maps
   const unsigned char *row_pool;     // row pool base (c_kv) for L2 prefetch
   int rows_contig;                   // row pool with fused 576-wide rows: a page is 73728 contiguous bytes
-  static constexpr bool kOwn = false;
-  __device__ __forceinline__ int begin(int) const { return kv_begin; }
-};
-
-// Every sequence begins at its own key (a multiple of 64): the keys before it are attended to elsewhere.
-struct TcOwnParams : TcParams {
-  const int *own_begin;              // [B], written by an earlier kernel on the stream
-  static constexpr bool kOwn = true;
-  __device__ __forceinline__ int begin(int b) const { return own_begin[b]; }
 };
 
 __device__ __forceinline__ int seq_len_clamped(const TcParams &p, int b) {
@@ -185,10 +176,9 @@ __device__ __forceinline__ int key_end(const TcParams &p, int b) {
   return S < p.kv_end ? S : p.kv_end;
 }
 
-// Tiles (64-key pages) of a unit inside the key range; tile t holds keys begin + 64 t ...
-template <typename P>
-__device__ __forceinline__ int unit_tiles(const P &p, int u) {
-  const int e = key_end(p, u / p.n_rb) - p.begin(u / p.n_rb);
+// Tiles (64-key pages) of a unit inside the key range; tile t holds keys kv_begin + 64 t ...
+__device__ __forceinline__ int unit_tiles(const TcParams &p, int u) {
+  const int e = key_end(p, u / p.n_rb) - p.kv_begin;
   return e > 0 ? (e + kTileKeys - 1) / kTileKeys : 0;
 }
 
@@ -213,8 +203,7 @@ __device__ __forceinline__ int cluster_of(long long t, int k, const Split &sp) {
 
 // Warp-level plan: total tiles and cost, this cluster's tile range, its first unit and the tile,
 // non-empty-unit and segment prefixes of that unit.  Every CTA computes the same values.
-template <typename P>
-__device__ __forceinline__ void make_plan(const P &p, SmemB &sb, int cid, int C) {
+__device__ __forceinline__ void make_plan(const TcParams &p, SmemB &sb, int cid, int C) {
   const int lane = threadIdx.x & 31;
   long long total = 0;
   int une = 0;
@@ -319,8 +308,7 @@ struct SegIter {
   int u, prefix, seg_prefix, k;   // k: non-empty units before u
   long long pos, end;
   Split sp;
-  template <typename P>
-  __device__ __forceinline__ bool next(const P &p, int cid, int &b, int &rb, int &t0, int &t1, int &segid, bool &first_of_unit,
+  __device__ __forceinline__ bool next(const TcParams &p, int cid, int &b, int &rb, int &t0, int &t1, int &segid, bool &first_of_unit,
                        int &nseg_unit) {
     while (pos < end && u < p.U) {
       const int nt = unit_tiles(p, u);
@@ -399,9 +387,8 @@ __device__ __forceinline__ bool warp_wait(SmemB &sb, uint32_t bar, uint32_t pari
   return ok != 0;
 }
 
-template <typename P>
-__device__ __forceinline__ int64_t tile_row(const P &p, int b, int t) {
-  const int key = p.begin(b) + t * kTileKeys;
+__device__ __forceinline__ int64_t tile_row(const TcParams &p, int b, int t) {
+  const int key = p.kv_begin + t * kTileKeys;
   const int lb = key / p.block_size;
   if (lb >= p.max_blocks_per_seq) return -1;
   const int blk = p.block_table ? p.block_table[(int64_t)b * p.max_blocks_per_seq + lb]
@@ -416,14 +403,12 @@ __device__ __forceinline__ int64_t tile_row(const P &p, int b, int t) {
 struct PageRows {
   int b = -1, base = 0;
   int64_t r0 = -1, r1 = -1;
-  template <typename P>
-  __device__ __forceinline__ void load(const P &p) {
+  __device__ __forceinline__ void load(const TcParams &p) {
     const int lane = threadIdx.x & 31;
     r0 = tile_row(p, b, base + lane);
     r1 = tile_row(p, b, base + 32 + lane);
   }
-  template <typename P>
-  __device__ __forceinline__ int64_t get(const P &p, int seq, int page) {
+  __device__ __forceinline__ int64_t get(const TcParams &p, int seq, int page) {
     if (seq != b || page < base || page >= base + 96) {
       b = seq;
       base = page;
@@ -438,10 +423,9 @@ struct PageRows {
   }
 };
 
-template <typename P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_pe,
-                     const __grid_constant__ P p) {
+                     const __grid_constant__ TcParams p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   SmemB &sb = *reinterpret_cast<SmemB *>(tiles + kRegionA);
@@ -479,7 +463,6 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
     tmem_alloc(smem_u32(&sb.tmem_base), 512);
     tmem_relinquish();
   }
-  if (P::kOwn) grid_dep_wait();   // the plan needs own_begin
   if (warp == 0) make_plan(p, sb, cid, C);
   if (threadIdx.x == 32 && !p.tiled) {
     tma_prefetch_desc(&map_c);
@@ -681,7 +664,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
       bool ok = true;
       while (ok && it.next(p, cid, b, rb, t0, t1, segid, first_u, nseg)) {
         if (uc > 0 && !wait_or_abort(sb, bar(B_OFREE), (uc - 1) & 1, p.dev_status, false, p.timeout_rec, __LINE__)) break;
-        const int S = seq_len_clamped(p, b), kb = p.begin(b);
+        const int S = seq_len_clamped(p, b);
         for (int t = t0; t < t1; ++t, n += 2, ++np) {
           sb.prog[warp] = (int)n;
           const int pb = np % kPSlots;
@@ -691,7 +674,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
             ok = false;
             break;
           }
-          const bool tail = kb + (t + 1) * kTileKeys > S;
+          const bool tail = p.kv_begin + (t + 1) * kTileKeys > S;
           const uint32_t fa = slot_factors(smem_u32(tiles), pb);
           const bool resc = t != t0 && (ld_shared_u32(fa + 4 * 32) | ld_shared_u32(fa + 4 * (kPaWords + 32)) |
                                         ld_shared_u32(fa + 4 * (2 * kPaWords + 32)) |
@@ -706,7 +689,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
             // halves: the slot's P.V barrier counts both issuers) must have completed.
             if (resc && !wait_or_abort(sb, bar(B_PVDONE + (np - 1) % kPSlots), ((np - 1) / kPSlots) & 1, p.dev_status,
                                        false, p.timeout_rec, __LINE__)) { ok = false; break; }
-            sb.req[hv] = Req{0, sv, pb, S - kb - t * kTileKeys, tail ? 1 : 0, resc ? 1 : 0, 0, 0, 0};
+            sb.req[hv] = Req{0, sv, pb, S - p.kv_begin - t * kTileKeys, tail ? 1 : 0, resc ? 1 : 0, 0, 0, 0};
             mbar_arrive(bar(B_REQ + hv));
             if (!wait_or_abort(sb, bar(B_REQDONE + hv), nfix & 1, p.dev_status, false, p.timeout_rec, __LINE__)) { ok = false; break; }
             ++nfix;
@@ -839,7 +822,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
         const int S = seq_len_clamped(p, b);
         const int j = real ? gr / p.H : 0;
         // Keys this row may see, counted from the key range's first key.
-        const int vis_end = (real ? min(S - p.n_q + j + 1, p.kv_end) : 0) - p.begin(b);
+        const int vis_end = (real ? min(S - p.n_q + j + 1, p.kv_end) : 0) - p.kv_begin;
         float m_ref = -CUDART_INF_F, l = 0.f;
         for (int T = t0; T < t1; T += kSuper, ++ns) {
           if (lane == 0) sb.prog[warp] = (int)np;
@@ -1177,38 +1160,29 @@ struct Pieces {
   const float *lse;            // one log-sum-exp per row of `part`
   const int *seg_info;         // [units][2], or NULL for stacked partials
   int n_q, H, n_rb, max_segs, n_parts;
-  static constexpr bool kShared = false;
 };
 
-// With the pieces of a shared prefix behind those of the sequence's own keys: the group's rows are cut into units of
-// 256, unit u's pieces are the segments unit_segs[u] = (first, count) of 256 rows each, from row `shared_row` on.
-struct SharedPieces : Pieces {
-  const int2 *seq_unit;        // [B]: first unit of the sequence's group (-1: none), the group's first query row
-  const int2 *unit_segs;
-  int64_t shared_row;
-  int max_shared_segs;
-  static constexpr bool kShared = true;
-};
-constexpr int kSharedRows = 256;
-
-// The pieces of one output row: `own` rows from `first` on, `stride` apart, then rows from `first2` on, 256 apart.
+// The pieces of one output row: ns rows from `first` on, `stride` apart; with a shared prefix, `own` such rows of the
+// sequence's own keys, then rows from `first2` on, `stride2` apart, of the shared ones.
 struct PieceRows {
+  int ns = 0;
+  int64_t first = 0, stride = 0;
+  __device__ __forceinline__ int64_t at(int k) const { return first + k * stride; }
+};
+struct SharedPieceRows {
   int ns = 0, own = 0;
-  int64_t first = 0, stride = 0, first2 = 0;
-  template <bool kShared>
+  int64_t first = 0, stride = 0, first2 = 0, stride2 = 0;
   __device__ __forceinline__ int64_t at(int k) const {
-    if (kShared && k >= own) return first2 + (int64_t)(k - own) * kSharedRows;
-    return first + k * stride;
+    return k < own ? first + k * stride : first2 + (k - own) * stride2;
   }
 };
 
-template <typename P>
-__device__ __forceinline__ PieceRows piece_rows(const P &pc, int rows, int g, int s) {
+__device__ __forceinline__ PieceRows piece_rows(const Pieces &pc, int rows, int g, int s) {
   PieceRows r;
   if (!pc.seg_info) {
     r.first = (int64_t)g * pc.H + s;
     r.stride = (int64_t)rows * pc.H;
-    r.ns = r.own = pc.n_parts;
+    r.ns = pc.n_parts;
     return r;
   }
   const int b = g / pc.n_q, j = g % pc.n_q;
@@ -1219,31 +1193,39 @@ __device__ __forceinline__ PieceRows piece_rows(const P &pc, int rows, int g, in
   if (s0 >= 0 && s0 + ns <= pc.max_segs) {
     r.first = (int64_t)s0 * kRows + gr % kRows;
     r.stride = kRows;
-    r.ns = r.own = ns;
-  }
-  if constexpr (P::kShared) {
-    const int2 su = pc.seq_unit[b];
-    if (su.x >= 0) {
-      const int q = g * pc.H + s - su.y;   // row within the group
-      const int2 sg = pc.unit_segs[su.x + q / kSharedRows];
-      if (sg.x >= 0 && sg.y > 0 && sg.x + sg.y <= pc.max_shared_segs) {
-        r.first2 = pc.shared_row + (int64_t)sg.x * kSharedRows + q % kSharedRows;
-        r.ns += sg.y;
-      }
-    }
+    r.ns = ns;
   }
   return r;
 }
 
-// As tc_merge_kernel, with the pieces of a shared prefix.
+// The plan's own units of n_q * H rows come first, then its shared units of kSharedUnitRows.
+__device__ __forceinline__ SharedPieceRows piece_rows(const SharedPieces &pc, int, int g, int s) {
+  SharedPieceRows r;
+  const int b = g / pc.n_q, R = pc.n_q * pc.H;
+  const int2 ou = pc.unit_parts[b];
+  r.first = ou.x + (g * pc.H + s - b * R);
+  r.stride = R;
+  r.ns = r.own = ou.y;
+  const int2 su = pc.seq_group[b];
+  if (su.x >= 0) {
+    const int q = g * pc.H + s - su.y;   // row within the group
+    const int2 sp = pc.unit_parts[su.x + q / kSharedUnitRows];
+    r.first2 = sp.x + q % kSharedUnitRows;
+    r.stride2 = kSharedUnitRows;
+    r.ns += sp.y;
+  }
+  return r;
+}
+
+// As tc_merge_kernel, for the partials of a decode over shared prefixes.
 __global__ void __launch_bounds__(kMergeThreads)
 shared_merge_kernel(const SharedPieces pc, int rows, __nv_bfloat16 *o_lat, float *lse_out) {
   sm100::grid_dep_launch();
   sm100::grid_dep_wait();
   const int64_t item = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
   if (item >= (int64_t)rows * pc.H) return;
-  const PieceRows pr = piece_rows(pc, rows, (int)(item / pc.H), (int)(item % pc.H));
-  merge_row(threadIdx.x & 31, pr.ns, pc.part, pc.lse, [&](int k) { return pr.at<true>(k); }, o_lat + item * kDc,
+  const SharedPieceRows pr = piece_rows(pc, rows, (int)(item / pc.H), (int)(item % pc.H));
+  merge_row(threadIdx.x & 31, pr.ns, pc.part, pc.lse, [&](int k) { return pr.at(k); }, o_lat + item * kDc,
             lse_out ? lse_out + item : nullptr);
 }
 
@@ -1297,13 +1279,14 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int row
   {
     // Merge of row rr (output row g = g0 + rr); rows past the end become zero rows of the tile.
     const int rr = tid >> 2, q = tid & 3, g = g0 + rr;
-    const PieceRows pr = g < rows ? piece_rows(pc, rows, g, s) : PieceRows();
+    decltype(piece_rows(pc, rows, g, s)) pr;
+    if (g < rows) pr = piece_rows(pc, rows, g, s);
     const int ns = pr.ns;
     float m = -CUDART_INF_F;
-    for (int k = 0; k < ns; ++k) m = fmaxf(m, pc.lse[pr.at<P::kShared>(k)]);
+    for (int k = 0; k < ns; ++k) m = fmaxf(m, pc.lse[pr.at(k)]);
     float sum = 0.f;
     if (m != -CUDART_INF_F)
-      for (int k = 0; k < ns; ++k) sum += __expf(pc.lse[pr.at<P::kShared>(k)] - m);
+      for (int k = 0; k < ns; ++k) sum += __expf(pc.lse[pr.at(k)] - m);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
     for (int hh = 0; hh < 2; ++hh) {
@@ -1319,7 +1302,7 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int row
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
           const bool have = k0 + kk < ns;
-          const int64_t prow = pr.at<P::kShared>(have ? k0 + kk : 0);
+          const int64_t prow = pr.at(have ? k0 + kk : 0);
           const __nv_bfloat16 *src = pc.part + prow * kDc;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -1477,13 +1460,11 @@ int clusters_for_device() {
   if (const int c = cached[dev].load(std::memory_order_acquire)) return c;
   std::lock_guard<std::mutex> lock(mu);
   if (const int c = cached[dev].load(std::memory_order_acquire)) return c;
-  const auto kernel = mla_decode_tc_kernel<TcParams>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) ||
-      cudaFuncSetAttribute(mla_decode_tc_kernel<TcOwnParams>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes))
+  if (cudaFuncSetAttribute(mla_decode_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes))
     return 0;
   // One CTA of kThreads per SM needs at most kLaunchRegs registers per thread.
   cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs > kLaunchRegs) return 0;
+  if (cudaFuncGetAttributes(&fa, mla_decode_tc_kernel) != cudaSuccess || fa.numRegs > kLaunchRegs) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * kMaxClusters);
   cfg.blockDim = dim3(kThreads);
@@ -1496,7 +1477,7 @@ int clusters_for_device() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, mla_decode_tc_kernel, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     int sms = 0;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1522,18 +1503,17 @@ size_t tc_decode_workspace_bytes(const mla_dims &d, int B, int n_q) {
   return ws_layout(B, n_rb).total;
 }
 
-namespace {
-
-// The attention over [begin, kv_end) of every sequence: begin = kv_begin, or own_begin[b] when given.
-int launch_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
-                     const int32_t *seqlens, int max_seqlen, const TcBuffers &buf, int *dev_status, cudaStream_t st,
-                     int kv_begin, int kv_end, const int *own_begin) {
+int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
+                        const int32_t *seqlens, int max_seqlen, void *ws, int *dev_status, cudaStream_t st,
+                        int kv_begin, int kv_end) {
   if (kv_begin < 0 || kv_begin % kTileKeys) return MLA_ERR_INVALID_ARG;
   const bool tiled = cache.layout == MLA_CACHE_TILED;
   if ((reinterpret_cast<uintptr_t>(cache.c_kv) & 15) || (!tiled && (reinterpret_cast<uintptr_t>(cache.k_pe) & 15)) ||
       (reinterpret_cast<uintptr_t>(q_abs) & 15))
     return MLA_ERR_INVALID_ARG;
   const int n_rb = (n_q * d.n_heads + kRows - 1) / kRows;
+  const WsLayout L = ws_layout(B, n_rb);
+  char *w = static_cast<char *>(ws);
   CUtensorMap mc, mpe;
   memset(&mc, 0, sizeof(mc));
   memset(&mpe, 0, sizeof(mpe));
@@ -1545,7 +1525,7 @@ int launch_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const
   }
   const int C = clusters_for_device();
   if (C <= 0) return MLA_ERR_CUDA;
-  TcOwnParams p;
+  TcParams p;
   p.B = B;
   p.n_q = n_q;
   p.H = d.n_heads;
@@ -1563,14 +1543,13 @@ int launch_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const
   p.row_pool = static_cast<const unsigned char *>(cache.c_kv);
   p.rows_contig = !tiled && cache.ckv_stride == kW && cache.kpe_stride == kW &&
                   static_cast<const char *>(cache.k_pe) == static_cast<const char *>(cache.c_kv) + 2 * kDc;
-  p.o_part = buf.o_part;
-  p.lse_part = buf.lse_part;
-  p.seg_info = buf.seg_info;
+  p.o_part = reinterpret_cast<__nv_bfloat16 *>(w + L.o_part);
+  p.lse_part = reinterpret_cast<float *>(w + L.lse_part);
+  p.seg_info = reinterpret_cast<int *>(w + L.seg_info);
   p.timeout_rec = p.seg_info + 2 * p.U;
   p.dev_status = dev_status;
   p.kv_begin = kv_begin;
   p.kv_end = kv_end;
-  p.own_begin = own_begin;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * C);
   cfg.blockDim = dim3(kThreads);
@@ -1581,37 +1560,8 @@ int launch_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = own_begin ? cudaLaunchKernelEx(&cfg, mla_decode_tc_kernel<TcOwnParams>, mc, mpe, p)
-                                  : cudaLaunchKernelEx(&cfg, mla_decode_tc_kernel<TcParams>, mc, mpe,
-                                                       static_cast<const TcParams &>(p));
-  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
-}
-
-}  // namespace
-
-int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
-                        const int32_t *seqlens, int max_seqlen, void *ws, int *dev_status, cudaStream_t st,
-                        int kv_begin, int kv_end) {
-  const WsLayout L = ws_layout(B, (n_q * d.n_heads + kRows - 1) / kRows);
-  char *w = static_cast<char *>(ws);
-  const TcBuffers buf{reinterpret_cast<int *>(w + L.seg_info), reinterpret_cast<__nv_bfloat16 *>(w + L.o_part),
-                      reinterpret_cast<float *>(w + L.lse_part)};
-  return launch_attention(d, B, n_q, q_abs, cache, seqlens, max_seqlen, buf, dev_status, st, kv_begin, kv_end, nullptr);
-}
-
-int tc_own_segments(const mla_dims &d, int B, int n_q) {
-  const int C = clusters_for_device();
-  return B * ((n_q * d.n_heads + kRows - 1) / kRows) + (C > 0 ? C : kMaxClusters);
-}
-
-size_t tc_seg_info_bytes(const mla_dims &d, int B, int n_q) {
-  return ((size_t)B * ((n_q * d.n_heads + kRows - 1) / kRows) * 2 + kTimeoutRecInts) * sizeof(int);
-}
-
-int launch_tc_attention_own(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
-                            const int32_t *seqlens, int max_seqlen, const int *own_begin, const TcBuffers &buf,
-                            int *dev_status, cudaStream_t st) {
-  return launch_attention(d, B, n_q, q_abs, cache, seqlens, max_seqlen, buf, dev_status, st, 0, 0x7fffffff, own_begin);
+  if (cudaLaunchKernelEx(&cfg, mla_decode_tc_kernel, mc, mpe, p) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
 }
 
 namespace {
@@ -1663,18 +1613,10 @@ int launch_tc_combine(const mla_dims &d, int B, int n_q, const int32_t *seqlens,
              : MLA_ERR_CUDA;
 }
 
-int launch_tc_combine_shared(const mla_dims &d, int B, int n_q, const TcBuffers &buf, const int2 *seq_unit,
-                             const int2 *unit_segs, int max_shared_segs, const void *w_uv, void *out, float *lse,
-                             int *dev_status, cudaStream_t st) {
+int launch_tc_combine_shared(const mla_dims &d, int B, int n_q, const SharedPieces &pc, const void *w_uv, void *out,
+                             float *lse, int *dev_status, cudaStream_t st) {
   if (w_uv && (d.d_v != kDv || (reinterpret_cast<uintptr_t>(w_uv) & 15))) return MLA_ERR_UNSUPPORTED;
-  const int rows = B * n_q, max_segs = tc_own_segments(d, B, n_q);
-  SharedPieces pc;
-  static_cast<Pieces &>(pc) = Pieces{buf.o_part, buf.lse_part, buf.seg_info, n_q, d.n_heads,
-                                     (n_q * d.n_heads + kRows - 1) / kRows, max_segs, 0};
-  pc.seq_unit = seq_unit;
-  pc.unit_segs = unit_segs;
-  pc.shared_row = (int64_t)max_segs * kRows;
-  pc.max_shared_segs = max_shared_segs;
+  const int rows = B * n_q;
   if (w_uv) return launch_merge_wuv(d, rows, pc, w_uv, out, lse, dev_status, st);
   const int64_t warps = (int64_t)rows * d.n_heads;
   const dim3 mgrid((unsigned)((warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32)));

@@ -19,23 +19,17 @@ int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, co
 // Merge of the partials, and the W_UV product in the same kernel when w_uv != NULL.
 int launch_tc_combine(const mla_dims &d, int B, int n_q, const int32_t *seqlens, int max_seqlen, const void *w_uv,
                       void *out, float *lse, void *ws, int *dev_status, cudaStream_t st);
-
-// The shared-prefix decode: the attention of every sequence over its own keys from own_begin[b] on (a multiple of 64,
-// read on the device), and the merge of its partials with those of the shared keys.  Partials of the own keys are rows
-// 0 .. 128 tc_own_segments() - 1 of o_part and lse_part, those of the shared keys (256 rows a segment) follow.
-struct TcBuffers {
-  int *seg_info;             // tc_seg_info_bytes()
-  __nv_bfloat16 *o_part;     // [rows][512]
-  float *lse_part;           // [rows]
+// Where the partials of a decode over shared prefixes live (see shared_tc.cuh): row `part` of each piece, by unit.
+constexpr int kSharedUnitRows = 256;
+struct SharedPieces {
+  const __nv_bfloat16 *part;   // rows of 512 bf16
+  const float *lse;
+  const int2 *unit_parts;      // first partial row and number of partials of every unit: own units by sequence first
+  const int2 *seq_group;       // [B]: first shared unit of the sequence's group (-1: none), the group's first query row
+  int n_q, H;
 };
-int tc_own_segments(const mla_dims &d, int B, int n_q);
-size_t tc_seg_info_bytes(const mla_dims &d, int B, int n_q);
-int launch_tc_attention_own(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
-                            const int32_t *seqlens, int max_seqlen, const int *own_begin, const TcBuffers &buf,
-                            int *dev_status, cudaStream_t st);
-int launch_tc_combine_shared(const mla_dims &d, int B, int n_q, const TcBuffers &buf, const int2 *seq_unit,
-                             const int2 *unit_segs, int max_shared_segs, const void *w_uv, void *out, float *lse,
-                             int *dev_status, cudaStream_t st);
+int launch_tc_combine_shared(const mla_dims &d, int B, int n_q, const SharedPieces &pc, const void *w_uv, void *out,
+                             float *lse, int *dev_status, cudaStream_t st);
 // True when stacked partials of this shape merge on the path below (bf16, d_c 512, d_v 128 with
 // W_UV, 16-byte aligned rows).
 bool tc_merge_parts_supported(const mla_dims &d, const void *o_parts, const void *w_uv, const void *out);

@@ -1,12 +1,14 @@
-// Attention of a group's query rows over the keys that its sequences share, on tcgen05 (sm_100a).
+// Decode over shared prefixes: the attention of a group's query rows over the keys that its sequences share, and of
+// every sequence's rows over its own keys, in one launch on tcgen05 (sm_100a).
 //
 // In the absorbed form every head of every sequence attends to the same cached rows [c_i | kpe_i], so over a shared
 // prefix the rows of all sequences of a group are rows of one product,
 //   S = Q [rows x 576] . K^T [576 x keys],   O += P [rows x keys] . C [keys x 512],
 // with no mask (the shared keys end before every query).  2176 FLOPs per (row, key) against 1152 bytes per key and
-// 256 rows: bound by the tensor cores.
+// 256 rows: bound by the tensor cores.  A sequence's own keys are the same product with its n_q * H rows, masked at
+// the end.
 //
-// Shape.  A unit is 256 rows.  A cluster of four CTAs works on one unit at a time, as two pairs that issue M = 256
+// Shape.  A unit is at most 256 rows and the keys that they attend to.  A cluster of four CTAs works on one unit at a time, as two pairs that issue M = 256
 // MMAs (cta_group::2: each CTA holds 128 of the rows and half of the B operand, so each SM pulls half the bytes that
 // a 128-row tile of its own would need; at 128 rows the L2 -> SM path, not the tensor pipe, sets the pace):
 //   * ranks 0, 1 (score pair): Q_lat of the CTA's 128 rows in tensor memory (A operand), Q_rope in shared memory; a
@@ -82,9 +84,9 @@ enum Bar {
   B_STATSEMPTY = B_PEMPTY + kPSlots,    // score: the value CTA has read the row statistics
   B_STGFULL = B_STATSEMPTY + 1,         // score: a page of P is staged, per softmax group
   B_STGEMPTY = B_STGFULL + 2,           // score: its copy has read the staging tile
-  B_VFULL = B_STGEMPTY + 2,              // value: own stage has landed; at rank 2 also: rank 3 has P, C and its O rescaled
-  B_VEMPTY = B_VFULL + kVStages,        // value: the MMAs have read the stage (both CTAs)
-  B_PFULL = B_VEMPTY + kVStages,        // value: a page of P has landed
+  B_CFULL = B_STGEMPTY + 2,             // value: own latents have landed; at rank 2 also: rank 3 is ready for the page
+  B_CEMPTY = B_CFULL + kVStages,        // value: the MMAs have read the stage (both CTAs)
+  B_PFULL = B_CEMPTY + kVStages,        // value: a page of P has landed
   B_PVDONE = B_PFULL + kPSlots,         // value: the page's MMAs are complete (both CTAs)
   B_REQ = B_PVDONE + kPSlots,           // value: request to the epilogue warps
   B_REQDONE = B_REQ + 1,
@@ -94,8 +96,8 @@ enum Bar {
 };
 
 struct Req {
-  int kind;      // 0: rescale O before a page's MMAs, 1: the unit's epilogue
-  int slot, segid, last_slot, last_parity;
+  int kind;      // 0: before a page's MMAs, rescale O and/or zero the latent rows past the last key; 1: the epilogue
+  int rescale, slot, keys, stage, last_slot, last_parity;
 };
 
 struct Small {                          // behind the tiles
@@ -115,7 +117,7 @@ struct Params {
   const SharedUnit *units;
   const __nv_bfloat16 *q;
   const int32_t *block_table;
-  int max_blocks_per_seq, num_blocks, block_size;
+  int max_blocks_per_seq, num_blocks, block_size, H;
   float scale_log2;
   __nv_bfloat16 *o_part;
   float *lse_part;
@@ -177,32 +179,39 @@ __device__ __forceinline__ bool waitw(Small &sm, uint32_t bar, uint32_t parity, 
 }
 
 // ------------------------------------------------------------ work list
-// The (unit, tile) runs of one cluster.
+// The runs of tiles of one cluster: those whose place in the list lies in its share [lo, hi) of the total cost.
 struct Runs {
-  int u, pos, end, cid;
+  int u, units, lo, hi, cid;
   SharedUnit un;
   int t0, t1;       // tiles of the unit in this run
-  __device__ __forceinline__ Runs(const Params &p, int cid_) : u(0), pos(0), end(0), cid(cid_) {
-    const int N = p.head[0], C = p.head[1];
-    if (cid < C) {
-      pos = (int)((int64_t)cid * N / C);
-      end = (int)((int64_t)(cid + 1) * N / C);
+  __device__ __forceinline__ Runs(const Params &p, int cid_) : u(0), units(0), lo(0), hi(0), cid(cid_) {
+    const int4 h = *reinterpret_cast<const int4 *>(p.head);
+    if (cid < h.y) {
+      lo = (int)((int64_t)cid * h.x / h.y);
+      hi = (int)((int64_t)(cid + 1) * h.x / h.y);
+      units = h.z;
       u = p.cluster_unit[cid];
     }
   }
   __device__ __forceinline__ bool next(const Params &p) {
-    if (pos >= end) return false;
-    const int4 *src = reinterpret_cast<const int4 *>(p.units + u);
-    const int4 a = src[0], b = src[1];
-    un.tile0 = a.x; un.tiles = a.y; un.pages = a.z; un.seq = a.w;
-    un.row0 = b.x; un.rows = b.y;
-    t0 = pos - un.tile0;
-    t1 = min(end - un.tile0, un.tiles);
-    pos = un.tile0 + t1;
-    ++u;
-    return true;
+    for (; u < units; ++u) {
+      const int4 *src = reinterpret_cast<const int4 *>(p.units + u);
+      const int4 a = src[0], b = src[1], c = src[2];
+      un.cost0 = a.x; un.tiles = a.y; un.pages = a.z; un.seq = a.w;
+      un.row0 = b.x; un.rows = b.y; un.page0 = b.z; un.keys = b.w;
+      un.part0 = c.x; un.part_stride = c.y; un.vis0 = c.z;
+      if (un.cost0 >= hi) break;
+      t0 = max(lo - un.cost0, 0);
+      t1 = min(hi - un.cost0, un.tiles);
+      if (t0 < t1) {
+        ++u;
+        return true;
+      }
+    }
+    u = units;
+    return false;
   }
-  __device__ __forceinline__ int seg() const { return u - 1 + cid; }   // u and cid only rise along the list
+  __device__ __forceinline__ int part_row() const { return un.part0 + cid * un.part_stride; }
   __device__ __forceinline__ int pages_end() const { return min(2 * t1, un.pages); }
 };
 
@@ -255,7 +264,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
       uint32_t n = 1;
       if (i == B_QREADY || i == B_OFREE) n = 2 * kSoftWarps;
       if (i >= B_SEMPTY && i < B_SEMPTY + 2) n = kSoftWarps;   // four warps of each CTA
-      if (lead && ((i >= B_KFULL && i < B_KFULL + kKStages) || (i >= B_VFULL && i < B_VFULL + kVStages))) n = 2;
+      if (lead && ((i >= B_KFULL && i < B_KFULL + kKStages) || (i >= B_CFULL && i < B_CFULL + kVStages))) n = 2;
       if (i == B_STATSEMPTY || i == B_REQDONE) n = kSoftWarps;
       if (i >= B_STGFULL && i < B_STGFULL + 2) n = 4;
       if (i == B_STATSFULL) n = kRows;
@@ -289,11 +298,11 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         PageRows pr;
         int ok = 1;
         while (ok && it.next(p)) {
-          pr.start(p, it.un.seq, 2 * it.t0);
+          pr.start(p, it.un.seq, it.un.page0 + 2 * it.t0);
           for (int t = it.t0; ok && t < it.t1; ++t) {
             const int page = 2 * t + (int)side;
             const bool have = page < it.un.pages;
-            int64_t row = pr.get(p, have ? page : 2 * t);
+            int64_t row = pr.get(p, it.un.page0 + (have ? page : 2 * t));
             if (row < 0) {
               if (lane == 0) report(p.dev_status, MLA_ERR_BAD_INDEX);
               row = 0;
@@ -408,22 +417,22 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         PageRows pr;
         int ok = 1;
         while (ok && it.next(p)) {
-          pr.start(p, it.un.seq, 2 * it.t0);
+          pr.start(p, it.un.seq, it.un.page0 + 2 * it.t0);
           for (int g = 2 * it.t0; ok && g < it.pages_end(); ++g, ++n) {
-            int64_t row = pr.get(p, g);
+            int64_t row = pr.get(p, it.un.page0 + g);
             if (row < 0) row = 0;   // reported by the score pair
             const int s = n % kVStages;
             if (lane == 0) {
-              if (n >= kVStages && !wait1(sm, bar(B_VEMPTY + s), (n / kVStages - 1) & 1, p.dev_status)) ok = 0;
+              if (n >= kVStages && !wait1(sm, bar(B_CEMPTY + s), (n / kVStages - 1) & 1, p.dev_status)) ok = 0;
               if (ok) {
                 const uint32_t dst = smem_u32(tiles + s * kVStageBytes);
-                mbar_expect_tx(bar(B_VFULL + s), kVStageBytes);
+                mbar_expect_tx(bar(B_CFULL + s), kVStageBytes);
                 if (p.tiled)
                   bulk_load(dst, p.tiled + (row / kPage) * (9 * kChunkBytes) + side * kVStageBytes, kVStageBytes,
-                            bar(B_VFULL + s));
+                            bar(B_CFULL + s));
                 else
                   for (int c = 0; c < 4; ++c)
-                    tma_load_2d(dst + c * kChunkBytes, &map_c, 256 * (int)side + 64 * c, (int32_t)row, bar(B_VFULL + s));
+                    tma_load_2d(dst + c * kChunkBytes, &map_c, 256 * (int)side + 64 * c, (int32_t)row, bar(B_CFULL + s));
               }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -432,12 +441,12 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         }
         if (lane == 0)
           for (uint32_t i = n > kVStages ? n - kVStages : 0; i < n; ++i)
-            mbar_wait(bar(B_VFULL + i % kVStages), (i / kVStages) & 1, kWaitNs);
+            mbar_wait(bar(B_CFULL + i % kVStages), (i / kVStages) & 1, kWaitNs);
       } else if (warp == 1) {
         // ---- O += P . C.  Both CTAs walk the pages alike: P has landed, O rescaled where the page asks for it, C has
         // landed; rank 3 then reports to rank 2, which issues for both.
         const uint32_t idesc = idesc_bf16_f32(kUnitRows, 256, false, true);
-        const uint32_t ready = mapa(bar(B_VFULL), 2);
+        const uint32_t ready = mapa(bar(B_CFULL), 2);
         uint32_t np = 0, uc = 0, nfix = 0;
         bool ok = true;
         while (ok && it.next(p)) {
@@ -448,24 +457,27 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             if (!(ok = waitw(sm, bar(B_PFULL + pb), ppar, p.dev_status))) break;
             const uint32_t slot = smem_u32(tiles + kPOff + pb * kPSlotBytes);
             const bool first = g == 2 * it.t0;
+            // Rows past the last key may hold anything (NaN): they must be zero for 0 * row to be 0.
+            const int left = it.un.keys - kPage * g;
+            uint32_t moved = 0;
             if (!first) {
-              uint32_t moved = 0;
               const float *pa = reinterpret_cast<const float *>(tiles + kPOff + pb * kPSlotBytes + kPBytes);
 #pragma unroll
               for (int w = 0; w < 4; ++w) moved |= reinterpret_cast<const uint32_t *>(pa + w * kPaWords)[32];
-              if (moved) {
-                // O is read back: the previous page's MMAs must be complete.
-                if (!(ok = waitw(sm, bar(B_PVDONE + (np - 1) % kPSlots), ((np - 1) / kPSlots) & 1, p.dev_status))) break;
-                if (lane == 0) {
-                  sm.req = Req{0, pb, 0, 0, 0};
-                  mbar_arrive(bar(B_REQ));
-                }
-                if (!(ok = waitw(sm, bar(B_REQDONE), nfix & 1, p.dev_status))) break;
-                tc_fence_after();
-                ++nfix;
-              }
             }
-            if (!(ok = waitw(sm, bar(B_VFULL + sv), (np / kVStages) & 1, p.dev_status))) break;
+            if (!(ok = waitw(sm, bar(B_CFULL + sv), (np / kVStages) & 1, p.dev_status))) break;
+            if (moved || left < kPage) {
+              // O is read back for a rescale: the previous page's MMAs must be complete.
+              if (moved && !(ok = waitw(sm, bar(B_PVDONE + (np - 1) % kPSlots), ((np - 1) / kPSlots) & 1, p.dev_status)))
+                break;
+              if (lane == 0) {
+                sm.req = Req{0, moved != 0, pb, left, sv, 0, 0};
+                mbar_arrive(bar(B_REQ));
+              }
+              if (!(ok = waitw(sm, bar(B_REQDONE), nfix & 1, p.dev_status))) break;
+              tc_fence_after();
+              ++nfix;
+            }
             if (!lead) {
               tc_fence_before();
               __syncwarp();
@@ -481,13 +493,13 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
               for (int ks = 0; ks < 4; ++ks)
                 mma2_ss(tbase + 256 * h, ad + ((ks * 32) >> 4), bd + ((h * 2 * kChunkBytes + ks * 2048) >> 4), idesc,
                         (first && ks == 0) ? 0u : 1u);
-            commit2(bar(B_VEMPTY + sv), kValuePair);
+            commit2(bar(B_CEMPTY + sv), kValuePair);
             commit2(bar(B_PVDONE + pb), kValuePair);
           }
           if (!ok) break;
           const uint32_t last = np - 1;
           if (lane == 0) {
-            sm.req = Req{1, 0, it.seg(), (int)(last % kPSlots), (int)((last / kPSlots) & 1)};
+            sm.req = Req{1, 0, 0, 0, 0, (int)(last % kPSlots), (int)((last / kPSlots) & 1)};
             mbar_arrive(bar(B_REQ));
           }
           __syncwarp();
@@ -535,46 +547,44 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         staging_free();
         unsigned char *stg_w = stgp + q4 * 4096;
         const int j = lane & 7;
-        const uint4 *rowp[8];
-        bool live[8];
+        // This lane's rows are r0, r0 + 4, .. of the unit, contiguous in memory.
+        const int r0 = kRows * (int)side + q4 * 32 + (lane >> 3);
+        const int left = it.un.rows - r0;
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(it.un.row0 + r0) * kW) + j;
+        constexpr int kStep = 4 * kW / 8;   // 16-byte words between a lane's rows
+        // Two of the four 64-dim columns in flight; a column's registers take the one after next as soon as it is staged.
+        uint4 x[2][8];
+        auto load_column = [&](int cb) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int g = kRows * (int)side + q4 * 32 + 4 * k + (lane >> 3);
-          live[k] = g < it.un.rows;
-          rowp[k] = reinterpret_cast<const uint4 *>(p.q + (int64_t)(it.un.row0 + (live[k] ? g : 0)) * kW);
-        }
-#pragma unroll 1
-        for (int cb = 0; cb < 4; cb += 2) {
-          uint4 x[2][8];
+          for (int k = 0; k < 8; ++k)
+            x[cb & 1][k] = 4 * k < left ? __ldg(src + k * kStep + h * 32 + cb * 8) : make_uint4(0, 0, 0, 0);
+        };
+        load_column(0);
+        load_column(1);
 #pragma unroll
-          for (int rr = 0; rr < 2; ++rr)
+        for (int cb = 0; cb < 4; ++cb) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              x[rr][k] = live[k] ? __ldg(rowp[k] + h * 32 + (cb + rr) * 8 + j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int rr = 0; rr < 2; ++rr) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int lr = 4 * k + (lane >> 3);
-              *reinterpret_cast<uint4 *>(stg_w + (lr >> 3) * 1024 + (lr & 7) * 128 + ((j ^ (lr & 7)) << 4)) = x[rr][k];
-            }
-            __syncwarp();
-            uint32_t v[32];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 y = *reinterpret_cast<const uint4 *>(stg_w + (lane >> 3) * 1024 + (lane & 7) * 128 + ((i ^ (lane & 7)) << 4));
-              v[4 * i] = y.x; v[4 * i + 1] = y.y; v[4 * i + 2] = y.z; v[4 * i + 3] = y.w;
-            }
-            tmem_st32(tbase + lane_off + kQCol + 128 * h + 32 * (cb + rr), v);
-            __syncwarp();
+          for (int k = 0; k < 8; ++k) {
+            const int lr = 4 * k + (lane >> 3);
+            *reinterpret_cast<uint4 *>(stg_w + (lr >> 3) * 1024 + (lr & 7) * 128 + ((j ^ (lr & 7)) << 4)) = x[cb & 1][k];
           }
+          if (cb + 2 < 4) load_column(cb + 2);
+          __syncwarp();
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 y = *reinterpret_cast<const uint4 *>(stg_w + (lane >> 3) * 1024 + (lane & 7) * 128 + ((i ^ (lane & 7)) << 4));
+            w[4 * i] = y.x; w[4 * i + 1] = y.y; w[4 * i + 2] = y.z; w[4 * i + 3] = y.w;
+          }
+          tmem_st32(tbase + lane_off + kQCol + 128 * h + 32 * cb, w);
+          __syncwarp();
         }
         if (h == 0) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int rq = q4 * 32 + 4 * k + (lane >> 3);
             *reinterpret_cast<uint4 *>(tiles + kQpeOff + (rq >> 3) * 1024 + (rq & 7) * 128 + ((j ^ (rq & 7)) << 4)) =
-                live[k] ? __ldg(rowp[k] + 64 + j) : make_uint4(0, 0, 0, 0);
+                4 * k < left ? __ldg(src + k * kStep + 64) : make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -583,6 +593,8 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(qready);
       }
+      // Keys of the unit that this row sees; rows past the unit's end see what its last row sees (their queries are 0).
+      const int vis = min(it.un.keys, it.un.vis0 + min(kRows * (int)side + r, it.un.rows - 1) / p.H);
       float m_mine = -CUDART_INF_F, l = 0.f;   // l: this group's row sum, relative to m_mine
       const uint32_t ns_end = ns + (uint32_t)(it.t1 - it.t0);
       for (int t = it.t0; t < it.t1; ++t, ++ns) {
@@ -604,14 +616,28 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             mx = max3f(mx, __uint_as_float(v[1][k]), __uint_as_float(v[1][k + 1]));
           }
         };
+        // Only a sequence's last tiles have keys that some row does not see: warps whose rows all see the whole tile
+        // skip the mask.
+        const int seen = vis - 2 * kPage * t;
+        const bool whole = __all_sync(0xffffffffu, seen >= kPage * npg);
+        auto mask_page = [&](int pg) {
+          const int n = seen - kPage * pg;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            v[0][k] = k < n ? v[0][k] : __float_as_uint(-CUDART_INF_F);
+            v[1][k] = k + 32 < n ? v[1][k] : __float_as_uint(-CUDART_INF_F);
+          }
+        };
         // The second page only for its maximum (it is read again below), the first one to stay.
         if (npg == 2) {
           load_page(1);
           tmem_wait_ld();
+          if (!whole) mask_page(1);
           page_max();
         }
         load_page(0);
         tmem_wait_ld();
+        if (!whole) mask_page(0);
         page_max();
         mx *= p.scale_log2;
         // The reference after the previous tile, and this tile's for the next one.
@@ -623,10 +649,11 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         const bool need = mx > m_prev + kRescaleLog2;
         const float m_ref = need ? mx : m_prev;
         const float alpha = need ? exp2f(m_prev - mx) : 1.f;
+        const float m_use = m_ref == -CUDART_INF_F ? 0.f : m_ref;   // no key seen yet: every P is exp2(-inf) = 0
         sm.m_sh[h][r] = m_ref;
         asm volatile("bar.arrive %0, 256;" ::"r"(4 + h) : "memory");
         if (m_mine != m_ref) {
-          l *= exp2f(m_mine - m_ref);   // m_mine = -inf: l is 0
+          l *= exp2f(m_mine - m_ref);   // m_mine = -inf: l is 0 (and m_ref, which never falls, is finite)
           m_mine = m_ref;
         }
         const unsigned moved = __ballot_sync(0xffffffffu, need && t != it.t0);
@@ -637,8 +664,8 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
           for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = exp2f(__uint_as_float(v[c2][2 * e]) * p.scale_log2 - m_ref);
-              const float p1 = exp2f(__uint_as_float(v[c2][2 * e + 1]) * p.scale_log2 - m_ref);
+              const float p0 = exp2f(__uint_as_float(v[c2][2 * e]) * p.scale_log2 - m_use);
+              const float p1 = exp2f(__uint_as_float(v[c2][2 * e + 1]) * p.scale_log2 - m_use);
               pk[16 * c2 + e] = pack_bf16x2(p0, p1);
               psum0 += p0;
               psum1 += p1;
@@ -667,6 +694,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
           mbar_arrive_cluster_light(sempty + 8 * h);   // the last read of this S is done
         }
         if (npg == 2) {
+          if (!whole) mask_page(1);
           page_p();
           stage(1.f, false);
           __syncwarp();
@@ -680,7 +708,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
       if (!last) {
         asm volatile("bar.sync %0, 256;" ::"r"(5 - h) : "memory");
         const float m_end = sm.m_sh[h ^ 1][r];
-        sm.xl[r] = l > 0.f ? l * exp2f(m_mine - m_end) : 0.f;
+        sm.xl[r] = l > 0.f ? l * exp2f(m_mine - m_end) : 0.f;   // l > 0: m_mine is finite
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (last) {
@@ -709,19 +737,30 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         ++nreq;
         const Req q = sm.req;
         if (q.kind == 0) {
-          tc_fence_after();
-          const float a = reinterpret_cast<const float *>(tiles + kPOff + q.slot * kPSlotBytes + kPBytes)[(r >> 5) * kPaWords + (r & 31)];
+          if (q.rescale) {
+            tc_fence_after();
+            const float a = reinterpret_cast<const float *>(tiles + kPOff + q.slot * kPSlotBytes + kPBytes)[(r >> 5) * kPaWords + (r & 31)];
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t v[32];
-            tmem_ld32(tbase + lane_off + ocol + 32 * c, v);
-            tmem_wait_ld();
+            for (int c = 0; c < 8; ++c) {
+              uint32_t v[32];
+              tmem_ld32(tbase + lane_off + ocol + 32 * c, v);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
-            tmem_st32(tbase + lane_off + ocol + 32 * c, v);
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+              tmem_st32(tbase + lane_off + ocol + 32 * c, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
           }
-          tmem_wait_st();
-          tc_fence_before();
+          if (q.keys < kPage) {
+            // 4 chunks of 8 pieces of 16 bytes per row; the eight warps share the rows.
+            unsigned char *vt = tiles + q.stage * kVStageBytes;
+            for (int e = threadIdx.x - 128; e < (kPage - q.keys) * 32; e += 256) {
+              const int row = q.keys + (e >> 5);
+              *reinterpret_cast<uint4 *>(vt + ((e >> 3) & 3) * kChunkBytes + row * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_REQDONE));
           continue;
@@ -734,7 +773,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(statsempty_remote);
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int64_t prow = (int64_t)q.segid * kUnitRows + kRows * side + r;
+        const int64_t prow = (int64_t)it.part_row() + kRows * side + r;
         const bool live = kRows * (int)side + r < it.un.rows;
         __nv_bfloat16 *dst = p.o_part + prow * kDc;
 #pragma unroll 1
@@ -778,34 +817,83 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
 }
 
 // ------------------------------------------------------------ plan
-// One CTA.  Shared keys of a group: the whole blocks among its first min(prefix_lens[g], shortest visible run) keys,
-// where the first query token of sequence b sees seqlens[b] - n_q + 1 keys.
+// One CTA.  A group's shared keys are the whole blocks among its first min(prefix_lens[g], shortest visible run) keys,
+// where the first query token of sequence b sees seqlens[b] - n_q + 1 keys.  They become shared units where that saves
+// work: n sequences over T tiles cost n T by themselves and units (T + kUnitCost) together.
+//
+// The work list is the own units by sequence, then the shared ones; a tile costs 1, and every unit after the first
+// kUnitCost more (its queries go to tensor memory and the finished unit's O is written out while the MMAs wait).
+// Cluster c's share is [floor(c W / C), floor((c + 1) W / C)) of the total cost W.
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+constexpr int kUnitCost = 8;
 
-__device__ __forceinline__ int cluster_of(int64_t t, int N, int C) { return (int)(((t + 1) * C + N - 1) / N - 1); }
+__device__ __forceinline__ int cluster_of(int64_t at, int W, int C) { return (int)(((at + 1) * C + W - 1) / W - 1); }
+
+// Writes unit u and its partials, given its place among the tiles and the non-empty units before it.
+struct PlanOut {
+  SharedPlan pl;
+  int W, C;
+  __device__ __forceinline__ void unit(int u, int tile0, int before, SharedUnit un) const {
+    un.cost0 = tile0 + kUnitCost * before;
+    int4 *dst = reinterpret_cast<int4 *>(pl.units + u);
+    dst[0] = make_int4(un.cost0, un.tiles, un.pages, un.seq);
+    dst[1] = make_int4(un.row0, un.rows, un.page0, un.keys);
+    dst[2] = make_int4(un.part0, un.part_stride, un.vis0, 0);
+    if (un.tiles == 0) {
+      pl.unit_parts[u] = make_int2(0, 0);
+      return;
+    }
+    const int c0 = cluster_of(un.cost0, W, C), c1 = cluster_of((int64_t)un.cost0 + un.tiles - 1, W, C);
+    pl.unit_parts[u] = make_int2(un.part0 + c0 * un.part_stride, c1 - c0 + 1);
+    // The clusters whose share begins behind the previous unit's last tile and not behind this one's.
+    const int64_t from = before ? (int64_t)un.cost0 - kUnitCost : 0;
+    for (int x = cluster_of(from, W, C); x <= c1; ++x)
+      if ((int64_t)x * W / C >= from) pl.cluster_unit[x] = u;
+  }
+};
+
+// Exclusive scan of one packed value per thread (kPlanThreads of them), its total added to `carry`.
+__device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t *part, int64_t &carry) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t w = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += w;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = inc;
+  __syncthreads();
+  int64_t w = part[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  const int64_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+  const int64_t all = __shfl_sync(0xffffffffu, w, 31);
+  const int64_t exc = carry + (warp ? before : 0) + inc - v;
+  carry += all;
+  return exc;
+}
 
 __global__ void __launch_bounds__(kPlanThreads)
 shared_plan_kernel(SharedPlan pl, int B, int n_q, int R, int max_seqlen, int block_size, int G, int clusters,
-                   const int32_t *offsets,
-                   const int32_t *prefix_lens, const int32_t *seqlens, int *dev_status) {
+                   const int32_t *offsets, const int32_t *prefix_lens, const int32_t *seqlens, int *dev_status) {
   __shared__ int64_t part[kPlanWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_launch();
-  grid_dep_wait();   // earlier calls may still read the plan that is overwritten here
   int bad = 0;
   for (int g = tid; g < G; g += kPlanThreads) {
     const int lo = offsets[g], hi = offsets[g + 1];
     bad |= lo < 0 || lo > hi || hi > B || (g == 0 && lo != 0) || (g == G - 1 && hi != B) || prefix_lens[g] < 0;
   }
   bad = __syncthreads_or(bad);
+  grid_dep_wait();   // earlier calls may still read the plan that is overwritten from here on
   if (bad && tid == 0) report(dev_status, MLA_ERR_BAD_INDEX);
   if (bad) G = 0;
   if (G == 0)
-    for (int b = tid; b < B; b += kPlanThreads) {
-      pl.own_begin[b] = 0;
-      pl.seq_unit[b] = make_int2(-1, 0);
-    }
-  // Pages of every group.
+    for (int b = tid; b < B; b += kPlanThreads) pl.own_begin[b] = 0;
   for (int g = warp; g < G; g += kPlanWarps) {
     const int lo = offsets[g], hi = offsets[g + 1];
     int common = prefix_lens[g];
@@ -815,79 +903,84 @@ shared_plan_kernel(SharedPlan pl, int B, int n_q, int R, int max_seqlen, int blo
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) common = min(common, __shfl_xor_sync(0xffffffffu, common, o));
-    // A sequence alone shares nothing.
-    if (lane == 0) pl.group_pages[g] = hi - lo > 1 ? common / block_size * (block_size / kPage) : 0;
+    int pages = common / block_size * (block_size / kPage);
+    const int64_t tiles = (pages + 1) / 2, n = hi - lo;
+    const int64_t units = (n * R + kUnitRows - 1) / kUnitRows;
+    if (units * (tiles + kUnitCost) >= n * tiles) pages = 0;
+    if (lane == 0) pl.group_pages[g] = pages;
+    for (int b = lo + lane; b < hi; b += 32) pl.own_begin[b] = pages * kPage;
   }
   __syncthreads();
-  // First unit and first tile of every group (their sums packed: units low, tiles high), a slab of groups at a time.
-  // The totals are needed first (clusters are dealt out over all tiles), so there are two passes.
+  // Two passes over the list, packed as units (low word) and tiles (high): the totals, then the units.
+  PlanOut out{pl, 0, 1};
+  int U = B;
   for (int pass = 0; pass < 2; ++pass) {
-    __shared__ int64_t s_total;
     int64_t carry = 0;
-    const int64_t total = pass ? s_total : 0;
-    const int N = (int)(total >> 32), U = (int)(total & 0xffffffff);
-    const int C = N < clusters ? N : clusters;
+    for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+      const int b = b0 + tid;
+      SharedUnit un{};
+      if (b < B) {
+        const int S = seqlens[b], begin = pl.own_begin[b];
+        const int len = min(max(S, 0), max_seqlen);
+        if (!pass && (S < n_q || S > max_seqlen)) report(dev_status, MLA_ERR_BAD_INDEX);
+        un.keys = max(len - begin, 0);
+        un.pages = (un.keys + kPage - 1) / kPage;
+        un.tiles = (un.pages + 1) / 2;
+        un.seq = b;
+        un.row0 = b * R;
+        un.rows = R;
+        un.page0 = begin / kPage;
+        un.part0 = b * R;
+        un.part_stride = R;
+        un.vis0 = len - n_q + 1 - begin;
+      }
+      const int64_t exc = plan_scan((int64_t)(un.tiles > 0) | ((int64_t)un.tiles << 32), part, carry);
+      if (pass && b < B) out.unit(b, (int)(exc >> 32), (int)(exc & 0xffffffff), un);
+    }
+    int shared = B;   // the next shared unit
     for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
       const int g = g0 + tid;
-      int64_t v = 0;
+      int pages = 0, units = 0;
       if (g < G) {
-        const int pages = pl.group_pages[g];
-        const int units = pages ? (int)(((int64_t)(offsets[g + 1] - offsets[g]) * R + kUnitRows - 1) / kUnitRows) : 0;
-        v = (int64_t)units | ((int64_t)units * ((pages + 1) / 2) << 32);
+        pages = pl.group_pages[g];
+        units = pages ? (int)(((int64_t)(offsets[g + 1] - offsets[g]) * R + kUnitRows - 1) / kUnitRows) : 0;
       }
-      int64_t inc = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t w = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += w;
-      }
-      __syncthreads();
-      if (lane == 31) part[warp] = inc;
-      __syncthreads();
-      int64_t w = part[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-      }
-      const int64_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
-      const int64_t slab = __shfl_sync(0xffffffffu, w, 31);
-      const int64_t exc = carry + (warp ? before : 0) + inc - v;
-      carry += slab;
-      if (pass) {
-        // The warp writes its 32 groups one after another.
-        for (int k = 0; k < 32; ++k) {
+      const int64_t before = carry;
+      const int64_t exc = plan_scan((int64_t)units | ((int64_t)units * ((pages + 1) / 2) << 32), part, carry);
+      if (pass)
+        for (int k = 0; k < 32; ++k) {   // the warp writes its 32 groups one after another
           const int gg = g0 + warp * 32 + k;
           if (gg >= G) break;
           const int64_t e = __shfl_sync(0xffffffffu, exc, k);
-          const int u0 = (int)(e & 0xffffffff), tile0 = (int)(e >> 32);
-          const int lo = offsets[gg], hi = offsets[gg + 1], pages = pl.group_pages[gg];
-          const int rows = (hi - lo) * R, tiles = (pages + 1) / 2;
-          const int units = pages ? (rows + kUnitRows - 1) / kUnitRows : 0;
-          for (int b = lo + lane; b < hi; b += 32) {
-            pl.own_begin[b] = pages * kPage;
-            pl.seq_unit[b] = make_int2(pages ? u0 : -1, lo * R);
-          }
-          for (int i = lane; i < units; i += 32) {
-            const int u = u0 + i, ut = tile0 + i * tiles;
-            const int4 a = make_int4(ut, tiles, pages, lo);
-            const int4 c = make_int4(lo * R + i * kUnitRows, min(kUnitRows, rows - i * kUnitRows), 0, 0);
-            reinterpret_cast<int4 *>(pl.units + u)[0] = a;
-            reinterpret_cast<int4 *>(pl.units + u)[1] = c;
-            const int c0 = cluster_of(ut, N, C), c1 = cluster_of((int64_t)ut + tiles - 1, N, C);
-            pl.unit_segs[u] = make_int2(u + c0, c1 - c0 + 1);
-            // Clusters whose first tile lies in this unit.
-            for (int x = c0; x <= c1; ++x)
-              if ((int64_t)x * N / C >= ut) pl.cluster_unit[x] = u;
+          const int n = __shfl_sync(0xffffffffu, units, k), pg = __shfl_sync(0xffffffffu, pages, k);
+          const int u0 = shared + (int)((e - before) & 0xffffffff);
+          const int lo = offsets[gg], hi = offsets[gg + 1], rows = (hi - lo) * R, tiles = (pg + 1) / 2;
+          for (int b = lo + lane; b < hi; b += 32) pl.seq_group[b] = make_int2(n ? u0 : -1, lo * R);
+          for (int i = lane; i < n; i += 32) {
+            SharedUnit un{};
+            un.tiles = tiles;
+            un.pages = pg;
+            un.seq = lo;
+            un.row0 = lo * R + i * kUnitRows;
+            un.rows = min(kUnitRows, rows - i * kUnitRows);
+            un.keys = pg * kPage;
+            un.part0 = (B + clusters) * R + (u0 + i - B) * kUnitRows;
+            un.part_stride = kUnitRows;
+            un.vis0 = un.keys;
+            out.unit(u0 + i, (int)(e >> 32) + i * tiles, (int)(e & 0xffffffff) + i, un);
           }
         }
-      }
+      shared += (int)((carry - before) & 0xffffffff);
     }
-    __syncthreads();
-    if (!pass && tid == 0) s_total = carry;
-    __syncthreads();
-    if (pass && tid == 0) *reinterpret_cast<int4 *>(pl.head) = make_int4(N, C, U, 0);
+    if (G == 0 && pass)
+      for (int b = tid; b < B; b += kPlanThreads) pl.seq_group[b] = make_int2(-1, 0);
+    // Every thread holds the totals.
+    const int n = (int)(carry & 0xffffffff);
+    out.W = (int)(carry >> 32) + kUnitCost * max(n - 1, 0);
+    out.C = max(1, min(out.W, clusters));
+    U = shared;
   }
+  if (tid == 0) *reinterpret_cast<int4 *>(pl.head) = make_int4(out.W, out.W > 0 ? out.C : 0, U, 0);
 }
 
 }  // namespace
@@ -960,6 +1053,7 @@ int launch_shared_attention(const mla_dims &d, const SharedPlan &pl, const void 
   p.max_blocks_per_seq = cache.max_blocks_per_seq;
   p.num_blocks = cache.num_blocks;
   p.block_size = cache.block_size;
+  p.H = d.n_heads;
   p.scale_log2 = default_scale(d) * 1.4426950408889634f;
   p.o_part = o_part;
   p.lse_part = lse_part;
