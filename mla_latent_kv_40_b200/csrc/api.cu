@@ -215,20 +215,19 @@ AbsorbedLayout absorbed_layout(const mla_dims *d, int d_cq, int B, int n_q, int 
   return L;
 }
 
-// Decode over shared prefixes (tensor-core shapes): the absorbed queries, the plan, and the partials of the sequences'
-// own keys followed by those of the shared ones.
+// Decode over shared prefixes (tensor-core shapes): the absorbed queries, the plan, and the units' partials.
 struct SharedLayout {
-  size_t q_off, head_off, cluster_off, units_off, parts_off, seq_off, begin_off, pages_off, o_off, lse_off, total;
+  size_t q_off, head_off, cluster_off, units_off, parts_off, seq_off, own_off, shared_off, groups_off, o_off, lse_off, total;
 };
 
 SharedLayout shared_layout(const mla_dims *d, int B, int n_q, int num_groups) {
   SharedLayout L{};
   const int R = n_q * d->n_heads;
-  const int shared = shared_max_units(B, R, num_groups);
+  const int units = shared_max_units(B, R, num_groups);
   const int C = shared_clusters_for_device();
   const int clusters = C > 0 ? C : kSharedMaxClusters;
   // A list of n units cut at most clusters - 1 times leaves at most n + clusters - 1 partials.
-  const size_t rows = (size_t)(B + clusters) * R + (size_t)(shared + clusters) * kSharedUnitRows;
+  const size_t rows = (size_t)(units + clusters) * kSharedUnitRows;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -238,11 +237,12 @@ SharedLayout shared_layout(const mla_dims *d, int B, int n_q, int num_groups) {
   L.q_off = take((size_t)B * R * (d->d_c + d->d_rope) * 2);
   L.head_off = take(16);
   L.cluster_off = take((size_t)clusters * sizeof(int));
-  L.units_off = take((size_t)(B + shared) * sizeof(SharedUnit));
-  L.parts_off = take((size_t)(B + shared) * sizeof(int2));
+  L.units_off = take((size_t)units * sizeof(SharedUnit));
+  L.parts_off = take((size_t)units * sizeof(int2));
   L.seq_off = take((size_t)B * sizeof(int2));
-  L.begin_off = take((size_t)B * sizeof(int));
-  L.pages_off = take((size_t)num_groups * sizeof(int));
+  L.own_off = take((size_t)(B + 1) * sizeof(int));
+  L.shared_off = take((size_t)B * sizeof(int));
+  L.groups_off = take((size_t)(num_groups + 1) * sizeof(int));
   L.o_off = take(rows * d->d_c * 2);
   L.lse_off = take(rows * sizeof(float));
   L.total = off;
@@ -452,8 +452,8 @@ int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *q_nope, 
   void *qbuf = ws + L.q_off;
   const SharedPlan pl{reinterpret_cast<int *>(ws + L.head_off), reinterpret_cast<int *>(ws + L.cluster_off),
                       reinterpret_cast<SharedUnit *>(ws + L.units_off), reinterpret_cast<int2 *>(ws + L.parts_off),
-                      reinterpret_cast<int2 *>(ws + L.seq_off), reinterpret_cast<int *>(ws + L.begin_off),
-                      reinterpret_cast<int *>(ws + L.pages_off)};
+                      reinterpret_cast<int2 *>(ws + L.seq_off), reinterpret_cast<int *>(ws + L.own_off),
+                      reinterpret_cast<int *>(ws + L.shared_off), reinterpret_cast<int *>(ws + L.groups_off)};
   __nv_bfloat16 *o_part = reinterpret_cast<__nv_bfloat16 *>(ws + L.o_off);
   float *lse_part = reinterpret_cast<float *>(ws + L.lse_off);
   const CacheView cv{c_kv, k_pe, dims->ckv_stride, dims->kpe_stride, block_table, max_blocks_per_seq, num_blocks,
@@ -466,8 +466,9 @@ int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *q_nope, 
   const AbsorbArgs ab{B, n_q, dims->n_heads, dims->d_c, dims->d_rope, dims->d_nope,
                       q_nope, q_pe, w_uk, seqlens, qbuf, dims->rope_base};
   if ((rc = absorb_dispatch(ab, true, dev_status, st))) return rc;
-  if ((rc = launch_shared_attention(*dims, pl, qbuf, cv, o_part, lse_part, dev_status, st))) return rc;
-  const SharedPieces pc{o_part, lse_part, pl.unit_parts, pl.seq_group, n_q, dims->n_heads};
+  if ((rc = launch_shared_attention(*dims, n_q, max_seqlen, pl, qbuf, cv, seqlens, o_part, lse_part, dev_status, st))) return rc;
+  const SharedPieces pc{o_part, lse_part, pl.unit_parts, pl.seq_group, n_q, dims->n_heads,
+                        shared_unit_rows(n_q * dims->n_heads)};
   return launch_tc_combine_shared(*dims, B, n_q, pc, w_uv, out, lse, dev_status, st);
 }
 

@@ -1162,19 +1162,11 @@ struct Pieces {
   int n_q, H, n_rb, max_segs, n_parts;
 };
 
-// The pieces of one output row: ns rows from `first` on, `stride` apart; with a shared prefix, `own` such rows of the
-// sequence's own keys, then rows from `first2` on, `stride2` apart, of the shared ones.
+// The pieces of one output row: ns rows from `first` on, `stride` apart.
 struct PieceRows {
   int ns = 0;
   int64_t first = 0, stride = 0;
   __device__ __forceinline__ int64_t at(int k) const { return first + k * stride; }
-};
-struct SharedPieceRows {
-  int ns = 0, own = 0;
-  int64_t first = 0, stride = 0, first2 = 0, stride2 = 0;
-  __device__ __forceinline__ int64_t at(int k) const {
-    return k < own ? first + k * stride : first2 + (k - own) * stride2;
-  }
 };
 
 __device__ __forceinline__ PieceRows piece_rows(const Pieces &pc, int rows, int g, int s) {
@@ -1198,22 +1190,14 @@ __device__ __forceinline__ PieceRows piece_rows(const Pieces &pc, int rows, int 
   return r;
 }
 
-// The plan's own units of n_q * H rows come first, then its shared units of kSharedUnitRows.
-__device__ __forceinline__ SharedPieceRows piece_rows(const SharedPieces &pc, int, int g, int s) {
-  SharedPieceRows r;
-  const int b = g / pc.n_q, R = pc.n_q * pc.H;
-  const int2 ou = pc.unit_parts[b];
-  r.first = ou.x + (g * pc.H + s - b * R);
-  r.stride = R;
-  r.ns = r.own = ou.y;
-  const int2 su = pc.seq_group[b];
-  if (su.x >= 0) {
-    const int q = g * pc.H + s - su.y;   // row within the group
-    const int2 sp = pc.unit_parts[su.x + q / kSharedUnitRows];
-    r.first2 = sp.x + q % kSharedUnitRows;
-    r.stride2 = kSharedUnitRows;
-    r.ns += sp.y;
-  }
+__device__ __forceinline__ PieceRows piece_rows(const SharedPieces &pc, int, int g, int s) {
+  PieceRows r;
+  const int2 sg = pc.seq_group[g / pc.n_q];
+  const int q = g * pc.H + s - sg.y;   // row within the group
+  const int2 up = pc.unit_parts[sg.x + q / pc.unit_rows];
+  r.first = (int64_t)up.x * kSharedUnitRows + q % pc.unit_rows;
+  r.stride = kSharedUnitRows;
+  r.ns = up.y;
   return r;
 }
 
@@ -1224,7 +1208,7 @@ shared_merge_kernel(const SharedPieces pc, int rows, __nv_bfloat16 *o_lat, float
   sm100::grid_dep_wait();
   const int64_t item = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
   if (item >= (int64_t)rows * pc.H) return;
-  const SharedPieceRows pr = piece_rows(pc, rows, (int)(item / pc.H), (int)(item % pc.H));
+  const PieceRows pr = piece_rows(pc, rows, (int)(item / pc.H), (int)(item % pc.H));
   merge_row(threadIdx.x & 31, pr.ns, pc.part, pc.lse, [&](int k) { return pr.at(k); }, o_lat + item * kDc,
             lse_out ? lse_out + item : nullptr);
 }
@@ -1279,8 +1263,7 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int row
   {
     // Merge of row rr (output row g = g0 + rr); rows past the end become zero rows of the tile.
     const int rr = tid >> 2, q = tid & 3, g = g0 + rr;
-    decltype(piece_rows(pc, rows, g, s)) pr;
-    if (g < rows) pr = piece_rows(pc, rows, g, s);
+    const PieceRows pr = g < rows ? piece_rows(pc, rows, g, s) : PieceRows();
     const int ns = pr.ns;
     float m = -CUDART_INF_F;
     for (int k = 0; k < ns; ++k) m = fmaxf(m, pc.lse[pr.at(k)]);

@@ -19,14 +19,14 @@ int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, co
 // Merge of the partials, and the W_UV product in the same kernel when w_uv != NULL.
 int launch_tc_combine(const mla_dims &d, int B, int n_q, const int32_t *seqlens, int max_seqlen, const void *w_uv,
                       void *out, float *lse, void *ws, int *dev_status, cudaStream_t st);
-// Where the partials of a decode over shared prefixes live (see shared_tc.cuh): row `part` of each piece, by unit.
-constexpr int kSharedUnitRows = 256;
+// Where the partials of a decode over shared prefixes live (see shared_tc.cuh).
+constexpr int kSharedUnitRows = 256;   // rows of a partial
 struct SharedPieces {
   const __nv_bfloat16 *part;   // rows of 512 bf16
   const float *lse;
-  const int2 *unit_parts;      // first partial row and number of partials of every unit: own units by sequence first
-  const int2 *seq_group;       // [B]: first shared unit of the sequence's group (-1: none), the group's first query row
-  int n_q, H;
+  const int2 *unit_parts;      // first partial and number of partials of every unit
+  const int2 *seq_group;       // [B]: first unit of the sequence's group, the group's first query row
+  int n_q, H, unit_rows;       // unit_rows: query rows of a full unit
 };
 int launch_tc_combine_shared(const mla_dims &d, int B, int n_q, const SharedPieces &pc, const void *w_uv, void *out,
                              float *lse, int *dev_status, cudaStream_t st);

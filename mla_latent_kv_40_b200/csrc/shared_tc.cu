@@ -5,10 +5,13 @@
 // prefix the rows of all sequences of a group are rows of one product,
 //   S = Q [rows x 576] . K^T [576 x keys],   O += P [rows x keys] . C [keys x 512],
 // with no mask (the shared keys end before every query).  2176 FLOPs per (row, key) against 1152 bytes per key and
-// 256 rows: bound by the tensor cores.  A sequence's own keys are the same product with its n_q * H rows, masked at
-// the end.
+// 256 rows: bound by the tensor cores.
 //
-// Shape.  A unit is at most 256 rows and the keys that they attend to.  A cluster of four CTAs works on one unit at a time, as two pairs that issue M = 256
+// Shape.  A unit is at most 256 consecutive rows of a group, and a list of pages of 64 keys: the group's shared pages,
+// then the own pages of every sequence with rows in the unit, which the other rows do not see (a mask by owner and
+// length; S of such a page is computed for all rows, as an MMA with fewer rows would take the same time).  Own pages in
+// units of their own were slower by what a unit costs at its start and end: 106 us of attention for 64 sequences of
+// 128 heads behind 4096 shared tokens and up to 512 own ones.  A cluster of four CTAs works on one unit at a time, as two pairs that issue M = 256
 // MMAs (cta_group::2: each CTA holds 128 of the rows and half of the B operand, so each SM pulls half the bytes that
 // a 128-row tile of its own would need; at 128 rows the L2 -> SM path, not the tensor pipe, sets the pace):
 //   * ranks 0, 1 (score pair): Q_lat of the CTA's 128 rows in tensor memory (A operand), Q_rope in shared memory; a
@@ -116,8 +119,9 @@ struct Params {
   const int *head, *cluster_unit;
   const SharedUnit *units;
   const __nv_bfloat16 *q;
-  const int32_t *block_table;
-  int max_blocks_per_seq, num_blocks, block_size, H;
+  const int32_t *block_table, *seqlens;
+  const int *own_pages;
+  int max_blocks_per_seq, num_blocks, block_size, H, n_q, max_seqlen;
   float scale_log2;
   __nv_bfloat16 *o_part;
   float *lse_part;
@@ -197,9 +201,9 @@ struct Runs {
     for (; u < units; ++u) {
       const int4 *src = reinterpret_cast<const int4 *>(p.units + u);
       const int4 a = src[0], b = src[1], c = src[2];
-      un.cost0 = a.x; un.tiles = a.y; un.pages = a.z; un.seq = a.w;
-      un.row0 = b.x; un.rows = b.y; un.page0 = b.z; un.keys = b.w;
-      un.part0 = c.x; un.part_stride = c.y; un.vis0 = c.z;
+      un.cost0 = a.x; un.tiles = a.y; un.pages = a.z; un.shared = a.w;
+      un.row0 = b.x; un.rows = b.y; un.seq0 = b.z; un.members = b.w;
+      un.table_seq = c.x;
       if (un.cost0 >= hi) break;
       t0 = max(lo - un.cost0, 0);
       t1 = min(hi - un.cost0, un.tiles);
@@ -211,7 +215,8 @@ struct Runs {
     u = units;
     return false;
   }
-  __device__ __forceinline__ int part_row() const { return un.part0 + cid * un.part_stride; }
+  // u and cid only rise along the list, so that every (unit, cluster) has a partial of its own.
+  __device__ __forceinline__ int64_t part_row() const { return (int64_t)(u - 1 + cid) * kUnitRows; }
   __device__ __forceinline__ int pages_end() const { return min(2 * t1, un.pages); }
 };
 
@@ -224,23 +229,60 @@ __device__ __forceinline__ int64_t page_row(const Params &p, int seq, int page) 
   return (int64_t)blk * p.block_size + key % p.block_size;
 }
 
+// The members of a unit, one per lane, and whose page is whose.  Warp-collective.
+struct Members {
+  int first, keys;    // this lane's member: its first page among the unit's own pages, its own keys
+  int shared;
+  __device__ __forceinline__ void load(const Params &p, const SharedUnit &un) {
+    const int lane = threadIdx.x & 31, b = un.seq0 + min(lane, un.members - 1);
+    shared = un.shared;
+    first = p.own_pages[b] - p.own_pages[un.seq0];
+    keys = min(max(p.seqlens[b], 0), p.max_seqlen) - kPage * shared;
+    if (lane >= un.members) first = 0x7fffffff;
+  }
+  // Owner of page v of the unit, the same for the whole warp (-1: shared), and which of its own pages it is.
+  __device__ __forceinline__ int owner(int v, int &page) const {
+    const int x = v - shared;
+    const int m = __popc(__ballot_sync(0xffffffffu, first <= x)) - 1;   // members without pages share their successor's place
+    page = x - __shfl_sync(0xffffffffu, first, max(m, 0));
+    return m;
+  }
+  // Pool row of page v, one page per lane.
+  __device__ __forceinline__ int64_t row(const Params &p, const SharedUnit &un, int v) const {
+    const int x = v - shared;
+    int m = 0, f = 0;
+    for (int i = 0; i < un.members; ++i) {
+      const int fi = __shfl_sync(0xffffffffu, first, i);
+      if (fi <= x) {
+        m = i;
+        f = fi;
+      }
+    }
+    return x < 0 ? page_row(p, un.table_seq, v) : page_row(p, un.seq0 + m, shared + x - f);
+  }
+};
+
 // Pool rows of a run's pages, looked up a warp-load at a time, one load ahead.
 struct PageRows {
-  int seq = -1, base = 0;
+  Members mem;
+  int base = 0;
   int64_t r0 = -1, r1 = -1;
-  __device__ __forceinline__ void start(const Params &p, int seq_, int page) {
-    const int lane = threadIdx.x & 31;
-    seq = seq_;
+  __device__ __forceinline__ int64_t look(const Params &p, const SharedUnit &un, int v) const {
+    const int64_t r = mem.row(p, un, min(v, un.pages - 1));
+    return v < un.pages ? r : -1;
+  }
+  __device__ __forceinline__ void start(const Params &p, const SharedUnit &un, int page) {
+    mem.load(p, un);
     base = page;
-    r0 = page_row(p, seq, base + lane);
-    r1 = page_row(p, seq, base + 32 + lane);
+    r0 = look(p, un, base + (threadIdx.x & 31));
+    r1 = look(p, un, base + 32 + (threadIdx.x & 31));
   }
   // Pages must be asked for in ascending order from the start page on.
-  __device__ __forceinline__ int64_t get(const Params &p, int page) {
+  __device__ __forceinline__ int64_t get(const Params &p, const SharedUnit &un, int page) {
     while (page >= base + 32) {
       base += 32;
       r0 = r1;
-      r1 = page_row(p, seq, base + 32 + (threadIdx.x & 31));
+      r1 = look(p, un, base + 32 + (threadIdx.x & 31));
     }
     return __shfl_sync(0xffffffffu, r0, page - base);
   }
@@ -298,11 +340,11 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         PageRows pr;
         int ok = 1;
         while (ok && it.next(p)) {
-          pr.start(p, it.un.seq, it.un.page0 + 2 * it.t0);
+          pr.start(p, it.un, 2 * it.t0);
           for (int t = it.t0; ok && t < it.t1; ++t) {
             const int page = 2 * t + (int)side;
             const bool have = page < it.un.pages;
-            int64_t row = pr.get(p, it.un.page0 + (have ? page : 2 * t));
+            int64_t row = pr.get(p, it.un, have ? page : 2 * t);
             if (row < 0) {
               if (lane == 0) report(p.dev_status, MLA_ERR_BAD_INDEX);
               row = 0;
@@ -417,9 +459,9 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         PageRows pr;
         int ok = 1;
         while (ok && it.next(p)) {
-          pr.start(p, it.un.seq, it.un.page0 + 2 * it.t0);
+          pr.start(p, it.un, 2 * it.t0);
           for (int g = 2 * it.t0; ok && g < it.pages_end(); ++g, ++n) {
-            int64_t row = pr.get(p, it.un.page0 + g);
+            int64_t row = pr.get(p, it.un, g);
             if (row < 0) row = 0;   // reported by the score pair
             const int s = n % kVStages;
             if (lane == 0) {
@@ -450,6 +492,8 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         uint32_t np = 0, uc = 0, nfix = 0;
         bool ok = true;
         while (ok && it.next(p)) {
+          Members mem;
+          mem.load(p, it.un);
           if (uc > 0 && !(ok = waitw(sm, bar(B_OFREE), (uc - 1) & 1, p.dev_status))) break;
           for (int g = 2 * it.t0; g < it.pages_end(); ++g, ++np) {
             const int pb = np % kPSlots, sv = np % kVStages;
@@ -458,7 +502,9 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             const uint32_t slot = smem_u32(tiles + kPOff + pb * kPSlotBytes);
             const bool first = g == 2 * it.t0;
             // Rows past the last key may hold anything (NaN): they must be zero for 0 * row to be 0.
-            const int left = it.un.keys - kPage * g;
+            int own;
+            const int m = mem.owner(g, own);
+            const int left = m < 0 ? kPage : __shfl_sync(0xffffffffu, mem.keys, m) - kPage * own;
             uint32_t moved = 0;
             if (!first) {
               const float *pa = reinterpret_cast<const float *>(tiles + kPOff + pb * kPSlotBytes + kPBytes);
@@ -527,10 +573,6 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
     const int q4 = warp & 3, h = (warp - 4) >> 2;
     const int r = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const uint32_t mate = 2 + side;                       // the value CTA of these rows
-    const uint32_t statl_remote = mapa(smem_u32(&sm.stat_l[0]), mate), statm_remote = mapa(smem_u32(&sm.stat_m[0]), mate);
-    const uint32_t statsfull_remote = mapa(bar(B_STATSFULL), mate);
-    const uint32_t sempty = mapa(bar(B_SEMPTY), 0), qready = mapa(bar(B_QREADY), 0);
     unsigned char *stgp = tiles + kStgOff + h * kPSlotBytes;
     unsigned char *stga = stgp + kPBytes;
     unsigned char *prow = stgp + 4096 * q4 + (lane >> 3) * 1024 + (lane & 7) * 128;
@@ -591,10 +633,14 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(qready);
+        if (lane == 0) mbar_arrive_cluster(mapa(bar(B_QREADY), 0));
       }
-      // Keys of the unit that this row sees; rows past the unit's end see what its last row sees (their queries are 0).
-      const int vis = min(it.un.keys, it.un.vis0 + min(kRows * (int)side + r, it.un.rows - 1) / p.H);
+      // This row's member and how many of that member's own keys it sees; rows past the unit's end see none.
+      Members mem;
+      mem.load(p, it.un);
+      const int gr = it.un.row0 + kRows * (int)side + r, R = p.n_q * p.H;
+      const int my_m = kRows * (int)side + r < it.un.rows ? gr / R - it.un.seq0 : -2;
+      const int vis = __shfl_sync(0xffffffffu, mem.keys, max(my_m, 0)) - p.n_q + 1 + (gr % R) / p.H;
       float m_mine = -CUDART_INF_F, l = 0.f;   // l: this group's row sum, relative to m_mine
       const uint32_t ns_end = ns + (uint32_t)(it.t1 - it.t0);
       for (int t = it.t0; t < it.t1; ++t, ++ns) {
@@ -616,12 +662,15 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             mx = max3f(mx, __uint_as_float(v[1][k]), __uint_as_float(v[1][k + 1]));
           }
         };
-        // Only a sequence's last tiles have keys that some row does not see: warps whose rows all see the whole tile
-        // skip the mask.
-        const int seen = vis - 2 * kPage * t;
-        const bool whole = __all_sync(0xffffffffu, seen >= kPage * npg);
-        auto mask_page = [&](int pg) {
-          const int n = seen - kPage * pg;
+        // Visible keys of both pages: 64 or more of a shared page, none of another member's page.
+        auto seen = [&](int pg) {
+          int own;
+          const int m = mem.owner(2 * t + pg, own);
+          return m < 0 ? kPage : (m == my_m ? vis - kPage * own : 0);
+        };
+        const int n0 = seen(0), n1 = npg == 2 ? seen(1) : 0;
+        auto mask_page = [&](int n) {   // only pages that some row of the warp does not see whole
+          if (__all_sync(0xffffffffu, n >= kPage)) return;
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             v[0][k] = k < n ? v[0][k] : __float_as_uint(-CUDART_INF_F);
@@ -632,12 +681,12 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         if (npg == 2) {
           load_page(1);
           tmem_wait_ld();
-          if (!whole) mask_page(1);
+          mask_page(n1);
           page_max();
         }
         load_page(0);
         tmem_wait_ld();
-        if (!whole) mask_page(0);
+        mask_page(n0);
         page_max();
         mx *= p.scale_log2;
         // The reference after the previous tile, and this tile's for the next one.
@@ -691,10 +740,10 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(B_STGFULL + h));
-          mbar_arrive_cluster_light(sempty + 8 * h);   // the last read of this S is done
+          mbar_arrive_cluster_light(mapa(bar(B_SEMPTY + h), 0));   // the last read of this S is done
         }
         if (npg == 2) {
-          if (!whole) mask_page(1);
+          mask_page(n1);
           page_p();
           stage(1.f, false);
           __syncwarp();
@@ -714,9 +763,10 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
       if (last) {
         l += sm.xl[r];
         if (uc > 0) waitw(sm, bar(B_STATSEMPTY), (uc - 1) & 1, p.dev_status);
-        st_cluster_f32(statl_remote + r * 4, l);
-        st_cluster_f32(statm_remote + r * 4, m_mine);
-        mbar_arrive_cluster(statsfull_remote);
+        const uint32_t mate = 2 + side;   // the value CTA of these rows
+        st_cluster_f32(mapa(smem_u32(&sm.stat_l[r]), mate), l);
+        st_cluster_f32(mapa(smem_u32(&sm.stat_m[r]), mate), m_mine);
+        mbar_arrive_cluster(mapa(bar(B_STATSFULL), mate));
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");   // xl and m_sh may be used again
       ++uc;
@@ -773,7 +823,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(statsempty_remote);
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int64_t prow = (int64_t)it.part_row() + kRows * side + r;
+        const int64_t prow = it.part_row() + kRows * side + r;
         const bool live = kRows * (int)side + r < it.un.rows;
         __nv_bfloat16 *dst = p.o_part + prow * kDc;
 #pragma unroll 1
@@ -818,41 +868,17 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
 
 // ------------------------------------------------------------ plan
 // One CTA.  A group's shared keys are the whole blocks among its first min(prefix_lens[g], shortest visible run) keys,
-// where the first query token of sequence b sees seqlens[b] - n_q + 1 keys.  They become shared units where that saves
-// work: n sequences over T tiles cost n T by themselves and units (T + kUnitCost) together.
+// where the first query token of sequence b sees seqlens[b] - n_q + 1 keys.
 //
-// The work list is the own units by sequence, then the shared ones; a tile costs 1, and every unit after the first
-// kUnitCost more (its queries go to tensor memory and the finished unit's O is written out while the MMAs wait).
-// Cluster c's share is [floor(c W / C), floor((c + 1) W / C)) of the total cost W.
+// The work list is the units in order; a tile costs 1, and every unit after the first kUnitCost more (its queries go to
+// tensor memory and the finished unit's O is written out while the MMAs wait).  Cluster c's share is
+// [floor(c W / C), floor((c + 1) W / C)) of the total cost W.
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr int kUnitCost = 8;
 
 __device__ __forceinline__ int cluster_of(int64_t at, int W, int C) { return (int)(((at + 1) * C + W - 1) / W - 1); }
 
-// Writes unit u and its partials, given its place among the tiles and the non-empty units before it.
-struct PlanOut {
-  SharedPlan pl;
-  int W, C;
-  __device__ __forceinline__ void unit(int u, int tile0, int before, SharedUnit un) const {
-    un.cost0 = tile0 + kUnitCost * before;
-    int4 *dst = reinterpret_cast<int4 *>(pl.units + u);
-    dst[0] = make_int4(un.cost0, un.tiles, un.pages, un.seq);
-    dst[1] = make_int4(un.row0, un.rows, un.page0, un.keys);
-    dst[2] = make_int4(un.part0, un.part_stride, un.vis0, 0);
-    if (un.tiles == 0) {
-      pl.unit_parts[u] = make_int2(0, 0);
-      return;
-    }
-    const int c0 = cluster_of(un.cost0, W, C), c1 = cluster_of((int64_t)un.cost0 + un.tiles - 1, W, C);
-    pl.unit_parts[u] = make_int2(un.part0 + c0 * un.part_stride, c1 - c0 + 1);
-    // The clusters whose share begins behind the previous unit's last tile and not behind this one's.
-    const int64_t from = before ? (int64_t)un.cost0 - kUnitCost : 0;
-    for (int x = cluster_of(from, W, C); x <= c1; ++x)
-      if ((int64_t)x * W / C >= from) pl.cluster_unit[x] = u;
-  }
-};
-
-// Exclusive scan of one packed value per thread (kPlanThreads of them), its total added to `carry`.
+// Exclusive scan of one value per thread (kPlanThreads of them), its total added to `carry`.
 __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t *part, int64_t &carry) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t inc = v;
@@ -882,6 +908,7 @@ shared_plan_kernel(SharedPlan pl, int B, int n_q, int R, int max_seqlen, int blo
                    const int32_t *offsets, const int32_t *prefix_lens, const int32_t *seqlens, int *dev_status) {
   __shared__ int64_t part[kPlanWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int unit_rows = shared_unit_rows(R);
   grid_dep_launch();
   int bad = 0;
   for (int g = tid; g < G; g += kPlanThreads) {
@@ -891,96 +918,90 @@ shared_plan_kernel(SharedPlan pl, int B, int n_q, int R, int max_seqlen, int blo
   bad = __syncthreads_or(bad);
   grid_dep_wait();   // earlier calls may still read the plan that is overwritten from here on
   if (bad && tid == 0) report(dev_status, MLA_ERR_BAD_INDEX);
-  if (bad) G = 0;
-  if (G == 0)
-    for (int b = tid; b < B; b += kPlanThreads) pl.own_begin[b] = 0;
+  if (bad) G = 1;    // then one group that shares nothing
+  auto first_of = [&](int g) { return bad ? g * B : offsets[g]; };
+  // Units before each group.
+  int64_t units = 0;
+  for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    const int64_t rows = g < G ? (int64_t)(first_of(g + 1) - first_of(g)) * R : 0;
+    const int64_t exc = plan_scan((rows + unit_rows - 1) / unit_rows, part, units);
+    if (g < G) pl.group_units[g] = (int)exc;
+  }
+  if (tid == 0) pl.group_units[G] = (int)units;
+  __syncthreads();
+  const int U = (int)units;
+  // Shared pages of every group; the parts of its units that do not depend on the others.
   for (int g = warp; g < G; g += kPlanWarps) {
-    const int lo = offsets[g], hi = offsets[g + 1];
-    int common = prefix_lens[g];
+    const int lo = first_of(g), hi = first_of(g + 1), u0 = pl.group_units[g], n = pl.group_units[g + 1] - u0;
+    int common = bad ? 0 : prefix_lens[g];
     for (int b = lo + lane; b < hi; b += 32) {
-      const int S = min(seqlens[b], max_seqlen);
-      common = min(common, max(S - n_q + 1, 0));
+      const int S = seqlens[b];
+      if (S < n_q || S > max_seqlen) report(dev_status, MLA_ERR_BAD_INDEX);
+      common = min(common, max(min(S, max_seqlen) - n_q + 1, 0));
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) common = min(common, __shfl_xor_sync(0xffffffffu, common, o));
-    int pages = common / block_size * (block_size / kPage);
-    const int64_t tiles = (pages + 1) / 2, n = hi - lo;
-    const int64_t units = (n * R + kUnitRows - 1) / kUnitRows;
-    if (units * (tiles + kUnitCost) >= n * tiles) pages = 0;
-    if (lane == 0) pl.group_pages[g] = pages;
-    for (int b = lo + lane; b < hi; b += 32) pl.own_begin[b] = pages * kPage;
+    const int shared = common / block_size * (block_size / kPage);
+    for (int b = lo + lane; b < hi; b += 32) {
+      pl.seq_shared[b] = shared;
+      pl.seq_group[b] = make_int2(u0, lo * R);
+    }
+    for (int i = lane; i < n; i += 32) {
+      const int row0 = lo * R + i * unit_rows, rows = min(unit_rows, hi * R - row0);
+      const int seq0 = row0 / R, last = (row0 + rows - 1) / R;
+      int4 *dst = reinterpret_cast<int4 *>(pl.units + u0 + i);
+      dst[0] = make_int4(0, 0, 0, shared);
+      dst[1] = make_int4(row0, rows, seq0, last - seq0 + 1);
+      dst[2] = make_int4(lo, 0, 0, 0);
+    }
   }
   __syncthreads();
-  // Two passes over the list, packed as units (low word) and tiles (high): the totals, then the units.
-  PlanOut out{pl, 0, 1};
-  int U = B;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t carry = 0;
-    for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
-      const int b = b0 + tid;
-      SharedUnit un{};
-      if (b < B) {
-        const int S = seqlens[b], begin = pl.own_begin[b];
-        const int len = min(max(S, 0), max_seqlen);
-        if (!pass && (S < n_q || S > max_seqlen)) report(dev_status, MLA_ERR_BAD_INDEX);
-        un.keys = max(len - begin, 0);
-        un.pages = (un.keys + kPage - 1) / kPage;
-        un.tiles = (un.pages + 1) / 2;
-        un.seq = b;
-        un.row0 = b * R;
-        un.rows = R;
-        un.page0 = begin / kPage;
-        un.part0 = b * R;
-        un.part_stride = R;
-        un.vis0 = len - n_q + 1 - begin;
-      }
-      const int64_t exc = plan_scan((int64_t)(un.tiles > 0) | ((int64_t)un.tiles << 32), part, carry);
-      if (pass && b < B) out.unit(b, (int)(exc >> 32), (int)(exc & 0xffffffff), un);
-    }
-    int shared = B;   // the next shared unit
-    for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
-      const int g = g0 + tid;
-      int pages = 0, units = 0;
-      if (g < G) {
-        pages = pl.group_pages[g];
-        units = pages ? (int)(((int64_t)(offsets[g + 1] - offsets[g]) * R + kUnitRows - 1) / kUnitRows) : 0;
-      }
-      const int64_t before = carry;
-      const int64_t exc = plan_scan((int64_t)units | ((int64_t)units * ((pages + 1) / 2) << 32), part, carry);
-      if (pass)
-        for (int k = 0; k < 32; ++k) {   // the warp writes its 32 groups one after another
-          const int gg = g0 + warp * 32 + k;
-          if (gg >= G) break;
-          const int64_t e = __shfl_sync(0xffffffffu, exc, k);
-          const int n = __shfl_sync(0xffffffffu, units, k), pg = __shfl_sync(0xffffffffu, pages, k);
-          const int u0 = shared + (int)((e - before) & 0xffffffff);
-          const int lo = offsets[gg], hi = offsets[gg + 1], rows = (hi - lo) * R, tiles = (pg + 1) / 2;
-          for (int b = lo + lane; b < hi; b += 32) pl.seq_group[b] = make_int2(n ? u0 : -1, lo * R);
-          for (int i = lane; i < n; i += 32) {
-            SharedUnit un{};
-            un.tiles = tiles;
-            un.pages = pg;
-            un.seq = lo;
-            un.row0 = lo * R + i * kUnitRows;
-            un.rows = min(kUnitRows, rows - i * kUnitRows);
-            un.keys = pg * kPage;
-            un.part0 = (B + clusters) * R + (u0 + i - B) * kUnitRows;
-            un.part_stride = kUnitRows;
-            un.vis0 = un.keys;
-            out.unit(u0 + i, (int)(e >> 32) + i * tiles, (int)(e & 0xffffffff) + i, un);
-          }
-        }
-      shared += (int)((carry - before) & 0xffffffff);
-    }
-    if (G == 0 && pass)
-      for (int b = tid; b < B; b += kPlanThreads) pl.seq_group[b] = make_int2(-1, 0);
-    // Every thread holds the totals.
-    const int n = (int)(carry & 0xffffffff);
-    out.W = (int)(carry >> 32) + kUnitCost * max(n - 1, 0);
-    out.C = max(1, min(out.W, clusters));
-    U = shared;
+  // Own pages before each sequence.
+  int64_t own = 0;
+  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < B) n = (max(min(seqlens[b], max_seqlen) - kPage * pl.seq_shared[b], 0) + kPage - 1) / kPage;
+    const int64_t exc = plan_scan(n, part, own);
+    if (b < B) pl.own_pages[b] = (int)exc;
   }
-  if (tid == 0) *reinterpret_cast<int4 *>(pl.head) = make_int4(out.W, out.W > 0 ? out.C : 0, U, 0);
+  if (tid == 0) pl.own_pages[B] = (int)own;
+  __syncthreads();
+  // Tiles of every unit and its place in the list; non-empty units are counted in the low word.
+  int64_t list = 0;
+  for (int u0 = 0; u0 < U; u0 += kPlanThreads) {
+    const int u = u0 + tid;
+    int pages = 0, shared = 0;
+    if (u < U) {
+      shared = reinterpret_cast<int4 *>(pl.units + u)[0].w;
+      const int4 c = reinterpret_cast<int4 *>(pl.units + u)[1];
+      pages = shared + pl.own_pages[c.z + c.w] - pl.own_pages[c.z];
+    }
+    const int tiles = (pages + 1) / 2;
+    const int64_t exc = plan_scan((int64_t)(tiles > 0) | ((int64_t)tiles << 32), part, list);
+    if (u < U)
+      reinterpret_cast<int4 *>(pl.units + u)[0] =
+          make_int4((int)(exc >> 32) + kUnitCost * (int)(exc & 0xffffffff), tiles, pages, shared);
+  }
+  const int full = (int)(list & 0xffffffff);
+  const int W = (int)(list >> 32) + kUnitCost * max(full - 1, 0);
+  const int C = min(W, clusters);
+  __syncthreads();
+  for (int u = tid; u < U; u += kPlanThreads) {
+    const int4 a = reinterpret_cast<int4 *>(pl.units + u)[0];
+    if (a.y == 0) {
+      pl.unit_parts[u] = make_int2(0, 0);
+      continue;
+    }
+    const int c0 = cluster_of(a.x, W, C), c1 = cluster_of((int64_t)a.x + a.y - 1, W, C);
+    pl.unit_parts[u] = make_int2(u + c0, c1 - c0 + 1);
+    // The clusters whose share begins behind the previous unit's last tile and not behind this one's.
+    const int from = max(a.x - kUnitCost, 0);
+    for (int x = cluster_of(from, W, C); x <= c1; ++x)
+      if ((int64_t)x * W / C >= from) pl.cluster_unit[x] = u;
+  }
+  if (tid == 0) *reinterpret_cast<int4 *>(pl.head) = make_int4(W, C, U, 0);
 }
 
 }  // namespace
@@ -1030,8 +1051,9 @@ int launch_shared_plan(const SharedPlan &pl, int B, int n_q, int H, int max_seql
              : MLA_ERR_CUDA;
 }
 
-int launch_shared_attention(const mla_dims &d, const SharedPlan &pl, const void *q_abs, const CacheView &cache,
-                            __nv_bfloat16 *o_part, float *lse_part, int *dev_status, cudaStream_t st) {
+int launch_shared_attention(const mla_dims &d, int n_q, int max_seqlen, const SharedPlan &pl, const void *q_abs,
+                            const CacheView &cache, const int32_t *seqlens, __nv_bfloat16 *o_part, float *lse_part,
+                            int *dev_status, cudaStream_t st) {
   const bool tiled = cache.layout == MLA_CACHE_TILED;
   CUtensorMap mc, mpe;
   memset(&mc, 0, sizeof(mc));
@@ -1054,6 +1076,10 @@ int launch_shared_attention(const mla_dims &d, const SharedPlan &pl, const void 
   p.num_blocks = cache.num_blocks;
   p.block_size = cache.block_size;
   p.H = d.n_heads;
+  p.n_q = n_q;
+  p.max_seqlen = max_seqlen;
+  p.seqlens = seqlens;
+  p.own_pages = pl.own_pages;
   p.scale_log2 = default_scale(d) * 1.4426950408889634f;
   p.o_part = o_part;
   p.lse_part = lse_part;
