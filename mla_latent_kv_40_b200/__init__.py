@@ -384,29 +384,47 @@ def mla_decode_shared_workspace_size(dims, B, n_q, max_seqlen, num_groups) -> in
     return int(n.value)
 
 
-def _group_args(B, group_offsets, prefix_lens):
-    """(num_groups, group_offsets, prefix_lens) as the C calls take them; both None: no groups."""
-    if (group_offsets is None) != (prefix_lens is None):
+def _check_tensors(dev, *specs):
+    """One pass over (name, tensor, dtype, shape or None): a dense CUDA tensor of that type and shape on device `dev`,
+    or None.  The tests are few and cheap, since the small calls take as long on the host as on the GPU; what is wrong
+    is worked out after one has failed."""
+    for name, t, dtype, shape in specs:
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or
+                              (shape is not None and t.shape != shape)):
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            _dense(t, name)
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _groups(B, group_offsets, prefix_lens):
+    """The number of groups, and what _check_tensors is to look at; both arrays None: no groups."""
+    if group_offsets is None and prefix_lens is None:
+        return 0, ()
+    if group_offsets is None or prefix_lens is None:
         raise ValueError("group_offsets and prefix_lens go together")
-    if group_offsets is None:
-        return 0, None, None
-    _same_shape(prefix_lens, (group_offsets.numel() - 1,), "prefix_lens")
-    if not 0 < prefix_lens.numel() <= B:
+    G = group_offsets.numel() - 1
+    if not 0 < G <= B:
         raise ValueError("there must be 1 .. B groups")
-    return (prefix_lens.numel(), _ptr(_dense(group_offsets, "group_offsets"), torch.int32, "group_offsets"),
-            _ptr(_dense(prefix_lens, "prefix_lens"), torch.int32, "prefix_lens"))
+    return G, (("group_offsets", group_offsets, torch.int32, (G + 1,)), ("prefix_lens", prefix_lens, torch.int32, (G,)))
 
 
-def _same_shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _need(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
 
 
-def _on_current_device(*tensors):
-    """The kernels run on the current device: tensors of another one are refused."""
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def mla_decode_shared(dims, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,
@@ -414,31 +432,30 @@ def mla_decode_shared(dims, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_pe
                       stream=None):
     """mla_decode for groups of sequences that share their first tokens: group_offsets [G + 1] and prefix_lens [G]
     (int32, device); the shared tokens of a group are attended to once for all its sequences.  w_uv None: out is
-    o_lat [B, n_q, H, d_c]."""
-    et = _elem_dtype(dims)
+    o_lat [B, n_q, H, d_c].  k_pe is not read (and may be None) for a tiled pool."""
+    et, i32, dev = _elem_dtype(dims), torch.int32, torch.cuda.current_device()
+    _need(q_nope=q_nope, q_pe=q_pe, c_kv=c_kv, block_table=block_table, seqlens=seqlens, w_uk=w_uk, out=out,
+          workspace=workspace)
     B, n_q = q_nope.shape[0], q_nope.shape[1]
-    for n, t in (("q_nope", q_nope), ("q_pe", q_pe), ("block_table", block_table), ("seqlens", seqlens),
-                 ("w_uk", w_uk), ("w_uv", w_uv), ("out", out), ("lse", lse)):
-        _dense(t, n)
-    H, dv = dims.n_heads, dims.d_v if w_uv is not None else dims.d_c
-    for n, t, shape in (("q_nope", q_nope, (B, n_q, H, dims.d_nope)), ("q_pe", q_pe, (B, n_q, H, dims.d_rope)),
-                        ("seqlens", seqlens, (B,)), ("block_table", block_table, (B, max_blocks_per_seq)),
-                        ("w_uk", w_uk, (H, dims.d_c, dims.d_nope)), ("w_uv", w_uv, (H, dims.d_c, dims.d_v)),
-                        ("out", out, (B, n_q, H, dv)), ("lse", lse, (B, n_q, H))):
-        if t is not None:
-            _same_shape(t, shape, n)
-    _on_current_device(q_nope, q_pe, c_kv, k_pe, block_table, seqlens, group_offsets, prefix_lens, w_uk, w_uv, out, lse,
-                       workspace, dev_status)
-    G, offs, lens = _group_args(B, group_offsets, prefix_lens)
-    rc = _lib.mla_decode_shared(ctypes.byref(dims), B, n_q, _ptr(q_nope, et, "q_nope"), _ptr(q_pe, et, "q_pe"),
-                                _ptr(c_kv, et, "c_kv"), _ptr(k_pe, et, "k_pe", True),
-                                _ptr(block_table, torch.int32, "block_table"), int(max_blocks_per_seq),
-                                int(num_blocks), _ptr(seqlens, torch.int32, "seqlens"), int(max_seqlen), G, offs, lens,
-                                _ptr(w_uk, et, "w_uk"), _ptr(w_uv, et, "w_uv", True), _ptr(out, et, "out"),
-                                _ptr(lse, torch.float32, "lse", True), _ptr(workspace, None, "workspace"),
-                                ctypes.c_size_t(workspace.numel() * workspace.element_size()),
-                                _ptr(dev_status, torch.int32, "dev_status", True), _stream(stream))
-    _check("mla_decode_shared", rc)
+    H, d_c = dims.n_heads, dims.d_c
+    G, group_specs = _groups(B, group_offsets, prefix_lens)
+    _check_tensors(dev, ("q_nope", q_nope, et, (B, n_q, H, dims.d_nope)), ("q_pe", q_pe, et, (B, n_q, H, dims.d_rope)),
+                   ("block_table", block_table, i32, (B, max_blocks_per_seq)), ("seqlens", seqlens, i32, (B,)),
+                   ("w_uk", w_uk, et, (H, d_c, dims.d_nope)), ("w_uv", w_uv, et, (H, d_c, dims.d_v)),
+                   ("out", out, et, (B, n_q, H, d_c if w_uv is None else dims.d_v)),
+                   ("lse", lse, torch.float32, (B, n_q, H)), ("workspace", workspace, workspace.dtype, None),
+                   ("dev_status", dev_status, i32, None), *group_specs)
+    for name, t in (("c_kv", c_kv), ("k_pe", k_pe)):   # pools may be strided views
+        if t is not None and (t.dtype is not et or t.get_device() != dev):
+            _ptr(t, et, name)
+            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    rc = _lib.mla_decode_shared(ctypes.byref(dims), B, n_q, q_nope.data_ptr(), q_pe.data_ptr(), c_kv.data_ptr(),
+                                _addr(k_pe), block_table.data_ptr(), max_blocks_per_seq, num_blocks, seqlens.data_ptr(),
+                                max_seqlen, G, _addr(group_offsets), _addr(prefix_lens), w_uk.data_ptr(), _addr(w_uv),
+                                out.data_ptr(), _addr(lse), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _addr(dev_status), _raw_stream(stream))
+    if rc:
+        _check("mla_decode_shared", rc)
 
 
 def mla_plan_step(dims, cached_lens, new_lens, group_offsets, prefix_lens, prefix_table, free_list, free_count,
@@ -448,61 +465,52 @@ def mla_plan_step(dims, cached_lens, new_lens, group_offsets, prefix_lens, prefi
     updated in place; seqlens [B], cu_seqlens [B + 1], seq_idx and pos [max_tokens], slots [max_tokens] (int64, or
     None) and free_count_out [1] are written.  seqlens may be cached_lens and free_count_out may be free_count.
     group_offsets, prefix_lens and prefix_table [G, max_prefix_blocks] are None without shared prefixes."""
-    i32 = torch.int32
-    B = cached_lens.numel()
-    for n, t in (("cached_lens", cached_lens), ("new_lens", new_lens), ("prefix_table", prefix_table),
-                 ("free_list", free_list), ("block_table", block_table), ("seqlens", seqlens),
-                 ("cu_seqlens", cu_seqlens), ("seq_idx", seq_idx), ("pos", pos), ("slots", slots)):
-        _dense(t, n)
-    for n, t, shape in (("new_lens", new_lens, (B,)), ("seqlens", seqlens, (B,)), ("cu_seqlens", cu_seqlens, (B + 1,)),
-                        ("pos", pos, tuple(seq_idx.shape)), ("free_count", free_count, (1,)),
-                        ("free_count_out", free_count_out, (1,))):
-        _same_shape(t, shape, n)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_blocks_per_seq]")
-    if slots is not None:
-        _same_shape(slots, seq_idx.shape, "slots")
-    _on_current_device(cached_lens, new_lens, group_offsets, prefix_lens, prefix_table, free_list, free_count,
-                       block_table, seqlens, cu_seqlens, seq_idx, pos, slots, free_count_out, dev_status)
-    G, offs, lens = _group_args(B, group_offsets, prefix_lens)
-    if G and (prefix_table is None or prefix_table.dim() != 2 or prefix_table.shape[0] != G):
-        raise ValueError("prefix_table must be [num_groups, max_prefix_blocks]")
-    rc = _lib.mla_plan_step(ctypes.byref(dims), B, _ptr(cached_lens, i32, "cached_lens"),
-                            _ptr(new_lens, i32, "new_lens"), G, offs, lens,
-                            _ptr(prefix_table, i32, "prefix_table", True), int(prefix_table.shape[1]) if G else 0,
-                            _ptr(free_list, i32, "free_list"), free_list.numel(), _ptr(free_count, i32, "free_count"),
-                            _ptr(block_table, i32, "block_table"), int(block_table.shape[1]), int(num_blocks),
-                            seq_idx.numel(), _ptr(seqlens, i32, "seqlens"), _ptr(cu_seqlens, i32, "cu_seqlens"),
-                            _ptr(seq_idx, i32, "seq_idx"), _ptr(pos, i32, "pos"),
-                            _ptr(slots, torch.int64, "slots", True), _ptr(free_count_out, i32, "free_count_out"),
-                            _ptr(dev_status, i32, "dev_status", True), _stream(stream))
-    _check("mla_plan_step", rc)
+    i32, dev = torch.int32, torch.cuda.current_device()
+    _need(cached_lens=cached_lens, new_lens=new_lens, free_list=free_list, free_count=free_count, block_table=block_table,
+          seqlens=seqlens, cu_seqlens=cu_seqlens, seq_idx=seq_idx, pos=pos, free_count_out=free_count_out)
+    B, T = cached_lens.numel(), seq_idx.numel()
+    G, group_specs = _groups(B, group_offsets, prefix_lens)
+    if block_table.dim() != 2 or (G and (prefix_table is None or prefix_table.dim() != 2)):
+        raise ValueError("block_table must be [B, max_blocks_per_seq], and prefix_table [num_groups, max_prefix_blocks]")
+    mb, mpb = block_table.shape[1], prefix_table.shape[1] if G else 0
+    _check_tensors(dev, ("cached_lens", cached_lens, i32, (B,)), ("new_lens", new_lens, i32, (B,)),
+                   ("free_list", free_list, i32, None), ("free_count", free_count, i32, (1,)),
+                   ("block_table", block_table, i32, (B, mb)), ("seqlens", seqlens, i32, (B,)),
+                   ("cu_seqlens", cu_seqlens, i32, (B + 1,)), ("seq_idx", seq_idx, i32, (T,)), ("pos", pos, i32, (T,)),
+                   ("slots", slots, torch.int64, (T,)), ("free_count_out", free_count_out, i32, (1,)),
+                   ("dev_status", dev_status, i32, None),
+                   *((("prefix_table", prefix_table, i32, (G, mpb)),) if G else ()), *group_specs)
+    rc = _lib.mla_plan_step(ctypes.byref(dims), B, cached_lens.data_ptr(), new_lens.data_ptr(), G, _addr(group_offsets),
+                            _addr(prefix_lens), _addr(prefix_table) if G else None, mpb, free_list.data_ptr(),
+                            free_list.numel(), free_count.data_ptr(), block_table.data_ptr(), mb, num_blocks, T,
+                            seqlens.data_ptr(), cu_seqlens.data_ptr(), seq_idx.data_ptr(), pos.data_ptr(), _addr(slots),
+                            free_count_out.data_ptr(), _addr(dev_status), _raw_stream(stream))
+    if rc:
+        _check("mla_plan_step", rc)
 
 
 def mla_release_blocks(dims, done, seqlens, group_offsets, prefix_lens, block_table, num_blocks, free_list,
                        free_count, seqlens_out, free_count_out, dev_status=None, stream=None):
     """The own blocks of every request with done[b] != 0 are appended to free_list; its length becomes 0.
     seqlens_out may be seqlens and free_count_out may be free_count."""
-    i32 = torch.int32
+    i32, dev = torch.int32, torch.cuda.current_device()
+    _need(done=done, seqlens=seqlens, block_table=block_table, free_list=free_list, free_count=free_count,
+          seqlens_out=seqlens_out, free_count_out=free_count_out)
     B = seqlens.numel()
-    for n, t in (("done", done), ("seqlens", seqlens), ("block_table", block_table), ("free_list", free_list),
-                 ("seqlens_out", seqlens_out)):
-        _dense(t, n)
-    for n, t, shape in (("done", done, (B,)), ("seqlens_out", seqlens_out, (B,)), ("free_count", free_count, (1,)),
-                        ("free_count_out", free_count_out, (1,))):
-        _same_shape(t, shape, n)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    G, group_specs = _groups(B, group_offsets, prefix_lens)
+    if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks_per_seq]")
-    _on_current_device(done, seqlens, group_offsets, prefix_lens, block_table, free_list, free_count, seqlens_out,
-                       free_count_out, dev_status)
-    G, offs, lens = _group_args(B, group_offsets, prefix_lens)
-    rc = _lib.mla_release_blocks(ctypes.byref(dims), B, _ptr(done, i32, "done"), _ptr(seqlens, i32, "seqlens"), G,
-                                 offs, lens, _ptr(block_table, i32, "block_table"), int(block_table.shape[1]),
-                                 int(num_blocks), _ptr(free_list, i32, "free_list"), free_list.numel(),
-                                 _ptr(free_count, i32, "free_count"), _ptr(seqlens_out, i32, "seqlens_out"),
-                                 _ptr(free_count_out, i32, "free_count_out"), _ptr(dev_status, i32, "dev_status", True),
-                                 _stream(stream))
-    _check("mla_release_blocks", rc)
+    mb = block_table.shape[1]
+    _check_tensors(dev, ("done", done, i32, (B,)), ("seqlens", seqlens, i32, (B,)), ("block_table", block_table, i32, (B, mb)),
+                   ("free_list", free_list, i32, None), ("free_count", free_count, i32, (1,)),
+                   ("seqlens_out", seqlens_out, i32, (B,)), ("free_count_out", free_count_out, i32, (1,)),
+                   ("dev_status", dev_status, i32, None), *group_specs)
+    rc = _lib.mla_release_blocks(ctypes.byref(dims), B, done.data_ptr(), seqlens.data_ptr(), G, _addr(group_offsets),
+                                 _addr(prefix_lens), block_table.data_ptr(), mb, num_blocks, free_list.data_ptr(),
+                                 free_list.numel(), free_count.data_ptr(), seqlens_out.data_ptr(),
+                                 free_count_out.data_ptr(), _addr(dev_status), _raw_stream(stream))
+    if rc:
+        _check("mla_release_blocks", rc)
 
 
 def mla_decode_latent(dims, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,

@@ -1009,13 +1009,18 @@ shared_plan_kernel(SharedPlan pl, int B, int n_q, int R, int max_seqlen, int blo
 int shared_clusters_for_device() {
   static std::atomic<int> cached[128];
   static std::mutex mu;
-  int dev = 0, ndev = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {   // no device
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev < 0 || dev >= 128) return 0;
+  if (const int c = cached[dev].load(std::memory_order_acquire)) return c;
+  int ndev = 0;
   if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev <= 0) {
     cudaGetLastError();
     return 0;
   }
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
-  if (const int c = cached[dev].load(std::memory_order_acquire)) return c;
   std::lock_guard<std::mutex> lock(mu);
   if (const int c = cached[dev].load(std::memory_order_acquire)) return c;
   if (cudaFuncSetAttribute(shared_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes)) return 0;

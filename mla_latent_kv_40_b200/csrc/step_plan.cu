@@ -9,13 +9,15 @@
 //   token t of the step belongs to the request whose range of the prefix sums of n holds t.
 // All of it is two prefix sums over the requests and one search per four tokens (or ids).
 //
-// Shape.  One cluster of kCtas CTAs does the whole call in one launch: every CTA loads the lengths and
-// forms the prefix sums in its own shared memory (redundantly: they are a few KB and the alternative is
-// a second launch), then the table entries and tokens are dealt out over all threads of the cluster.
-// The outputs that may alias inputs (lengths, free count) are written after a cluster barrier that every
-// CTA enters once it has read them, so the state of a serving loop can be updated in place, also in a
-// replayed graph.  No atomics: the result does not depend on timing.  The call is bound by latency (the
-// dependent loads of the scan and of the search), not by its bytes.
+// Shape.  Every CTA loads the lengths and forms the prefix sums in its own shared memory (redundantly: they are a few
+// KB), then the table entries and tokens are dealt out over all threads.  Outputs that may alias inputs (lengths, free
+// count) are written only when every CTA has read them, so that the state of a serving loop can be updated in place,
+// also in a replayed graph.  Two forms of that:
+//   * little work: one cluster of kCtas CTAs in one launch, with a cluster barrier before those outputs;
+//   * much work: kBodyCtas CTAs that leave those outputs alone, and a second launch of one CTA that forms the sums again
+//     (while the first kernel runs) and writes them once that has finished.
+// No atomics: the result does not depend on timing.  The call is bound by latency (the dependent loads of the scan and
+// of the search), not by its bytes.
 #include "kernels.cuh"
 #include "sm100.cuh"
 
@@ -25,6 +27,11 @@ namespace {
 using namespace sm100;
 
 constexpr int kCtas = 8;          // the largest portable cluster
+constexpr int kBodyCtas = 128;
+// Up to so many words that a call may have to write, one cluster takes it.
+constexpr int64_t kWholeWords = 65536;
+// What one launch is to do.
+enum Mode { kWhole, kBody, kFinish };
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 4;           // consecutive tokens (or block ids) per thread and search
@@ -107,7 +114,8 @@ __device__ __forceinline__ void fill_groups(int B, int G, const int32_t *offsets
 
 __device__ __forceinline__ int blocks_of(int tokens, int bs) { return tokens / bs + (tokens % bs != 0); }
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) step_plan_kernel(const StepPlanArgs a) {
+template <Mode kMode>
+__global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanArgs a) {
   extern __shared__ int32_t sm[];
   __shared__ long long part[kWarps];
   __shared__ int s_taken;
@@ -116,14 +124,18 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) step_p
   int32_t *cum = cu + B + 1;           // [B + 1] first new block of each request
   int32_t *held = cum + B + 1;         // [B] cached tokens; ~cached where the request is refused
   int32_t *gid = held + B;             // [B] group; then, where the request joins its prefix, still the group, else -1
-  const int rank = (int)cluster_ctarank();
+  const int rank = blockIdx.x, threads = gridDim.x * kThreads;
   const int gtid = rank * kThreads + tid;
+  // The finishing launch may form its sums while this one runs.  The other modes let nothing start early: kernels behind
+  // them read lengths and positions before they wait for their predecessor.
+  if (kMode == kBody) grid_dep_launch();
+  int *const status = kMode == kFinish ? nullptr : a.dev_status;   // each error is reported by one launch
   const int per = (B + kThreads - 1) / kThreads;
 
-  fill_groups(B, a.num_groups, a.group_offsets, gid, rank == 0 ? a.dev_status : nullptr);
+  fill_groups(B, a.num_groups, a.group_offsets, gid, rank == 0 ? status : nullptr);
   int free = *a.free_count;
   if (free < 0 || free > a.free_capacity) {
-    if (gtid == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+    if (gtid == 0) report(status, MLA_ERR_BAD_INDEX);
     free = free < 0 ? 0 : a.free_capacity;
   }
   // Lengths and refusals that do not depend on the other requests.
@@ -138,7 +150,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) step_p
     cu[b] = n;
     held[b] = bad ? ~max(c, 0) : c;
     if (bad || P <= 0 || c != P) gid[b] = -1;
-    if (bad && rank == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+    if (bad && rank == 0) report(status, MLA_ERR_BAD_INDEX);
   }
   __syncthreads();
   // First tokens.  cum holds the token counts meanwhile.
@@ -151,7 +163,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) step_p
       if (held[b] >= 0 && cum[b] > 0 && (long long)cu[b] + cum[b] > a.max_tokens) {
         held[b] = ~held[b];
         gid[b] = -1;
-        if (rank == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+        if (rank == 0) report(status, MLA_ERR_BAD_INDEX);
       }
     __syncthreads();
   }
@@ -178,7 +190,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) step_p
         } else {                   // the free list ends here: this request and every later one that needs a block
           held[b] = ~held[b];
           gid[b] = -1;
-          if (rank == 0) report(a.dev_status, MLA_ERR_NO_BLOCKS);
+          if (rank == 0) report(status, MLA_ERR_NO_BLOCKS);
         }
       }
     }
@@ -195,100 +207,109 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) step_p
     __syncthreads();
   }
   const int taken = s_taken;
-  // Every CTA has read the lengths and the free count.
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (kMode == kWhole) {   // this CTA has read the lengths and the free count
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
 
-  // New table entries.
-  for (int k0 = gtid * kPer; k0 < taken; k0 += kCtas * kThreads * kPer) {
-    int b = last_le(cum, B, k0);
+  if (kMode != kFinish) {
+    // New table entries.
+    for (int k0 = gtid * kPer; k0 < taken; k0 += threads * kPer) {
+      int b = last_le(cum, B, k0);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int k = k0 + i;
-      if (k >= taken) break;
-      while (b + 1 < B && cum[b + 1] <= k) ++b;
-      int id = a.free_list[free - 1 - k];
-      if (id < 0 || id >= a.num_blocks) {
-        report(a.dev_status, MLA_ERR_BAD_INDEX);
-        id = -1;
+      for (int i = 0; i < kPer; ++i) {
+        const int k = k0 + i;
+        if (k >= taken) break;
+        while (b + 1 < B && cum[b + 1] <= k) ++b;
+        int id = a.free_list[free - 1 - k];
+        if (id < 0 || id >= a.num_blocks) {
+          report(status, MLA_ERR_BAD_INDEX);
+          id = -1;
+        }
+        a.block_table[(int64_t)b * a.max_blocks_per_seq + blocks_of(held[b], bs) + (k - cum[b])] = id;
       }
-      a.block_table[(int64_t)b * a.max_blocks_per_seq + blocks_of(held[b], bs) + (k - cum[b])] = id;
     }
-  }
-  // The shared blocks of requests that join their group's prefix.
-  for (int b = gtid >> 5; b < B; b += kCtas * kWarps) {
-    const int g = gid[b];
-    if (g < 0) continue;
-    const int np = held[b] / bs;
-    const int32_t *src = a.prefix_table + (int64_t)g * a.max_prefix_blocks;
-    int32_t *dst = a.block_table + (int64_t)b * a.max_blocks_per_seq;
-    for (int i = tid & 31; i < np; i += 32) dst[i] = src[i];
-  }
-  // Tokens: request, position and pool row.
-  const int T = cu[B];
-  for (int t0 = gtid * kPer; t0 < T; t0 += kCtas * kThreads * kPer) {
-    int b = last_le(cu, B, t0);
-    int32_t sq[kPer], ps[kPer];
-    int64_t sl[kPer];
-    int at_b = -1, at_l = -1;
-    int32_t blk = -1;
+    // The shared blocks of requests that join their group's prefix.
+    for (int b = gtid >> 5; b < B; b += threads / 32) {
+      const int g = gid[b];
+      if (g < 0) continue;
+      const int np = held[b] / bs;
+      const int32_t *src = a.prefix_table + (int64_t)g * a.max_prefix_blocks;
+      int32_t *dst = a.block_table + (int64_t)b * a.max_blocks_per_seq;
+      for (int i = tid & 31; i < np; i += 32) dst[i] = src[i];
+    }
+    // Tokens: request, position and pool row.
+    const int T = cu[B];
+    for (int t0 = gtid * kPer; t0 < T; t0 += threads * kPer) {
+      int b = last_le(cu, B, t0);
+      int32_t sq[kPer], ps[kPer];
+      int64_t sl[kPer];
+      int at_b = -1, at_l = -1;
+      int32_t blk = -1;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = t0 + i;
-      sq[i] = ps[i] = -1;
-      sl[i] = -1;
-      if (t < T) {
-        while (b + 1 < B && cu[b + 1] <= t) ++b;
-        const int c = held[b];
-        if (c >= 0) {
-          const int p = c + (t - cu[b]), l = p / bs, have = blocks_of(c, bs);
-          if (b != at_b || l != at_l) {
-            blk = l < have ? a.block_table[(int64_t)b * a.max_blocks_per_seq + l]
-                           : a.free_list[free - 1 - (cum[b] + l - have)];
-            if (blk < 0 || blk >= a.num_blocks) {
-              report(a.dev_status, MLA_ERR_BAD_INDEX);
-              blk = -1;
+      for (int i = 0; i < kPer; ++i) {
+        const int t = t0 + i;
+        sq[i] = ps[i] = -1;
+        sl[i] = -1;
+        if (t < T) {
+          while (b + 1 < B && cu[b + 1] <= t) ++b;
+          const int c = held[b];
+          if (c >= 0) {
+            const int p = c + (t - cu[b]), l = p / bs, have = blocks_of(c, bs);
+            if (b != at_b || l != at_l) {
+              blk = l < have ? a.block_table[(int64_t)b * a.max_blocks_per_seq + l]
+                             : a.free_list[free - 1 - (cum[b] + l - have)];
+              if (blk < 0 || blk >= a.num_blocks) {
+                report(status, MLA_ERR_BAD_INDEX);
+                blk = -1;
+              }
+              at_b = b;
+              at_l = l;
             }
-            at_b = b;
-            at_l = l;
-          }
-          if (blk >= 0) {
-            sq[i] = b;
-            ps[i] = p;
-            sl[i] = (int64_t)blk * bs + p % bs;
+            if (blk >= 0) {
+              sq[i] = b;
+              ps[i] = p;
+              sl[i] = (int64_t)blk * bs + p % bs;
+            }
           }
         }
       }
-    }
-    if (a.vec && t0 + kPer <= T) {
-      *reinterpret_cast<int4 *>(a.seq_idx + t0) = make_int4(sq[0], sq[1], sq[2], sq[3]);
-      *reinterpret_cast<int4 *>(a.pos + t0) = make_int4(ps[0], ps[1], ps[2], ps[3]);
-      if (a.slots) {
-        *reinterpret_cast<longlong2 *>(a.slots + t0) = make_longlong2(sl[0], sl[1]);
-        *reinterpret_cast<longlong2 *>(a.slots + t0 + 2) = make_longlong2(sl[2], sl[3]);
-      }
-    } else {
+      if (a.vec && t0 + kPer <= T) {
+        *reinterpret_cast<int4 *>(a.seq_idx + t0) = make_int4(sq[0], sq[1], sq[2], sq[3]);
+        *reinterpret_cast<int4 *>(a.pos + t0) = make_int4(ps[0], ps[1], ps[2], ps[3]);
+        if (a.slots) {
+          *reinterpret_cast<longlong2 *>(a.slots + t0) = make_longlong2(sl[0], sl[1]);
+          *reinterpret_cast<longlong2 *>(a.slots + t0 + 2) = make_longlong2(sl[2], sl[3]);
+        }
+      } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (t0 + i < T) {
-          a.seq_idx[t0 + i] = sq[i];
-          a.pos[t0 + i] = ps[i];
-          if (a.slots) a.slots[t0 + i] = sl[i];
-        }
+        for (int i = 0; i < kPer; ++i)
+          if (t0 + i < T) {
+            a.seq_idx[t0 + i] = sq[i];
+            a.pos[t0 + i] = ps[i];
+            if (a.slots) a.slots[t0 + i] = sl[i];
+          }
+      }
     }
+    for (int b = gtid; b <= B; b += threads) a.cu_seqlens[b] = cu[b];
   }
-  for (int b = gtid; b <= B; b += kCtas * kThreads) a.cu_seqlens[b] = cu[b];
+  if (kMode == kBody) return;
   // In-place outputs.  new = cu[b + 1] - cu[b] for a served request (refused ones keep what they held).
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  for (int b = gtid; b < B; b += kCtas * kThreads) {
+  if (kMode == kWhole) {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    grid_dep_wait();
+  }
+  for (int b = gtid; b < B; b += threads) {
     const int c = held[b];
     a.seqlens[b] = c >= 0 ? c + (cu[b + 1] - cu[b]) : ~c;
   }
   if (gtid == 0) *a.free_count_out = free - taken;
 }
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) {
+template <Mode kMode>
+__global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) {
   extern __shared__ int32_t sm[];
   __shared__ long long part[kWarps];
   __shared__ int s_put;
@@ -297,14 +318,18 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) releas
   int32_t *first = cum + B + 1;        // [B] first own table entry
   int32_t *left = first + B;           // [B] length after the call
   int32_t *gid = left + B;             // [B] group
-  const int rank = (int)cluster_ctarank();
+  const int rank = blockIdx.x, threads = gridDim.x * kThreads;
   const int gtid = rank * kThreads + tid;
+  // The finishing launch may form its sums while this one runs.  The other modes let nothing start early: kernels behind
+  // them read lengths and positions before they wait for their predecessor.
+  if (kMode == kBody) grid_dep_launch();
+  int *const status = kMode == kFinish ? nullptr : a.dev_status;   // each error is reported by one launch
   const int per = (B + kThreads - 1) / kThreads;
 
-  fill_groups(B, a.num_groups, a.group_offsets, gid, rank == 0 ? a.dev_status : nullptr);
+  fill_groups(B, a.num_groups, a.group_offsets, gid, rank == 0 ? status : nullptr);
   int free = *a.free_count;
   if (free < 0 || free > a.free_capacity) {
-    if (gtid == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+    if (gtid == 0) report(status, MLA_ERR_BAD_INDEX);
     free = free < 0 ? 0 : a.free_capacity;
   }
   for (int b = tid; b < B; b += kThreads) {
@@ -315,7 +340,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) releas
     first[b] = 0;
     if (a.done[b]) {
       if (n < 0 || P < 0 || P % bs != 0 || blocks_of(n, bs) > a.max_blocks_per_seq) {
-        if (rank == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+        if (rank == 0) report(status, MLA_ERR_BAD_INDEX);
       } else {
         own = max(0, blocks_of(n, bs) - P / bs);
         first[b] = P / bs;
@@ -342,7 +367,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) releas
           put = (int)at;
         } else {                   // the list is full: this request and every later one keeps its blocks
           left[b] = a.seqlens[b];
-          if (rank == 0) report(a.dev_status, MLA_ERR_BAD_INDEX);
+          if (rank == 0) report(status, MLA_ERR_BAD_INDEX);
         }
       }
     }
@@ -359,44 +384,77 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) releas
     __syncthreads();
   }
   const int put = s_put;
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  for (int k0 = gtid * kPer; k0 < put; k0 += kCtas * kThreads * kPer) {
-    int b = last_le(cum, B, k0);
+  if (kMode == kWhole) {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  if (kMode != kFinish) {
+    for (int k0 = gtid * kPer; k0 < put; k0 += threads * kPer) {
+      int b = last_le(cum, B, k0);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int k = k0 + i;
-      if (k >= put) break;
-      while (b + 1 < B && cum[b + 1] <= k) ++b;
-      const int id = a.block_table[(int64_t)b * a.max_blocks_per_seq + first[b] + (k - cum[b])];
-      if (id < 0 || id >= a.num_blocks) report(a.dev_status, MLA_ERR_BAD_INDEX);
-      a.free_list[free + k] = id;
+      for (int i = 0; i < kPer; ++i) {
+        const int k = k0 + i;
+        if (k >= put) break;
+        while (b + 1 < B && cum[b + 1] <= k) ++b;
+        const int id = a.block_table[(int64_t)b * a.max_blocks_per_seq + first[b] + (k - cum[b])];
+        if (id < 0 || id >= a.num_blocks) report(status, MLA_ERR_BAD_INDEX);
+        a.free_list[free + k] = id;
+      }
     }
   }
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  for (int b = gtid; b < B; b += kCtas * kThreads) a.seqlens_out[b] = left[b];
+  if (kMode == kBody) return;
+  if (kMode == kWhole) {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    grid_dep_wait();
+  }
+  for (int b = gtid; b < B; b += threads) a.seqlens_out[b] = left[b];
   if (gtid == 0) *a.free_count_out = free + put;
 }
 
+using Cache = std::atomic<int>[kSmemCacheDevs];
+
+// One launch of a bookkeeping kernel: a cluster (kWhole), many CTAs (kBody), or one that may begin while the launch
+// before it is still running (kFinish).
 template <typename Args>
-int launch_cluster(void (*kernel)(Args), const Args &a, size_t smem, std::atomic<int> (&cache)[kSmemCacheDevs],
-                   cudaStream_t st) {
+int launch(Mode mode, void (*kernel)(Args), const Args &a, size_t smem, Cache &cache, cudaStream_t st) {
   if (smem_limit(kernel, smem, cache) != cudaSuccess) return MLA_ERR_CUDA;
-  kernel<<<kCtas, kThreads, smem, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  if (mode == kFinish) return launch_pdl(kernel, dim3(1), dim3(kThreads), smem, st, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(mode == kWhole ? kCtas : kBodyCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = mode == kWhole ? kCtas : 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace
 
 int launch_step_plan(const StepPlanArgs &a, cudaStream_t st) {
-  static std::atomic<int> cache[kSmemCacheDevs];
-  return launch_cluster(step_plan_kernel, a, (size_t)(4 * a.B + 2) * sizeof(int32_t), cache, st);
+  static Cache cache[3];
+  const size_t smem = (size_t)(4 * a.B + 2) * sizeof(int32_t);
+  // The most that the call can have to write: its tokens, and whole table rows of joining requests.
+  const int64_t most = (int64_t)a.max_tokens + (int64_t)a.B * min(a.max_prefix_blocks, a.max_blocks_per_seq);
+  if (most <= kWholeWords) return launch(kWhole, step_plan_kernel<kWhole>, a, smem, cache[0], st);
+  const int rc = launch(kBody, step_plan_kernel<kBody>, a, smem, cache[1], st);
+  return rc ? rc : launch(kFinish, step_plan_kernel<kFinish>, a, smem, cache[2], st);
 }
 
 int launch_release(const ReleaseArgs &a, cudaStream_t st) {
-  static std::atomic<int> cache[kSmemCacheDevs];
-  return launch_cluster(release_kernel, a, (size_t)(4 * a.B + 1) * sizeof(int32_t), cache, st);
+  static Cache cache[3];
+  const size_t smem = (size_t)(4 * a.B + 1) * sizeof(int32_t);
+  const int64_t most = min((int64_t)a.B * a.max_blocks_per_seq, (int64_t)a.free_capacity);
+  if (most <= kWholeWords) return launch(kWhole, release_kernel<kWhole>, a, smem, cache[0], st);
+  const int rc = launch(kBody, release_kernel<kBody>, a, smem, cache[1], st);
+  return rc ? rc : launch(kFinish, release_kernel<kFinish>, a, smem, cache[2], st);
 }
 
 }  // namespace mla
