@@ -55,7 +55,9 @@ constexpr int kSoftWarps = 8;
 constexpr uint32_t kChunkBytes = kPage * 128;      // [64 keys x 64 dims] bf16, 128-byte swizzled
 constexpr int kKStages = 4;                        // half pages: chunks 0-3, then 4-8
 __host__ __device__ constexpr int half_chunks(int half) { return half ? 5 : 4; }
-constexpr uint32_t kKStageBytes = 5 * kChunkBytes;
+// Even stages take first halves, odd ones second halves.
+__host__ __device__ constexpr uint32_t k_stage_off(int s) { return (s >> 1) * 9 * kChunkBytes + (s & 1) * 4 * kChunkBytes; }
+static_assert(kKStages % 2 == 0, "a stage always holds the same half");
 constexpr int kVStages = 4;                        // a page's 256 latent dims of this CTA
 constexpr uint32_t kVStageBytes = 4 * kChunkBytes;
 constexpr uint32_t kPBytes = kRows * kPage * 2;
@@ -66,9 +68,10 @@ constexpr uint32_t kPTxBytes = kPBytes + 4 * kPaWords * 4;
 constexpr uint32_t kPSlotBytes = ((kPTxBytes + 1023) / 1024) * 1024;
 constexpr uint32_t kQpeOff = 0;
 constexpr uint32_t kKOff = kRows * 128;
-constexpr uint32_t kStgOff = kKOff + kKStages * kKStageBytes;
+constexpr uint32_t kStgOff = kKOff + k_stage_off(kKStages);
+constexpr int kStgTiles = 3;                       // staged pages of P, shared by the two softmax groups in turn
 constexpr uint32_t kPOff = kVStages * kVStageBytes;
-constexpr uint32_t kScoreEnd = kStgOff + 2 * kPSlotBytes, kValueEnd = kPOff + kPSlots * kPSlotBytes;
+constexpr uint32_t kScoreEnd = kStgOff + kStgTiles * kPSlotBytes, kValueEnd = kPOff + kPSlots * kPSlotBytes;
 constexpr uint32_t kRegion = ((kScoreEnd > kValueEnd ? kScoreEnd : kValueEnd) + 1023) & ~1023u;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s per wait
@@ -85,9 +88,9 @@ enum Bar {
   B_QREADY = B_SEMPTY + 2,              // rank 0: both CTAs' queries are in place
   B_PEMPTY = B_QREADY + 1,              // score: the value CTA's P slot may be written
   B_STATSEMPTY = B_PEMPTY + kPSlots,    // score: the value CTA has read the row statistics
-  B_STGFULL = B_STATSEMPTY + 1,         // score: a page of P is staged, per softmax group
-  B_STGEMPTY = B_STGFULL + 2,           // score: its copy has read the staging tile
-  B_CFULL = B_STGEMPTY + 2,             // value: own latents have landed; at rank 2 also: rank 3 is ready for the page
+  B_STGFULL = B_STATSEMPTY + 1,         // score: a page of P is staged
+  B_STGEMPTY = B_STGFULL + kStgTiles,   // score: its copy has read the staging tile
+  B_CFULL = B_STGEMPTY + kStgTiles,         // value: own latents have landed; at rank 2 also: rank 3 is ready for the page
   B_CEMPTY = B_CFULL + kVStages,        // value: the MMAs have read the stage (both CTAs)
   B_PFULL = B_CEMPTY + kVStages,        // value: a page of P has landed
   B_PVDONE = B_PFULL + kPSlots,         // value: the page's MMAs are complete (both CTAs)
@@ -308,7 +311,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
       if (i >= B_SEMPTY && i < B_SEMPTY + 2) n = kSoftWarps;   // four warps of each CTA
       if (lead && ((i >= B_KFULL && i < B_KFULL + kKStages) || (i >= B_CFULL && i < B_CFULL + kVStages))) n = 2;
       if (i == B_STATSEMPTY || i == B_REQDONE) n = kSoftWarps;
-      if (i >= B_STGFULL && i < B_STGFULL + 2) n = 4;
+      if (i >= B_STGFULL && i < B_STGFULL + kStgTiles) n = 4;
       if (i == B_STATSFULL) n = kRows;
       mbar_init(bar(i), n);
     }
@@ -360,7 +363,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
                   mbar_arrive(bar(B_KFULL + s));
                   continue;
                 }
-                const uint32_t dst = smem_u32(tiles + kKOff + s * kKStageBytes);
+                const uint32_t dst = smem_u32(tiles + kKOff + k_stage_off(s));
                 const int c0 = 4 * half, nc = half_chunks(half);
                 mbar_expect_tx(bar(B_KFULL + s), nc * kChunkBytes);
                 if (p.tiled)
@@ -398,7 +401,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
               ok = ok && waitw(sm, bar(B_KFULL + s), par, p.dev_status);
               if (!ok) break;
               tc_fence_after();
-              const uint64_t kd = smem_desc_sw128(smem_u32(tiles + kKOff + s * kKStageBytes), 16, 1024);
+              const uint64_t kd = smem_desc_sw128(smem_u32(tiles + kKOff + k_stage_off(s)), 16, 1024);
 #pragma unroll
               for (int c = 0; c < half_chunks(half); ++c) {
                 const int j = 4 * half + c;
@@ -425,30 +428,26 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             ok = wait1(sm, bar(B_KFULL + s), (n / kKStages) & 1, p.dev_status);
             if (ok) mbar_arrive_cluster_light(kpeer + 8 * s);
           }
-      } else if (warp >= 2 && lane == 0) {
-        // ---- sender of softmax group h = warp - 2: every staged page goes to the value CTA of these rows, into the slot
-        // of its place in the unit's pages, once the MMAs that read the slot before are complete.
-        const int h = warp - 2;
+      } else if (warp == 2 && lane == 0) {
+        // ---- sender: every staged page, in order, to the value CTA of these rows, once the MMAs that read the slot before
+        // are complete.  A staging tile is given back when the page after it is under way.  That the tiles come back in
+        // order is what lets both softmax groups wait for them by parity: whoever stages page q has seen page q - 6
+        // given back (with its own page before q, at most three earlier, it waited for a page at or behind q - 6).
         const uint32_t mate = 2 + side;
         const uint32_t pslot_remote = mapa(smem_u32(tiles + kPOff), mate), pfull_remote = mapa(bar(B_PFULL), mate);
-        const uint32_t stg = smem_u32(tiles + kStgOff + h * kPSlotBytes);
-        uint32_t ns = 0, np = 0, nst = 0;
+        uint32_t pn = 0;
         bool ok = true;
         while (ok && it.next(p))
-          for (int t = it.t0; ok && t < it.t1; ++t, ++ns) {
-            const int npg = min(2, it.un.pages - 2 * t);
-            if ((int)(ns & 1) == h)
-              for (int pg = 0; ok && pg < npg; ++pg, ++nst) {
-                const uint32_t pn = np + pg, pb = pn % kPSlots;
-                ok = wait1(sm, bar(B_STGFULL + h), nst & 1, p.dev_status) &&
-                     (pn < kPSlots || wait1(sm, bar(B_PEMPTY + pb), (pn / kPSlots - 1) & 1, p.dev_status));
-                if (!ok) break;
-                bulk_copy_to_peer(pslot_remote + pb * kPSlotBytes, stg, kPTxBytes, pfull_remote + 8 * pb);
-                bulk_commit();
-                bulk_wait_read_all();
-                mbar_arrive(bar(B_STGEMPTY + h));
-              }
-            np += npg;
+          for (int g = 2 * it.t0; g < it.pages_end(); ++g, ++pn) {
+            const uint32_t pb = pn % kPSlots, sg = pn % kStgTiles;
+            ok = wait1(sm, bar(B_STGFULL + sg), (pn / kStgTiles) & 1, p.dev_status) &&
+                 (pn < kPSlots || wait1(sm, bar(B_PEMPTY + pb), (pn / kPSlots - 1) & 1, p.dev_status));
+            if (!ok) break;
+            bulk_copy_to_peer(pslot_remote + pb * kPSlotBytes, smem_u32(tiles + kStgOff + sg * kPSlotBytes), kPTxBytes,
+                              pfull_remote + 8 * pb);
+            bulk_commit();
+            bulk_wait_read_but_last();
+            if (pn > 0) mbar_arrive(bar(B_STGEMPTY + (pn - 1) % kStgTiles));
           }
         bulk_wait_all();   // the copies have landed before the CTA may exit
       }
@@ -573,21 +572,20 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
     const int q4 = warp & 3, h = (warp - 4) >> 2;
     const int r = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    unsigned char *stgp = tiles + kStgOff + h * kPSlotBytes;
-    unsigned char *stga = stgp + kPBytes;
-    unsigned char *prow = stgp + 4096 * q4 + (lane >> 3) * 1024 + (lane & 7) * 128;
-    uint32_t ns = 0, nst = 0, uc = 0;                     // nst: pages staged by this group
-    // This warp's part of the staging tile may be written once the previous copy out of it has been read.
-    auto staging_free = [&]() {
-      if (nst > 0) waitw(sm, bar(B_STGEMPTY + h), (nst - 1) & 1, p.dev_status);
+    uint32_t ns = 0, np = 0, uc = 0;
+    // The staging tile of page pn, once the copy of page pn - kStgTiles has read it.  (The copies of earlier pages do not
+    // wait for this one, whichever group stages them.)
+    auto staging = [&](uint32_t pn) {
+      if (pn >= kStgTiles)
+        waitw(sm, bar(B_STGEMPTY + pn % kStgTiles), (pn / kStgTiles - 1) & 1, p.dev_status);
+      return tiles + kStgOff + (pn % kStgTiles) * kPSlotBytes;
     };
     while (it.next(p)) {
       // Queries of the unit: latent dims 256 h .. of the warp's rows into tensor memory, coalesced through the warp's
-      // part of the P staging tile (whose last copy must have been read); half 0 also stages the RoPE dims.  Both
+      // part of a P staging tile (one that the unit's first two pages will use); half 0 also stages the RoPE dims.  Both
       // groups have read the last S of the previous unit, so its MMAs are complete.
       {
-        staging_free();
-        unsigned char *stg_w = stgp + q4 * 4096;
+        unsigned char *stg_w = staging(np + h) + q4 * 4096;
         const int j = lane & 7;
         // This lane's rows are r0, r0 + 4, .. of the unit, contiguous in memory.
         const int r0 = kRows * (int)side + q4 * 32 + (lane >> 3);
@@ -644,8 +642,10 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
       float m_mine = -CUDART_INF_F, l = 0.f;   // l: this group's row sum, relative to m_mine
       const uint32_t ns_end = ns + (uint32_t)(it.t1 - it.t0);
       for (int t = it.t0; t < it.t1; ++t, ++ns) {
-        if ((int)(ns & 1) != h) continue;   // the other group's
         const int npg = min(2, it.un.pages - 2 * t);
+        const uint32_t pn = np;             // the tile's first page
+        np += npg;
+        if ((int)(ns & 1) != h) continue;   // the other group's
         waitw(sm, bar(B_SFULL + h), (ns >> 1) & 1, p.dev_status);
         tc_fence_after();
         const uint32_t scol = tbase + lane_off + kSCol + 128 * h;
@@ -721,33 +721,30 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             }
         };
         // The first page of a tile carries its rows' rescale factors.
-        auto stage = [&](float factor, bool flag) {
-          staging_free();
+        auto stage = [&](uint32_t page, float factor, bool flag) {
+          unsigned char *stg = staging(page);
+          unsigned char *prow = stg + 4096 * q4 + (lane >> 3) * 1024 + (lane & 7) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             *reinterpret_cast<uint4 *>(prow + ((c ^ (lane & 7)) << 4)) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-          float *pa = reinterpret_cast<float *>(stga) + q4 * kPaWords;
+          float *pa = reinterpret_cast<float *>(stg + kPBytes) + q4 * kPaWords;
           pa[lane] = factor;
           if (lane < 4) reinterpret_cast<uint32_t *>(pa + 32)[lane] = (lane == 0 && flag) ? 1u : 0u;
           fence_proxy_async_smem();
-          ++nst;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_STGFULL + page % kStgTiles));
         };
         page_p();
-        load_page(1);                 // in flight while the first page is staged (unused columns where there is no page)
-        stage(alpha, moved != 0);
+        load_page(1);                 // (unused columns where there is no second page)
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(B_STGFULL + h));
-          mbar_arrive_cluster_light(mapa(bar(B_SEMPTY + h), 0));   // the last read of this S is done
-        }
+        if (lane == 0) mbar_arrive_cluster_light(mapa(bar(B_SEMPTY + h), 0));   // the last read of this S is done
+        stage(pn, alpha, moved != 0);
         if (npg == 2) {
           mask_page(n1);
           page_p();
-          stage(1.f, false);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_STGFULL + h));
+          stage(pn + 1, 1.f, false);
         }
         l += psum0 + psum1;
       }
