@@ -217,7 +217,7 @@ AbsorbedLayout absorbed_layout(const mla_dims *d, int d_cq, int B, int n_q, int 
 
 // Decode over shared prefixes (tensor-core shapes): the absorbed queries, the plan, and the units' partials.
 struct SharedLayout {
-  size_t q_off, head_off, cluster_off, units_off, parts_off, seq_off, own_off, shared_off, groups_off, o_off, lse_off, total;
+  size_t q_off, shares_off, units_off, parts_off, seq_off, own_off, scratch_off, o_off, lse_off, total;
 };
 
 SharedLayout shared_layout(const mla_dims *d, int B, int n_q, int num_groups) {
@@ -235,14 +235,12 @@ SharedLayout shared_layout(const mla_dims *d, int B, int n_q, int num_groups) {
     return at;
   };
   L.q_off = take((size_t)B * R * (d->d_c + d->d_rope) * 2);
-  L.head_off = take(16);
-  L.cluster_off = take((size_t)clusters * sizeof(int));
+  L.shares_off = take((size_t)clusters * sizeof(SharedShare));
   L.units_off = take((size_t)units * sizeof(SharedUnit));
   L.parts_off = take((size_t)units * sizeof(int2));
   L.seq_off = take((size_t)B * sizeof(int2));
   L.own_off = take((size_t)(B + 1) * sizeof(int));
-  L.shared_off = take((size_t)B * sizeof(int));
-  L.groups_off = take((size_t)(num_groups + 1) * sizeof(int));
+  L.scratch_off = take(shared_plan_words(B, units, num_groups) * sizeof(int));
   L.o_off = take(rows * d->d_c * 2);
   L.lse_off = take(rows * sizeof(float));
   L.total = off;
@@ -450,22 +448,27 @@ int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *q_nope, 
     return MLA_ERR_INVALID_ARG;
   char *ws = static_cast<char *>(workspace);
   void *qbuf = ws + L.q_off;
-  const SharedPlan pl{reinterpret_cast<int *>(ws + L.head_off), reinterpret_cast<int *>(ws + L.cluster_off),
-                      reinterpret_cast<SharedUnit *>(ws + L.units_off), reinterpret_cast<int2 *>(ws + L.parts_off),
-                      reinterpret_cast<int2 *>(ws + L.seq_off), reinterpret_cast<int *>(ws + L.own_off),
-                      reinterpret_cast<int *>(ws + L.shared_off), reinterpret_cast<int *>(ws + L.groups_off)};
+  const SharedPlan pl{reinterpret_cast<SharedShare *>(ws + L.shares_off), reinterpret_cast<SharedUnit *>(ws + L.units_off),
+                      reinterpret_cast<int2 *>(ws + L.parts_off), reinterpret_cast<int2 *>(ws + L.seq_off),
+                      reinterpret_cast<int *>(ws + L.own_off), reinterpret_cast<int *>(ws + L.scratch_off)};
   __nv_bfloat16 *o_part = reinterpret_cast<__nv_bfloat16 *>(ws + L.o_off);
   float *lse_part = reinterpret_cast<float *>(ws + L.lse_off);
   const CacheView cv{c_kv, k_pe, dims->ckv_stride, dims->kpe_stride, block_table, max_blocks_per_seq, num_blocks,
                      dims->block_size, dims->cache_layout, dims->d_c, dims->d_c + dims->d_rope};
-  // (1) Who shares what and which cluster does what, (2) the latent queries, (3) the shared keys for all rows of a
-  // group and every sequence's own keys, (4) the merge of the partials and W_UV.
-  if ((rc = launch_shared_plan(pl, B, n_q, dims->n_heads, max_seqlen, dims->block_size, num_groups, group_offsets,
-                               prefix_lens, seqlens, dev_status, st)))
-    return rc;
+  // (1) Who shares what and which cluster does what, and the latent queries; (2) the shared keys for all rows of a group
+  // and every sequence's own keys; (3) the merge of the partials and W_UV.
+  const SharedPlanArgs plan{pl, B, n_q, n_q * dims->n_heads, max_seqlen, dims->block_size, num_groups,
+                            shared_max_units(B, n_q * dims->n_heads, num_groups), shared_clusters_for_device(),
+                            group_offsets, prefix_lens, seqlens, dev_status};
+  if (plan.clusters <= 0) return MLA_ERR_CUDA;
   const AbsorbArgs ab{B, n_q, dims->n_heads, dims->d_c, dims->d_rope, dims->d_nope,
                       q_nope, q_pe, w_uk, seqlens, qbuf, dims->rope_base};
-  if ((rc = absorb_dispatch(ab, true, dev_status, st))) return rc;
+  if (absorb_tc_supported(ab, true)) {
+    if ((rc = launch_absorb_plan(ab, plan, dev_status, st))) return rc;
+  } else {
+    if ((rc = launch_shared_plan(plan, st))) return rc;
+    if ((rc = absorb_dispatch(ab, true, dev_status, st))) return rc;
+  }
   if ((rc = launch_shared_attention(*dims, n_q, max_seqlen, pl, qbuf, cv, seqlens, o_part, lse_part, dev_status, st))) return rc;
   const SharedPieces pc{o_part, lse_part, pl.unit_parts, pl.seq_group, n_q, dims->n_heads,
                         shared_unit_rows(n_q * dims->n_heads)};

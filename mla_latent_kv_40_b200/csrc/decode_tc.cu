@@ -1218,17 +1218,19 @@ shared_merge_kernel(const SharedPieces pc, int rows, __nv_bfloat16 *o_lat, float
 // bf16), then out^T [d_v x 64] = W_UV^(s)T . o_lat^T on the tensor cores, with W_UV supplying the
 // 128-row M side (A = W_UV^T, M-major; fp32 accumulator in 64 tensor-memory columns).  All of
 // W_UV[s] (128 KB) is requested by TMA before the kernel waits for the attention kernel, so its
-// transfer overlaps that kernel's tail.  The merge runs on all 256 threads at once: four threads
-// per row, each owning 16 of the row's 64 16-byte column blocks (blocks 4 i + q), so that the four
-// threads of a row read 64 contiguous bytes per load.
+// transfer overlaps that kernel's tail.  The merge runs on all 256 threads at once: kTpr threads per
+// row (four for 64 rows, up to 64 where there are few), each owning 64 / kTpr of the row's 64 16-byte
+// column blocks (blocks kTpr i + q), so that the threads of a row read contiguous bytes, and always 16
+// loads of a thread are in flight.  With four threads per row whatever the rows, two rows of five
+// pieces took six rounds of loads, one after another.
 constexpr int kCombRows = 64;
 constexpr int kCombThreads = 256;
 constexpr int kDv = 128;                                   // the W_UV tile width this kernel takes
 constexpr uint32_t kOlBytes = kCombRows * kDc * 2;         // o_lat: [8 K-chunks][64 rows][128 B]
 constexpr uint32_t kWuvBytes = kDc * kDv * 2;              // W_UV^T: [8 K-chunks][2 M-chunks][64 K rows][128 B]
-static_assert(kCombThreads == 4 * kCombRows, "four merging threads per row");
+static_assert(kCombThreads == 4 * kCombRows, "four merging threads per row of a full tile");
 
-template <typename P>
+template <typename P, int kTpr>
 __global__ void __launch_bounds__(kCombThreads)
 tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int rows, float *lse_out,
                   __nv_bfloat16 *out, int *dev_status) {
@@ -1261,8 +1263,10 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int row
   }
   sm100::grid_dep_wait();   // the partials and the segment list come from the attention kernel
   {
-    // Merge of row rr (output row g = g0 + rr); rows past the end become zero rows of the tile.
-    const int rr = tid >> 2, q = tid & 3, g = g0 + rr;
+    // Merge of row rr (output row g = g0 + rr).  Rows past the end become zero rows of the tile, or, where the threads do
+    // not reach them, stay as they are: a row of B touches its own column of the product only.
+    constexpr int kNb = 64 / kTpr, kAtOnce = kNb < 8 ? kNb : 8, kFly = 16 / kAtOnce;
+    const int rr = tid / kTpr, q = tid % kTpr, g = g0 + rr;
     const PieceRows pr = g < rows ? piece_rows(pc, rows, g, s) : PieceRows();
     const int ns = pr.ns;
     float m = -CUDART_INF_F;
@@ -1272,30 +1276,30 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int row
       for (int k = 0; k < ns; ++k) sum += __expf(pc.lse[pr.at(k)] - m);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
-    for (int hh = 0; hh < 2; ++hh) {
-      // this round: column blocks cb = 4 (8 hh + i) + q, i < 8 (8 bf16 each)
-      float acc[8][8];
+    for (int hh = 0; hh < kNb / kAtOnce; ++hh) {
+      // this round: column blocks cb = kTpr (kAtOnce hh + i) + q, i < kAtOnce (8 bf16 each)
+      float acc[kAtOnce][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
-      for (int k0 = 0; k0 < ns; k0 += 2) {
-        uint4 x[2][8];
-        float wk[2];
+      for (int k0 = 0; k0 < ns; k0 += kFly) {
+        uint4 x[kFly][kAtOnce];
+        float wk[kFly];
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
+        for (int kk = 0; kk < kFly; ++kk) {
           const bool have = k0 + kk < ns;
           const int64_t prow = pr.at(have ? k0 + kk : 0);
           const __nv_bfloat16 *src = pc.part + prow * kDc;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            x[kk][i] = have ? *reinterpret_cast<const uint4 *>(src + 8 * (4 * (8 * hh + i) + q)) : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < kAtOnce; ++i)
+            x[kk][i] = have ? *reinterpret_cast<const uint4 *>(src + 8 * (kTpr * (kAtOnce * hh + i) + q)) : make_uint4(0, 0, 0, 0);
           wk[kk] = have && m != -CUDART_INF_F ? __expf(pc.lse[prow] - m) * inv : 0.f;
         }
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk < kFly; ++kk)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < kAtOnce; ++i) {
             const __nv_bfloat162 *xh = reinterpret_cast<const __nv_bfloat162 *>(&x[kk][i]);
 #pragma unroll
             for (int e2 = 0; e2 < 4; ++e2) {
@@ -1306,8 +1310,8 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int row
           }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int cb = 4 * (8 * hh + i) + q, kc = cb >> 3, jj = cb & 7;
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int cb = kTpr * (kAtOnce * hh + i) + q, kc = cb >> 3, jj = cb & 7;
         uint4 packed;
         packed.x = pack_bf16x2(acc[i][0], acc[i][1]);
         packed.y = pack_bf16x2(acc[i][2], acc[i][3]);
@@ -1551,6 +1555,19 @@ namespace {
 
 // out [rows][H][128] = (pieces of each row, merged) . W_UV^(s) per head s, on the tensor cores;
 // lse (if non-null) gets the merged log-sum-exps.
+template <typename P, int kTpr>
+int launch_merge_wuv_as(const CUtensorMap &mw, const mla_dims &d, int rows, const P &pc, void *out, float *lse,
+                        int *dev_status, cudaStream_t st) {
+  const size_t smem = 1024 + kOlBytes + kWuvBytes;
+  static std::atomic<int> smem_set[kSmemCacheDevs];
+  if (smem_limit(tc_combine_kernel<P, kTpr>, smem, smem_set) != cudaSuccess) return MLA_ERR_CUDA;
+  const dim3 grid(d.n_heads, (rows + kCombRows - 1) / kCombRows);
+  return launch_pdl(tc_combine_kernel<P, kTpr>, grid, dim3(kCombThreads), smem, st, mw, pc, rows, lse,
+                    static_cast<__nv_bfloat16 *>(out), dev_status) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
 template <typename P>
 int launch_merge_wuv(const mla_dims &d, int rows, const P &pc, const void *w_uv, void *out, float *lse,
                      int *dev_status, cudaStream_t st) {
@@ -1558,15 +1575,11 @@ int launch_merge_wuv(const mla_dims &d, int rows, const P &pc, const void *w_uv,
   CUtensorMap mw;
   int rc = make_map(&mw, w_uv, kDv, (uint64_t)d.n_heads * kDc, (uint64_t)kDv * 2);
   if (rc) return rc;
-  const size_t smem = 1024 + kOlBytes + kWuvBytes;
-  static std::atomic<int> smem_set[kSmemCacheDevs];
-  if (smem_limit(tc_combine_kernel<P>, smem, smem_set) != cudaSuccess)
-    return MLA_ERR_CUDA;
-  const dim3 grid(d.n_heads, (rows + kCombRows - 1) / kCombRows);
-  return launch_pdl(tc_combine_kernel<P>, grid, dim3(kCombThreads), smem, st, mw, pc, rows, lse,
-                    static_cast<__nv_bfloat16 *>(out), dev_status) == cudaSuccess
-             ? MLA_OK
-             : MLA_ERR_CUDA;
+  // As many threads per row as the rows of a tile leave.
+  if (rows <= 4) return launch_merge_wuv_as<P, 64>(mw, d, rows, pc, out, lse, dev_status, st);
+  if (rows <= 16) return launch_merge_wuv_as<P, 16>(mw, d, rows, pc, out, lse, dev_status, st);
+  if (rows <= 32) return launch_merge_wuv_as<P, 8>(mw, d, rows, pc, out, lse, dev_status, st);
+  return launch_merge_wuv_as<P, 4>(mw, d, rows, pc, out, lse, dev_status, st);
 }
 
 }  // namespace

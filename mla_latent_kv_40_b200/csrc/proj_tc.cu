@@ -16,6 +16,7 @@
 #include "append_finish.cuh"
 #include "kernels.cuh"
 #include "sm100.cuh"
+#include "shared_plan.cuh"
 #include "tmap.cuh"
 
 namespace mla {
@@ -180,6 +181,23 @@ absorb_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                  int *dev_status) {
   extern __shared__ unsigned char smem_raw[];
   absorb_tc_body(map_w, map_q, a, dev_status, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.y, align1024(smem_raw));
+}
+
+// The absorption and, in block 0, the plan of a decode over shared prefixes: neither needs the other, and as launches of
+// their own the absorption's writes would wait for the plan to end (about 3 us of a small call).  In the fused launch the
+// plan works in the operand tiles' space.
+__global__ void __launch_bounds__(kTcThreads)
+absorb_plan_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_q,
+                   const __grid_constant__ AbsorbArgs a, const __grid_constant__ SharedPlanArgs plan, int in_smem, int ny,
+                   int *dev_status) {
+  extern __shared__ unsigned char smem_raw[];
+  if (blockIdx.x == 0) {
+    grid_dep_launch();
+    shared_plan_body(plan, in_smem ? reinterpret_cast<int *>(smem_raw) : nullptr);
+    return;
+  }
+  const int id = blockIdx.x - 1, s = id % a.H, by = (id / a.H) % ny, bz = id / (a.H * ny);
+  absorb_tc_body(map_w, map_q, a, dev_status, s, by, bz, ny, align1024(smem_raw));
 }
 
 // ------------------------------------------------------------------ append projection
@@ -390,6 +408,23 @@ int launch_absorb_tc(const AbsorbArgs &a, int *dev_status, cudaStream_t st) {
     return MLA_ERR_CUDA;
   const dim3 grid(a.H, a.d_c / 128, (R + kTcN - 1) / kTcN);
   return launch_pdl(absorb_tc_kernel, grid, dim3(kTcThreads), smem, st, mw, mq, a, dev_status) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+int launch_absorb_plan(const AbsorbArgs &a, const SharedPlanArgs &plan, int *dev_status, cudaStream_t st) {
+  const int R = a.B * a.n_q;
+  CUtensorMap mw, mq;
+  if (!make_tmap_bf16(&mw, a.w_uk, a.d_nope, (uint64_t)a.H * a.d_c, (uint64_t)a.d_nope * 2, 128) ||
+      !make_tmap_bf16(&mq, a.q_nope, (uint64_t)a.H * a.d_nope, R, (uint64_t)a.H * a.d_nope * 2, kTcN))
+    return MLA_ERR_CUDA;
+  const size_t smem = 1024 + a.d_nope / 64 * (kAChunk + kBChunk);
+  static std::atomic<int> smem_set[kSmemCacheDevs];
+  if (smem_limit(absorb_plan_kernel, smem, smem_set) != cudaSuccess) return MLA_ERR_CUDA;
+  const bool in_smem = shared_plan_words(plan.B, plan.max_units, plan.num_groups) * sizeof(int) <= smem;
+  const int ny = a.d_c / 128, blocks = 1 + a.H * ny * ((R + kTcN - 1) / kTcN);
+  return launch_pdl(absorb_plan_kernel, dim3(blocks), dim3(kTcThreads), smem, st, mw, mq, a, plan, (int)in_smem, ny,
+                    dev_status) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }

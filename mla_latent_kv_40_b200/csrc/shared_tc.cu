@@ -37,6 +37,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "shared_plan.cuh"
 #include "shared_tc.cuh"
 #include "sm100.cuh"
 #include "tmap.cuh"
@@ -46,10 +47,10 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kPage = 64;                          // keys of a page
+constexpr int kPage = kSharedPage;                 // keys of a page
 constexpr int kDc = 512, kDr = 64, kW = kDc + kDr;
 constexpr int kRows = 128;                         // query rows per CTA
-constexpr int kUnitRows = 256;
+constexpr int kUnitRows = 256;                     // two CTAs' rows, and the rows of a partial
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
 constexpr uint32_t kChunkBytes = kPage * 128;      // [64 keys x 64 dims] bf16, 128-byte swizzled
@@ -119,7 +120,7 @@ constexpr size_t kSmemBytes = 1024 + kRegion + sizeof(Small);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct Params {
-  const int *head, *cluster_unit;
+  const SharedShare *shares;
   const SharedUnit *units;
   const __nv_bfloat16 *q;
   const int32_t *block_table, *seqlens;
@@ -186,32 +187,35 @@ __device__ __forceinline__ bool waitw(Small &sm, uint32_t bar, uint32_t parity, 
 }
 
 // ------------------------------------------------------------ work list
-// The runs of tiles of one cluster: those whose place in the list lies in its share [lo, hi) of the total cost.
+// The runs of tiles of one cluster: unit by unit, the tiles whose place lies in its share.
 struct Runs {
-  int u, units, lo, hi, cid;
+  int u, units, begin, end, cid;
+  bool fresh;       // `un` came with the share
   SharedUnit un;
   int t0, t1;       // tiles of the unit in this run
-  __device__ __forceinline__ Runs(const Params &p, int cid_) : u(0), units(0), lo(0), hi(0), cid(cid_) {
-    const int4 h = *reinterpret_cast<const int4 *>(p.head);
-    if (cid < h.y) {
-      lo = (int)((int64_t)cid * h.x / h.y);
-      hi = (int)((int64_t)(cid + 1) * h.x / h.y);
-      units = h.z;
-      u = p.cluster_unit[cid];
-    }
+  __device__ __forceinline__ void take(const int4 &a, const int4 &b, const int4 &c) {
+    un.cost0 = a.x; un.tiles = a.y; un.pages = a.z; un.shared = a.w;
+    un.row0 = b.x; un.rows = b.y; un.seq0 = b.z; un.members = b.w;
+    un.table_seq = c.x;
+  }
+  __device__ __forceinline__ Runs(const Params &p, int cid_) : cid(cid_), fresh(true) {
+    const int4 *src = reinterpret_cast<const int4 *>(p.shares + cid);
+    const int4 h = src[0];
+    take(src[1], src[2], src[3]);
+    begin = h.x; end = h.y; u = h.z; units = h.w;
   }
   __device__ __forceinline__ bool next(const Params &p) {
-    for (; u < units; ++u) {
-      const int4 *src = reinterpret_cast<const int4 *>(p.units + u);
-      const int4 a = src[0], b = src[1], c = src[2];
-      un.cost0 = a.x; un.tiles = a.y; un.pages = a.z; un.shared = a.w;
-      un.row0 = b.x; un.rows = b.y; un.seq0 = b.z; un.members = b.w;
-      un.table_seq = c.x;
-      if (un.cost0 >= hi) break;
-      t0 = max(lo - un.cost0, 0);
-      t1 = min(hi - un.cost0, un.tiles);
+    for (; u < units; ++u, fresh = false) {
+      if (!fresh) {
+        const int4 *src = reinterpret_cast<const int4 *>(p.units + u);
+        take(src[0], src[1], src[2]);
+      }
+      if (un.cost0 >= end) break;
+      t0 = max(begin - un.cost0, 0);
+      t1 = min(end - un.cost0, un.tiles);
       if (t0 < t1) {
         ++u;
+        fresh = false;
         return true;
       }
     }
@@ -823,20 +827,22 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         const int64_t prow = it.part_row() + kRows * side + r;
         const bool live = kRows * (int)side + r < it.un.rows;
         __nv_bfloat16 *dst = p.o_part + prow * kDc;
-#pragma unroll 1
+        uint32_t v[2][32];            // the next 32 columns are on their way while these are stored
+        tmem_ld32(tbase + lane_off + ocol, v[0]);
+#pragma unroll
         for (int c = 0; c < 8; ++c) {
-          uint32_t v[32];
-          tmem_ld32(tbase + lane_off + ocol + 32 * c, v);
           tmem_wait_ld();
+          if (c < 7) tmem_ld32(tbase + lane_off + ocol + 32 * (c + 1), v[(c + 1) & 1]);
           // Columns 256 g .. are rank 2's dims 128 g .. 128 g + 127, then rank 3's, 256 further on.
           const int dim = 256 * (c >> 2) + 128 * g + 32 * (c & 3);
+          const uint32_t (&x)[32] = v[c & 1];
           if (live)
 #pragma unroll
             for (int i = 0; i < 32; i += 16) {
               uint32_t w[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(v[i + 2 * e]) * inv, __uint_as_float(v[i + 2 * e + 1]) * inv);
+                w[e] = pack_bf16x2(__uint_as_float(x[i + 2 * e]) * inv, __uint_as_float(x[i + 2 * e + 1]) * inv);
               st_global_v8(dst + dim + i, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
             }
         }
@@ -863,142 +869,11 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
   cluster_sync();   // no CTA leaves while another may still reach its shared memory
 }
 
-// ------------------------------------------------------------ plan
-// One CTA.  A group's shared keys are the whole blocks among its first min(prefix_lens[g], shortest visible run) keys,
-// where the first query token of sequence b sees seqlens[b] - n_q + 1 keys.
-//
-// The work list is the units in order; a tile costs 1, and every unit after the first kUnitCost more (its queries go to
-// tensor memory and the finished unit's O is written out while the MMAs wait).  Cluster c's share is
-// [floor(c W / C), floor((c + 1) W / C)) of the total cost W.
-constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
-constexpr int kUnitCost = 8;
-
-__device__ __forceinline__ int cluster_of(int64_t at, int W, int C) { return (int)(((at + 1) * C + W - 1) / W - 1); }
-
-// Exclusive scan of one value per thread (kPlanThreads of them), its total added to `carry`.
-__device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t *part, int64_t &carry) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t inc = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t w = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += w;
-  }
-  __syncthreads();
-  if (lane == 31) part[warp] = inc;
-  __syncthreads();
-  int64_t w = part[lane];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += y;
-  }
-  const int64_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
-  const int64_t all = __shfl_sync(0xffffffffu, w, 31);
-  const int64_t exc = carry + (warp ? before : 0) + inc - v;
-  carry += all;
-  return exc;
-}
-
-__global__ void __launch_bounds__(kPlanThreads)
-shared_plan_kernel(SharedPlan pl, int B, int n_q, int R, int max_seqlen, int block_size, int G, int clusters,
-                   const int32_t *offsets, const int32_t *prefix_lens, const int32_t *seqlens, int *dev_status) {
-  __shared__ int64_t part[kPlanWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int unit_rows = shared_unit_rows(R);
+// The plan by itself, for queries that another kernel than absorb_tc_kernel absorbs.
+__global__ void __launch_bounds__(1024) shared_plan_kernel(const SharedPlanArgs a, int in_smem) {
+  extern __shared__ int plan_words[];
   grid_dep_launch();
-  int bad = 0;
-  for (int g = tid; g < G; g += kPlanThreads) {
-    const int lo = offsets[g], hi = offsets[g + 1];
-    bad |= lo < 0 || lo > hi || hi > B || (g == 0 && lo != 0) || (g == G - 1 && hi != B) || prefix_lens[g] < 0;
-  }
-  bad = __syncthreads_or(bad);
-  grid_dep_wait();   // earlier calls may still read the plan that is overwritten from here on
-  if (bad && tid == 0) report(dev_status, MLA_ERR_BAD_INDEX);
-  if (bad) G = 1;    // then one group that shares nothing
-  auto first_of = [&](int g) { return bad ? g * B : offsets[g]; };
-  // Units before each group.
-  int64_t units = 0;
-  for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
-    const int g = g0 + tid;
-    const int64_t rows = g < G ? (int64_t)(first_of(g + 1) - first_of(g)) * R : 0;
-    const int64_t exc = plan_scan((rows + unit_rows - 1) / unit_rows, part, units);
-    if (g < G) pl.group_units[g] = (int)exc;
-  }
-  if (tid == 0) pl.group_units[G] = (int)units;
-  __syncthreads();
-  const int U = (int)units;
-  // Shared pages of every group; the parts of its units that do not depend on the others.
-  for (int g = warp; g < G; g += kPlanWarps) {
-    const int lo = first_of(g), hi = first_of(g + 1), u0 = pl.group_units[g], n = pl.group_units[g + 1] - u0;
-    int common = bad ? 0 : prefix_lens[g];
-    for (int b = lo + lane; b < hi; b += 32) {
-      const int S = seqlens[b];
-      if (S < n_q || S > max_seqlen) report(dev_status, MLA_ERR_BAD_INDEX);
-      common = min(common, max(min(S, max_seqlen) - n_q + 1, 0));
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) common = min(common, __shfl_xor_sync(0xffffffffu, common, o));
-    const int shared = common / block_size * (block_size / kPage);
-    for (int b = lo + lane; b < hi; b += 32) {
-      pl.seq_shared[b] = shared;
-      pl.seq_group[b] = make_int2(u0, lo * R);
-    }
-    for (int i = lane; i < n; i += 32) {
-      const int row0 = lo * R + i * unit_rows, rows = min(unit_rows, hi * R - row0);
-      const int seq0 = row0 / R, last = (row0 + rows - 1) / R;
-      int4 *dst = reinterpret_cast<int4 *>(pl.units + u0 + i);
-      dst[0] = make_int4(0, 0, 0, shared);
-      dst[1] = make_int4(row0, rows, seq0, last - seq0 + 1);
-      dst[2] = make_int4(lo, 0, 0, 0);
-    }
-  }
-  __syncthreads();
-  // Own pages before each sequence.
-  int64_t own = 0;
-  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    int n = 0;
-    if (b < B) n = (max(min(seqlens[b], max_seqlen) - kPage * pl.seq_shared[b], 0) + kPage - 1) / kPage;
-    const int64_t exc = plan_scan(n, part, own);
-    if (b < B) pl.own_pages[b] = (int)exc;
-  }
-  if (tid == 0) pl.own_pages[B] = (int)own;
-  __syncthreads();
-  // Tiles of every unit and its place in the list; non-empty units are counted in the low word.
-  int64_t list = 0;
-  for (int u0 = 0; u0 < U; u0 += kPlanThreads) {
-    const int u = u0 + tid;
-    int pages = 0, shared = 0;
-    if (u < U) {
-      shared = reinterpret_cast<int4 *>(pl.units + u)[0].w;
-      const int4 c = reinterpret_cast<int4 *>(pl.units + u)[1];
-      pages = shared + pl.own_pages[c.z + c.w] - pl.own_pages[c.z];
-    }
-    const int tiles = (pages + 1) / 2;
-    const int64_t exc = plan_scan((int64_t)(tiles > 0) | ((int64_t)tiles << 32), part, list);
-    if (u < U)
-      reinterpret_cast<int4 *>(pl.units + u)[0] =
-          make_int4((int)(exc >> 32) + kUnitCost * (int)(exc & 0xffffffff), tiles, pages, shared);
-  }
-  const int full = (int)(list & 0xffffffff);
-  const int W = (int)(list >> 32) + kUnitCost * max(full - 1, 0);
-  const int C = min(W, clusters);
-  __syncthreads();
-  for (int u = tid; u < U; u += kPlanThreads) {
-    const int4 a = reinterpret_cast<int4 *>(pl.units + u)[0];
-    if (a.y == 0) {
-      pl.unit_parts[u] = make_int2(0, 0);
-      continue;
-    }
-    const int c0 = cluster_of(a.x, W, C), c1 = cluster_of((int64_t)a.x + a.y - 1, W, C);
-    pl.unit_parts[u] = make_int2(u + c0, c1 - c0 + 1);
-    // The clusters whose share begins behind the previous unit's last tile and not behind this one's.
-    const int from = max(a.x - kUnitCost, 0);
-    for (int x = cluster_of(from, W, C); x <= c1; ++x)
-      if ((int64_t)x * W / C >= from) pl.cluster_unit[x] = u;
-  }
-  if (tid == 0) *reinterpret_cast<int4 *>(pl.head) = make_int4(W, C, U, 0);
+  shared_plan_body(a, in_smem ? plan_words : nullptr);
 }
 
 }  // namespace
@@ -1042,13 +917,13 @@ int shared_clusters_for_device() {
   return n;
 }
 
-int launch_shared_plan(const SharedPlan &pl, int B, int n_q, int H, int max_seqlen, int block_size, int num_groups,
-                       const int32_t *group_offsets, const int32_t *prefix_lens, const int32_t *seqlens,
-                       int *dev_status, cudaStream_t st) {
-  const int C = shared_clusters_for_device();
-  if (C <= 0) return MLA_ERR_CUDA;
-  return launch_pdl(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, pl, B, n_q, n_q * H, max_seqlen, block_size,
-                    num_groups, C, group_offsets, prefix_lens, seqlens, dev_status) == cudaSuccess
+int launch_shared_plan(const SharedPlanArgs &a, cudaStream_t st) {
+  const size_t bytes = shared_plan_words(a.B, a.max_units, a.num_groups) * sizeof(int);
+  const bool in_smem = bytes <= 160 * 1024;
+  static std::atomic<int> cache[kSmemCacheDevs];
+  if (in_smem && smem_limit(shared_plan_kernel, bytes, cache) != cudaSuccess) return MLA_ERR_CUDA;
+  const int threads = a.B <= 256 ? 256 : 1024;
+  return launch_pdl(shared_plan_kernel, dim3(1), dim3(threads), in_smem ? bytes : 0, st, a, (int)in_smem) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }
@@ -1069,8 +944,7 @@ int launch_shared_attention(const mla_dims &d, int n_q, int max_seqlen, const Sh
   const int C = shared_clusters_for_device();
   if (C <= 0) return MLA_ERR_CUDA;
   Params p;
-  p.head = pl.head;
-  p.cluster_unit = pl.cluster_unit;
+  p.shares = pl.shares;
   p.units = pl.units;
   p.q = static_cast<const __nv_bfloat16 *>(q_abs);
   p.block_table = cache.block_table;

@@ -17,21 +17,30 @@ struct SharedUnit {
   int pad[3];
 };
 static_assert(sizeof(SharedUnit) == 48, "read as three 16-byte words");
+// One cluster's share of the work list: [begin, end), the first unit there, the number of units, and that unit.
+struct SharedShare {
+  int begin, end, unit, units;
+  SharedUnit first;
+};
+static_assert(sizeof(SharedShare) == 64, "read as four 16-byte words");
+constexpr int kSharedPage = 64;      // keys of a page
 constexpr int kSharedMembers = 32;
 // Query rows of a full unit of sequences with R rows each.
 __host__ __device__ constexpr int shared_unit_rows(int R) { return R >= 8 ? 256 : kSharedMembers * R; }
 
 // What the plan kernel leaves for the kernels behind it.
 struct SharedPlan {
-  int *head;                // [4]: total cost, clusters that get a share, units, 0
-  int *cluster_unit;        // [clusters]: the unit at which each cluster's share begins
+  SharedShare *shares;      // [clusters]
   SharedUnit *units;        // [units]
   int2 *unit_parts;         // [units]: first partial (of 256 rows) of the unit, number of partials
   int2 *seq_group;          // [B]: first unit of the sequence's group, the group's first query row
   int *own_pages;           // [B + 1]: own pages of the sequences before this one
-  int *seq_shared;          // [B] shared pages of the sequence's group
-  int *group_units;         // [num_groups + 1] scratch: first unit of each group
+  int *scratch;             // shared_plan_words() of the plan kernel's own
 };
+// Words that the plan works on (in shared memory while they fit there).
+inline size_t shared_plan_words(int B, int units, int num_groups) {
+  return 2 * (size_t)B + 1 + 4 * (size_t)units + 1 + (size_t)num_groups + 1;
+}
 
 constexpr int kSharedMaxClusters = 64;
 // Clusters of four CTAs that fit on the current device at once (0 without a device).
@@ -40,9 +49,15 @@ int shared_clusters_for_device();
 inline int shared_max_units(int B, int R, int num_groups) {
   return (int)(((int64_t)B * R) / shared_unit_rows(R)) + (num_groups < B ? num_groups : B);
 }
-int launch_shared_plan(const SharedPlan &pl, int B, int n_q, int H, int max_seqlen, int block_size, int num_groups,
-                       const int32_t *group_offsets, const int32_t *prefix_lens, const int32_t *seqlens,
-                       int *dev_status, cudaStream_t st);
+struct SharedPlanArgs {
+  SharedPlan out;
+  int B, n_q, R, max_seqlen, block_size, num_groups, max_units, clusters;
+  const int32_t *offsets, *prefix_lens, *seqlens;
+  int *dev_status;
+};
+int launch_shared_plan(const SharedPlanArgs &a, cudaStream_t st);
+// The plan and the query absorption in one launch (absorb_tc_supported shapes).
+int launch_absorb_plan(const AbsorbArgs &ab, const SharedPlanArgs &plan, int *dev_status, cudaStream_t st);
 // Attention of every unit over its pages: partials o_part [256 (u + c) + row][512] (bf16, normalised by their own
 // sums) and lse_part of cluster c's share of unit u.
 int launch_shared_attention(const mla_dims &d, int n_q, int max_seqlen, const SharedPlan &pl, const void *q_abs,
