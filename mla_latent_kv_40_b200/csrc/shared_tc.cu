@@ -104,7 +104,8 @@ enum Bar {
 
 struct Req {
   int kind;      // 0: before a page's MMAs, rescale O and/or zero the latent rows past the last key; 1: the epilogue
-  int rescale, slot, keys, stage, last_slot, last_parity;
+  int rescale, slot, keys, stage;
+  int np, pages;   // 1: pages so far, and those of the run
 };
 
 struct Small {                          // behind the tiles
@@ -393,7 +394,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         uint32_t n = 0, ns = 0, uc = 0;
         bool ok = true;
         while (ok && it.next(p)) {
-          ok = waitw(sm, bar(B_QREADY), uc & 1, p.dev_status, true);
+          ok = waitw(sm, bar(B_QREADY), uc & 1, p.dev_status);
           ++uc;
           for (int t = it.t0; ok && t < it.t1; ++t, ++ns) {
             const uint32_t sbuf = ns & 1, dcol = tbase + kSCol + 128 * sbuf;
@@ -493,11 +494,21 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         const uint32_t idesc = idesc_bf16_f32(kUnitRows, 256, false, true);
         const uint32_t ready = mapa(bar(B_CFULL), 2);
         uint32_t np = 0, uc = 0, nfix = 0;
+        int run_pages = 0;
         bool ok = true;
         while (ok && it.next(p)) {
           Members mem;
           mem.load(p, it.un);
-          if (uc > 0 && !(ok = waitw(sm, bar(B_OFREE), (uc - 1) & 1, p.dev_status))) break;
+          if (uc > 0) {
+            if (!(ok = waitw(sm, bar(B_OFREE), (uc - 1) & 1, p.dev_status))) break;
+            // The epilogue is through with the P slots of the finished run's last two pages, which it borrowed.
+            if (lane < 2 && run_pages >= 2) {
+              const int pb = (np - 2 + lane) % kPSlots;
+              mbar_expect_tx(bar(B_PFULL + pb), kPTxBytes);
+              mbar_arrive_cluster_light(mapa(bar(B_PEMPTY + pb), side));
+            }
+            __syncwarp();
+          }
           for (int g = 2 * it.t0; g < it.pages_end(); ++g, ++np) {
             const int pb = np % kPSlots, sv = np % kVStages;
             const uint32_t ppar = (np / kPSlots) & 1;
@@ -546,26 +557,30 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             commit2(bar(B_PVDONE + pb), kValuePair);
           }
           if (!ok) break;
-          const uint32_t last = np - 1;
+          run_pages = it.pages_end() - 2 * it.t0;
           if (lane == 0) {
-            sm.req = Req{1, 0, 0, 0, 0, (int)(last % kPSlots), (int)((last / kPSlots) & 1)};
+            sm.req = Req{1, 0, 0, 0, 0, (int)np, run_pages};
             mbar_arrive(bar(B_REQ));
           }
           __syncwarp();
           ++uc;
         }
       } else if (warp == 2 && lane == 0) {
-        // ---- a P slot may be written again once the MMAs that read it are complete.
+        // ---- a P slot may be written again once the MMAs that read it are complete (the last two of a run go to the
+        // epilogue first: see warp 1).
         const uint32_t pempty = mapa(bar(B_PEMPTY), side);
         uint32_t np = 0;
         bool ok = true;
-        while (ok && it.next(p))
-          for (int g = 2 * it.t0; g < it.pages_end(); ++g, ++np) {
+        while (ok && it.next(p)) {
+          const int n = it.pages_end() - 2 * it.t0;
+          for (int i = 0; i < n; ++i, ++np) {
             const int pb = np % kPSlots;
             if (!(ok = wait1(sm, bar(B_PVDONE + pb), (np / kPSlots) & 1, p.dev_status))) break;
+            if (n >= 2 && i >= n - 2) continue;
             mbar_expect_tx(bar(B_PFULL + pb), kPTxBytes);
             mbar_arrive_cluster_light(pempty + 8 * pb);
           }
+        }
       }
     }
   } else if (score) {
@@ -596,15 +611,15 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         const int left = it.un.rows - r0;
         const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(it.un.row0 + r0) * kW) + j;
         constexpr int kStep = 4 * kW / 8;   // 16-byte words between a lane's rows
-        // Two of the four 64-dim columns in flight; a column's registers take the one after next as soon as it is staged.
+        // Two of the four 64-dim columns in flight; a column's registers take the one after next as soon as it is staged,
+        // and the RoPE dims (half 0 only) after those.
         uint4 x[2][8];
-        auto load_column = [&](int cb) {
+        auto load_column = [&](uint4 (&dst)[8], int word) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            x[cb & 1][k] = 4 * k < left ? __ldg(src + k * kStep + h * 32 + cb * 8) : make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 8; ++k) dst[k] = 4 * k < left ? __ldg(src + k * kStep + word) : make_uint4(0, 0, 0, 0);
         };
-        load_column(0);
-        load_column(1);
+#pragma unroll
+        for (int cb = 0; cb < 2; ++cb) load_column(x[cb], h * 32 + cb * 8);
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) {
 #pragma unroll
@@ -612,7 +627,8 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             const int lr = 4 * k + (lane >> 3);
             *reinterpret_cast<uint4 *>(stg_w + (lr >> 3) * 1024 + (lr & 7) * 128 + ((j ^ (lr & 7)) << 4)) = x[cb & 1][k];
           }
-          if (cb + 2 < 4) load_column(cb + 2);
+          if (cb < 2) load_column(x[cb], h * 32 + (cb + 2) * 8);
+          if (cb == 2 && h == 0) load_column(x[0], 64);
           __syncwarp();
           uint32_t w[32];
 #pragma unroll
@@ -627,15 +643,14 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int rq = q4 * 32 + 4 * k + (lane >> 3);
-            *reinterpret_cast<uint4 *>(tiles + kQpeOff + (rq >> 3) * 1024 + (rq & 7) * 128 + ((j ^ (rq & 7)) << 4)) =
-                4 * k < left ? __ldg(src + k * kStep + 64) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(tiles + kQpeOff + (rq >> 3) * 1024 + (rq & 7) * 128 + ((j ^ (rq & 7)) << 4)) = x[0][k];
           }
-          fence_proxy_async_smem();
+          fence_proxy_async_smem();   // the MMAs read it
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa(bar(B_QREADY), 0));
+        if (lane == 0) mbar_arrive_cluster_light(mapa(bar(B_QREADY), 0));   // read by the async proxy only, which the fences order
       }
       // This row's member and how many of that member's own keys it sees; rows past the unit's end see none.
       Members mem;
@@ -816,7 +831,8 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
           if (lane == 0) mbar_arrive(bar(B_REQDONE));
           continue;
         }
-        if (!(ok = waitw(sm, bar(B_PVDONE + q.last_slot), q.last_parity, p.dev_status) &&
+        const uint32_t last = q.np - 1;
+        if (!(ok = waitw(sm, bar(B_PVDONE + last % kPSlots), (last / kPSlots) & 1, p.dev_status) &&
                    waitw(sm, bar(B_STATSFULL), uc & 1, p.dev_status, true)))
           break;
         tc_fence_after();
@@ -825,33 +841,70 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         if (lane == 0) mbar_arrive_cluster(statsempty_remote);
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const int64_t prow = it.part_row() + kRows * side + r;
-        const bool live = kRows * (int)side + r < it.un.rows;
+        const int rows = it.un.rows - kRows * (int)side;   // of this CTA
+        const bool live = r < rows;
         __nv_bfloat16 *dst = p.o_part + prow * kDc;
-        uint32_t v[2][32];            // the next 32 columns are on their way while these are stored
-        tmem_ld32(tbase + lane_off + ocol, v[0]);
+        // Columns 256 g .. are rank 2's dims 128 g .. 128 g + 127, then rank 3's, 256 further on.
+        if ((warp & 3) * 32 >= rows) {
+          // no rows of the unit here
+        } else if (q.pages >= 2) {
+          // 64 columns at a time through 4 KB of a P slot whose MMAs are complete (the run's last two: one per group), so
+          // that rows leave in whole 128-byte lines: 16 lanes x 32 bytes of different rows took 5 us of LSU time a unit.
+          unsigned char *stg = tiles + kPOff + ((q.np - 2 + g) % kPSlots) * kPSlotBytes + (warp & 3) * 4096;
+          __nv_bfloat16 *out = p.o_part + (it.part_row() + kRows * (int)side + (warp & 3) * 32) * kDc + 8 * (lane & 7);
+          const int left = rows - (warp & 3) * 32 - (lane >> 3);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[2][32];
+            tmem_ld32(tbase + lane_off + ocol + 64 * c, v[0]);
+            tmem_ld32(tbase + lane_off + ocol + 64 * c + 32, v[1]);
+            tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          tmem_wait_ld();
-          if (c < 7) tmem_ld32(tbase + lane_off + ocol + 32 * (c + 1), v[(c + 1) & 1]);
-          // Columns 256 g .. are rank 2's dims 128 g .. 128 g + 127, then rank 3's, 256 further on.
-          const int dim = 256 * (c >> 2) + 128 * g + 32 * (c & 3);
-          const uint32_t (&x)[32] = v[c & 1];
-          if (live)
+            for (int i = 0; i < 8; ++i) {
+              uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 32; i += 16) {
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(x[i + 2 * e]) * inv, __uint_as_float(x[i + 2 * e + 1]) * inv);
-              st_global_v8(dst + dim + i, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(v[i >> 2][8 * (i & 3) + 2 * e]) * inv,
+                                   __uint_as_float(v[i >> 2][8 * (i & 3) + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4 *>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
+            __syncwarp();
+            const int dim = 256 * (c >> 1) + 128 * g + 64 * (c & 1);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int lr = 4 * k + (lane >> 3);
+              const uint4 y = *reinterpret_cast<const uint4 *>(stg + lr * 128 + (((lane & 7) ^ (lr & 7)) << 4));
+              if (4 * k < left) *reinterpret_cast<uint4 *>(out + (int64_t)lr * kDc + dim) = y;
+            }
+            __syncwarp();
+          }
+          fence_proxy_async_smem();   // the slot is written by copies again
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[32];
+            tmem_ld32(tbase + lane_off + ocol + 32 * c, v);
+            tmem_wait_ld();
+            const int dim = 256 * (c >> 2) + 128 * g + 32 * (c & 3);
+            if (live)
+#pragma unroll
+              for (int i = 0; i < 32; i += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  w[e] = pack_bf16x2(__uint_as_float(v[i + 2 * e]) * inv, __uint_as_float(v[i + 2 * e + 1]) * inv);
+                st_global_v8(dst + dim + i, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+              }
+          }
         }
         if (g == 0 && live) p.lse_part[prow] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_cluster(ofree2);
-          mbar_arrive_cluster(ofree3);
+          // O has been read: no more than that, so nothing here waits for the stores above (a cluster-scope release
+          // did, for 3 us).
+          mbar_arrive_cluster_light(ofree2);
+          mbar_arrive_cluster_light(ofree3);
         }
         ++uc;
         break;
