@@ -1213,22 +1213,24 @@ shared_merge_kernel(const SharedPieces pc, int rows, __nv_bfloat16 *o_lat, float
             lse_out ? lse_out + item : nullptr);
 }
 
-// CTA = (head s, 64 query rows (b, j)): the rows' pieces are merged by their log-sum-exps straight
-// into the B operand tile of the W_UV product (o_lat [64 rows x 512], K-major, 128-byte swizzled,
-// bf16), then out^T [d_v x 64] = W_UV^(s)T . o_lat^T on the tensor cores, with W_UV supplying the
-// 128-row M side (A = W_UV^T, M-major; fp32 accumulator in 64 tensor-memory columns).  All of
-// W_UV[s] (128 KB) is requested by TMA before the kernel waits for the attention kernel, so its
-// transfer overlaps that kernel's tail.  The merge runs on all 256 threads at once: kTpr threads per
-// row (four for 64 rows, up to 64 where there are few), each owning 64 / kTpr of the row's 64 16-byte
-// column blocks (blocks kTpr i + q), so that the threads of a row read contiguous bytes, and always 16
-// loads of a thread are in flight.  With four threads per row whatever the rows, two rows of five
-// pieces took six rounds of loads, one after another.
+// CTA = (head s, 512 / kTpr query rows (b, j), 8 to 64): the rows' pieces are merged by their
+// log-sum-exps straight into the B operand tile of the W_UV product (o_lat [64 rows x 512], K-major,
+// 128-byte swizzled, bf16), then out^T [d_v x 64] = W_UV^(s)T . o_lat^T on the tensor cores, with W_UV
+// supplying the 128-row M side (A = W_UV^T, M-major; fp32 accumulator in 64 tensor-memory columns).
+// All of W_UV[s] (128 KB) is requested by TMA before the kernel waits for the attention kernel, so its
+// transfer overlaps that kernel's tail.  The merge runs on all 512 threads at once: kTpr threads per
+// row, each owning 64 / kTpr of the row's 64 16-byte column blocks (blocks kTpr i + q), so that the
+// threads of a row read contiguous bytes, and 8 or 16 loads of a thread are in flight.  The fewest
+// rows per CTA with which all CTAs are resident at once (one fits on an SM) keep the chain of loads
+// short; beyond that a CTA takes every gridDim.y-th tile of its head, since a second wave would load
+// W_UV again.  (Before, four threads per row and 64 rows: two rows of five pieces took six rounds of
+// loads one after another, and 32 rows of 16 heads ran on 16 SMs.)
 constexpr int kCombRows = 64;
-constexpr int kCombThreads = 256;
+constexpr int kCombThreads = 512;
 constexpr int kDv = 128;                                   // the W_UV tile width this kernel takes
 constexpr uint32_t kOlBytes = kCombRows * kDc * 2;         // o_lat: [8 K-chunks][64 rows][128 B]
 constexpr uint32_t kWuvBytes = kDc * kDv * 2;              // W_UV^T: [8 K-chunks][2 M-chunks][64 K rows][128 B]
-static_assert(kCombThreads == 4 * kCombRows, "four merging threads per row of a full tile");
+static_assert(kCombThreads == 8 * kCombRows, "eight merging threads per row of the largest tile");
 
 template <typename P, int kTpr>
 __global__ void __launch_bounds__(kCombThreads)
@@ -1242,7 +1244,6 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int row
   __shared__ uint32_t tmem_slot;
   __shared__ int s_loaded;
   const int s = blockIdx.x, H = pc.H;
-  const int g0 = blockIdx.y * kCombRows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   sm100::grid_dep_launch();
   // W_UV[s] (an input: no need to wait), as 16 TMA boxes of [64 K rows x 64 output columns] in the
@@ -1262,121 +1263,136 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int row
     tmem_relinquish();
   }
   sm100::grid_dep_wait();   // the partials and the segment list come from the attention kernel
-  {
-    // Merge of row rr (output row g = g0 + rr).  Rows past the end become zero rows of the tile, or, where the threads do
-    // not reach them, stay as they are: a row of B touches its own column of the product only.
-    constexpr int kNb = 64 / kTpr, kAtOnce = kNb < 8 ? kNb : 8, kFly = 16 / kAtOnce;
-    const int rr = tid / kTpr, q = tid % kTpr, g = g0 + rr;
-    const PieceRows pr = g < rows ? piece_rows(pc, rows, g, s) : PieceRows();
-    const int ns = pr.ns;
-    float m = -CUDART_INF_F;
-    for (int k = 0; k < ns; ++k) m = fmaxf(m, pc.lse[pr.at(k)]);
-    float sum = 0.f;
-    if (m != -CUDART_INF_F)
-      for (int k = 0; k < ns; ++k) sum += __expf(pc.lse[pr.at(k)] - m);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  int ok = 1, loaded = 1;
+  uint32_t tmem = 0, phase = 0;
+  constexpr int kR = kCombThreads / kTpr;   // rows of this CTA's tiles
+  for (int g0 = blockIdx.y * kR; g0 < rows; g0 += gridDim.y * kR, phase ^= 1) {
+    {
+      // Merge of row rr (output row g = g0 + rr).  Rows past the end become zero rows of the tile, and those past kR stay
+      // as they are: a row of B touches its own column of the product only.
+      constexpr int kNb = 64 / kTpr, kAtOnce = kNb < 4 ? kNb : 4, kFly = kAtOnce > 1 ? 16 / kAtOnce : 8;
+      const int rr = tid / kTpr, q = tid % kTpr, g = g0 + rr;
+      const PieceRows pr = g < rows ? piece_rows(pc, rows, g, s) : PieceRows();
+      const int ns = pr.ns;
+      float m = -CUDART_INF_F;
+      for (int k0 = 0; k0 < ns; k0 += 8) {   // eight loads in flight
+        float t[8];
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) t[kk] = k0 + kk < ns ? pc.lse[pr.at(k0 + kk)] : -CUDART_INF_F;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) m = fmaxf(m, t[kk]);
+      }
+      float sum = 0.f;
+      if (m != -CUDART_INF_F)
+        for (int k = 0; k < ns; ++k) sum += __expf(pc.lse[pr.at(k)] - m);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
-    for (int hh = 0; hh < kNb / kAtOnce; ++hh) {
-      // this round: column blocks cb = kTpr (kAtOnce hh + i) + q, i < kAtOnce (8 bf16 each)
-      float acc[kAtOnce][8];
+      for (int hh = 0; hh < kNb / kAtOnce; ++hh) {
+        // this round: column blocks cb = kTpr (kAtOnce hh + i) + q, i < kAtOnce (8 bf16 each)
+        float acc[kAtOnce][8];
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i)
+        for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
-      for (int k0 = 0; k0 < ns; k0 += kFly) {
-        uint4 x[kFly][kAtOnce];
-        float wk[kFly];
+          for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
+        for (int k0 = 0; k0 < ns; k0 += kFly) {
+          uint4 x[kFly][kAtOnce];
+          float wk[kFly];
 #pragma unroll
-        for (int kk = 0; kk < kFly; ++kk) {
-          const bool have = k0 + kk < ns;
-          const int64_t prow = pr.at(have ? k0 + kk : 0);
-          const __nv_bfloat16 *src = pc.part + prow * kDc;
+          for (int kk = 0; kk < kFly; ++kk) {
+            const bool have = k0 + kk < ns;
+            const int64_t prow = pr.at(have ? k0 + kk : 0);
+            const __nv_bfloat16 *src = pc.part + prow * kDc;
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i)
-            x[kk][i] = have ? *reinterpret_cast<const uint4 *>(src + 8 * (kTpr * (kAtOnce * hh + i) + q)) : make_uint4(0, 0, 0, 0);
-          wk[kk] = have && m != -CUDART_INF_F ? __expf(pc.lse[prow] - m) * inv : 0.f;
+            for (int i = 0; i < kAtOnce; ++i)
+              x[kk][i] = have ? *reinterpret_cast<const uint4 *>(src + 8 * (kTpr * (kAtOnce * hh + i) + q)) : make_uint4(0, 0, 0, 0);
+            wk[kk] = have && m != -CUDART_INF_F ? __expf(pc.lse[prow] - m) * inv : 0.f;
+          }
+#pragma unroll
+          for (int kk = 0; kk < kFly; ++kk)
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+              const __nv_bfloat162 *xh = reinterpret_cast<const __nv_bfloat162 *>(&x[kk][i]);
+#pragma unroll
+              for (int e2 = 0; e2 < 4; ++e2) {
+                const float2 f = __bfloat1622float2(xh[e2]);
+                acc[i][2 * e2] = fmaf(wk[kk], f.x, acc[i][2 * e2]);
+                acc[i][2 * e2 + 1] = fmaf(wk[kk], f.y, acc[i][2 * e2 + 1]);
+              }
+            }
         }
 #pragma unroll
-        for (int kk = 0; kk < kFly; ++kk)
-#pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) {
-            const __nv_bfloat162 *xh = reinterpret_cast<const __nv_bfloat162 *>(&x[kk][i]);
-#pragma unroll
-            for (int e2 = 0; e2 < 4; ++e2) {
-              const float2 f = __bfloat1622float2(xh[e2]);
-              acc[i][2 * e2] = fmaf(wk[kk], f.x, acc[i][2 * e2]);
-              acc[i][2 * e2 + 1] = fmaf(wk[kk], f.y, acc[i][2 * e2 + 1]);
-            }
-          }
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int cb = kTpr * (kAtOnce * hh + i) + q, kc = cb >> 3, jj = cb & 7;
+          uint4 packed;
+          packed.x = pack_bf16x2(acc[i][0], acc[i][1]);
+          packed.y = pack_bf16x2(acc[i][2], acc[i][3]);
+          packed.z = pack_bf16x2(acc[i][4], acc[i][5]);
+          packed.w = pack_bf16x2(acc[i][6], acc[i][7]);
+          *reinterpret_cast<uint4 *>(ol + kc * 8192 + (rr >> 3) * 1024 + (rr & 7) * 128 + ((jj ^ (rr & 7)) << 4)) = packed;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const int cb = kTpr * (kAtOnce * hh + i) + q, kc = cb >> 3, jj = cb & 7;
-        uint4 packed;
-        packed.x = pack_bf16x2(acc[i][0], acc[i][1]);
-        packed.y = pack_bf16x2(acc[i][2], acc[i][3]);
-        packed.z = pack_bf16x2(acc[i][4], acc[i][5]);
-        packed.w = pack_bf16x2(acc[i][6], acc[i][7]);
-        *reinterpret_cast<uint4 *>(ol + kc * 8192 + (rr >> 3) * 1024 + (rr & 7) * 128 + ((jj ^ (rr & 7)) << 4)) = packed;
-      }
+      if (q == 0 && lse_out && g < rows) lse_out[(int64_t)g * H + s] = sum > 0.f ? m + logf(sum) : -CUDART_INF_F;
+      fence_proxy_async_smem();   // the merged tile is read by the MMA (async proxy)
     }
-    if (q == 0 && lse_out && g < rows) lse_out[(int64_t)g * H + s] = sum > 0.f ? m + logf(sum) : -CUDART_INF_F;
-    fence_proxy_async_smem();   // the merged tile is read by the MMA (async proxy)
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-  int loaded = 1;
-  if (tid == 0) {
-    if (!mbar_wait(smem_u32(&bar_w), 0, kWaitNs)) {
-      report(dev_status, MLA_ERR_TIMEOUT);
-      loaded = 0;
-    }
-    s_loaded = loaded;
-  }
-  // Without its operands the MMA is skipped; its barrier is still completed (commit with nothing issued).
-  if (tid == 0) {
+    tc_fence_before();
+    __syncthreads();
     tc_fence_after();
-    const uint32_t idesc = idesc_bf16_f32(128, kCombRows, true, false);
-    for (int kc = 0; kc < kDc / 64 && loaded; ++kc)
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_ss(tmem, smem_desc_sw128(smem_u32(wa + kc * 16384) + kk * 2048, 8192, 1024),
-               smem_desc_sw128(smem_u32(ol + kc * 8192) + kk * 32, 16, 1024), idesc, (kc | kk) ? 1u : 0u);
-    tc_commit(smem_u32(&bar_mma));
-  }
-  int ok = 1;
-  if (lane == 0 && !mbar_wait(smem_u32(&bar_mma), 0, kWaitNs)) {
-    report(dev_status, MLA_ERR_TIMEOUT);
-    ok = 0;
-  }
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  if (ok) mbar_wait(smem_u32(&bar_mma), 0, kWaitNs);
-  tc_fence_after();
-  // Warp w drains output columns 32(w%4).. (its lane quadrant) for query rows 32(w/4)..: each thread
-  // holds one output column of 32 rows -> a [64 rows x 128] bf16 staging tile over o_lat's space.
-  __nv_bfloat16 *stg = reinterpret_cast<__nv_bfloat16 *>(ol);
-  constexpr int lds = kDv + 8;
-  {
-    uint32_t v[32];
-    tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 32 * (warp >> 2), v);
-    tmem_wait_ld();
-    __syncthreads();   // every thread is past its reads of o_lat (the MMAs completed before the loads)
-    ok = ok && s_loaded;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      stg[(32 * (warp >> 2) + i) * lds + (warp & 3) * 32 + lane] = __float2bfloat16_rn(__uint_as_float(v[i]));
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (ok)
-    for (int c = tid; c < kCombRows * (kDv / 8); c += kCombThreads) {
-      const int rr = c >> 4, q8 = c & 15, g = g0 + rr;
-      if (g < rows)
-        *reinterpret_cast<uint4 *>(out + ((int64_t)g * H + s) * kDv + q8 * 8) =
-            *reinterpret_cast<const uint4 *>(stg + rr * lds + q8 * 8);
+    tmem = tmem_slot;
+    if (tid == 0) {
+      if (!mbar_wait(smem_u32(&bar_w), 0, kWaitNs)) {
+        report(dev_status, MLA_ERR_TIMEOUT);
+        loaded = 0;
+      }
+      s_loaded = loaded;
     }
+    // Without its operands the MMA is skipped; its barrier is still completed (commit with nothing issued).
+    if (tid == 0) {
+      tc_fence_after();
+      const uint32_t idesc = idesc_bf16_f32(128, kCombRows, true, false);
+      for (int kc = 0; kc < kDc / 64 && loaded; ++kc)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ss(tmem, smem_desc_sw128(smem_u32(wa + kc * 16384) + kk * 2048, 8192, 1024),
+                 smem_desc_sw128(smem_u32(ol + kc * 8192) + kk * 32, 16, 1024), idesc, (kc | kk) ? 1u : 0u);
+      tc_commit(smem_u32(&bar_mma));
+    }
+    ok = 1;
+    if (lane == 0 && !mbar_wait(smem_u32(&bar_mma), phase, kWaitNs)) {
+      report(dev_status, MLA_ERR_TIMEOUT);
+      ok = 0;
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok) mbar_wait(smem_u32(&bar_mma), phase, kWaitNs);
+    tc_fence_after();
+    // Warp w drains output columns 32(w%4).. (its lane quadrant) for query rows 32(w/4)..: each thread
+    // holds one output column of 32 rows -> a [64 rows x 128] bf16 staging tile over o_lat's space.
+    __nv_bfloat16 *stg = reinterpret_cast<__nv_bfloat16 *>(ol);
+    constexpr int lds = kDv + 8;
+    {
+      uint32_t v[32];
+      if (warp < 8) {
+        tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 32 * (warp >> 2), v);
+        tmem_wait_ld();
+      }
+      __syncthreads();   // every thread is past its reads of o_lat (the MMAs completed before the loads)
+      ok = ok && s_loaded;
+      if (warp < 8)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          stg[(32 * (warp >> 2) + i) * lds + (warp & 3) * 32 + lane] = __float2bfloat16_rn(__uint_as_float(v[i]));
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (ok)
+      for (int c = tid; c < kR * (kDv / 8); c += kCombThreads) {
+        const int rr = c >> 4, q8 = c & 15, g = g0 + rr;
+        if (g < rows)
+          *reinterpret_cast<uint4 *>(out + ((int64_t)g * H + s) * kDv + q8 * 8) =
+              *reinterpret_cast<const uint4 *>(stg + rr * lds + q8 * 8);
+      }
+    __syncthreads();   // the staged rows have left before the next merge
+    tc_fence_after();
+  }
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, kCombRows);
@@ -1556,14 +1572,15 @@ namespace {
 // out [rows][H][128] = (pieces of each row, merged) . W_UV^(s) per head s, on the tensor cores;
 // lse (if non-null) gets the merged log-sum-exps.
 template <typename P, int kTpr>
-int launch_merge_wuv_as(const CUtensorMap &mw, const mla_dims &d, int rows, const P &pc, void *out, float *lse,
+int launch_merge_wuv_as(const CUtensorMap &mw, int sms, const mla_dims &d, int rows, const P &pc, void *out, float *lse,
                         int *dev_status, cudaStream_t st) {
   const size_t smem = 1024 + kOlBytes + kWuvBytes;
   static std::atomic<int> smem_set[kSmemCacheDevs];
   if (smem_limit(tc_combine_kernel<P, kTpr>, smem, smem_set) != cudaSuccess) return MLA_ERR_CUDA;
-  const dim3 grid(d.n_heads, (rows + kCombRows - 1) / kCombRows);
-  return launch_pdl(tc_combine_kernel<P, kTpr>, grid, dim3(kCombThreads), smem, st, mw, pc, rows, lse,
-                    static_cast<__nv_bfloat16 *>(out), dev_status) == cudaSuccess
+  constexpr int kR = kCombThreads / kTpr;
+  const int tiles = (rows + kR - 1) / kR, per = sms / d.n_heads > 1 ? sms / d.n_heads : 1;
+  return launch_pdl(tc_combine_kernel<P, kTpr>, dim3(d.n_heads, tiles < per ? tiles : per), dim3(kCombThreads), smem, st, mw,
+                    pc, rows, lse, static_cast<__nv_bfloat16 *>(out), dev_status) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }
@@ -1575,11 +1592,15 @@ int launch_merge_wuv(const mla_dims &d, int rows, const P &pc, const void *w_uv,
   CUtensorMap mw;
   int rc = make_map(&mw, w_uv, kDv, (uint64_t)d.n_heads * kDc, (uint64_t)kDv * 2);
   if (rc) return rc;
-  // As many threads per row as the rows of a tile leave.
-  if (rows <= 4) return launch_merge_wuv_as<P, 64>(mw, d, rows, pc, out, lse, dev_status, st);
-  if (rows <= 16) return launch_merge_wuv_as<P, 16>(mw, d, rows, pc, out, lse, dev_status, st);
-  if (rows <= 32) return launch_merge_wuv_as<P, 8>(mw, d, rows, pc, out, lse, dev_status, st);
-  return launch_merge_wuv_as<P, 4>(mw, d, rows, pc, out, lse, dev_status, st);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  // The fewest rows per CTA with which every CTA is resident at once.
+  auto fits = [&](int r) { return (int64_t)d.n_heads * ((rows + r - 1) / r) <= sms; };
+  if (fits(8)) return launch_merge_wuv_as<P, 64>(mw, sms, d, rows, pc, out, lse, dev_status, st);
+  if (fits(16)) return launch_merge_wuv_as<P, 32>(mw, sms, d, rows, pc, out, lse, dev_status, st);
+  if (fits(32)) return launch_merge_wuv_as<P, 16>(mw, sms, d, rows, pc, out, lse, dev_status, st);
+  return launch_merge_wuv_as<P, 8>(mw, sms, d, rows, pc, out, lse, dev_status, st);
 }
 
 }  // namespace
