@@ -227,7 +227,7 @@ SharedLayout shared_layout(const mla_dims *d, int B, int n_q, int num_groups) {
   const int C = shared_clusters_for_device();
   const int clusters = C > 0 ? C : kSharedMaxClusters;
   // A list of n units cut at most clusters - 1 times leaves at most n + clusters - 1 partials.
-  const size_t rows = (size_t)(units + clusters) * kSharedUnitRows;
+  const size_t rows = (size_t)(units + clusters) * kSharedPartRows;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -241,7 +241,7 @@ SharedLayout shared_layout(const mla_dims *d, int B, int n_q, int num_groups) {
   L.seq_off = take((size_t)B * sizeof(int2));
   L.own_off = take((size_t)(B + 1) * sizeof(int));
   L.scratch_off = take(shared_plan_words(B, units, num_groups) * sizeof(int));
-  L.o_off = take(rows * d->d_c * 2);
+  L.o_off = take(rows * d->d_c * sizeof(float));
   L.lse_off = take(rows * sizeof(float));
   L.total = off;
   return L;
@@ -446,13 +446,13 @@ int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *q_nope, 
   const bool tiled = dims->cache_layout == MLA_CACHE_TILED;
   if ((reinterpret_cast<uintptr_t>(c_kv) & 15) || (!tiled && (reinterpret_cast<uintptr_t>(k_pe) & 15)))
     return MLA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(out) & 15) || (reinterpret_cast<uintptr_t>(w_uv) & 15)) return MLA_ERR_UNSUPPORTED;
   char *ws = static_cast<char *>(workspace);
   void *qbuf = ws + L.q_off;
   const SharedPlan pl{reinterpret_cast<SharedShare *>(ws + L.shares_off), reinterpret_cast<SharedUnit *>(ws + L.units_off),
                       reinterpret_cast<int2 *>(ws + L.parts_off), reinterpret_cast<int2 *>(ws + L.seq_off),
                       reinterpret_cast<int *>(ws + L.own_off), reinterpret_cast<int *>(ws + L.scratch_off)};
-  __nv_bfloat16 *o_part = reinterpret_cast<__nv_bfloat16 *>(ws + L.o_off);
-  float *lse_part = reinterpret_cast<float *>(ws + L.lse_off);
+  float *o_part = reinterpret_cast<float *>(ws + L.o_off), *lse_part = reinterpret_cast<float *>(ws + L.lse_off);
   const CacheView cv{c_kv, k_pe, dims->ckv_stride, dims->kpe_stride, block_table, max_blocks_per_seq, num_blocks,
                      dims->block_size, dims->cache_layout, dims->d_c, dims->d_c + dims->d_rope};
   // (1) Who shares what and which cluster does what, and the latent queries; (2) the shared keys for all rows of a group
@@ -470,9 +470,7 @@ int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *q_nope, 
     if ((rc = absorb_dispatch(ab, true, dev_status, st))) return rc;
   }
   if ((rc = launch_shared_attention(*dims, n_q, max_seqlen, pl, qbuf, cv, seqlens, o_part, lse_part, dev_status, st))) return rc;
-  const SharedPieces pc{o_part, lse_part, pl.unit_parts, pl.seq_group, n_q, dims->n_heads,
-                        shared_unit_rows(n_q * dims->n_heads)};
-  return launch_tc_combine_shared(*dims, B, n_q, pc, w_uv, out, lse, dev_status, st);
+  return launch_shared_combine(*dims, B, n_q, pl, o_part, lse_part, w_uv, out, lse, dev_status, st);
 }
 
 // What the two bookkeeping calls check alike.

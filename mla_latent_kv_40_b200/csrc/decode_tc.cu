@@ -1059,6 +1059,17 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeUnroll = 4;
 constexpr int kMaxSegPerUnit = kMaxClusters + 1;
 
+// acc[0..8) += w * the eight bf16 of v.
+__device__ __forceinline__ void add8(const uint4 &v, float w, float *acc) {
+  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = __bfloat1622float2(h[e]);
+    acc[2 * e] = fmaf(w, f.x, acc[2 * e]);
+    acc[2 * e + 1] = fmaf(w, f.y, acc[2 * e + 1]);
+  }
+}
+
 template <typename Row>
 __device__ __forceinline__ void merge_row(int lane, int ns, const __nv_bfloat16 *part, const float *lse, Row row,
                                           __nv_bfloat16 *dst, float *lse_dst) {
@@ -1090,15 +1101,7 @@ __device__ __forceinline__ void merge_row(int lane, int ns, const __nv_bfloat16 
 #pragma unroll
     for (int i = 0; i < kMergeUnroll; ++i)
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const __nv_bfloat162 *xh = reinterpret_cast<const __nv_bfloat162 *>(&x[i][hh]);
-#pragma unroll
-        for (int e2 = 0; e2 < 4; ++e2) {
-          const float2 f = __bfloat1622float2(xh[e2]);
-          v[8 * hh + 2 * e2] = fmaf(wk[i], f.x, v[8 * hh + 2 * e2]);
-          v[8 * hh + 2 * e2 + 1] = fmaf(wk[i], f.y, v[8 * hh + 2 * e2 + 1]);
-        }
-      }
+      for (int hh = 0; hh < 2; ++hh) add8(x[i][hh], wk[i], v + 8 * hh);
   }
   dst += 8 * lane;
 #pragma unroll
@@ -1190,29 +1193,6 @@ __device__ __forceinline__ PieceRows piece_rows(const Pieces &pc, int rows, int 
   return r;
 }
 
-__device__ __forceinline__ PieceRows piece_rows(const SharedPieces &pc, int, int g, int s) {
-  PieceRows r;
-  const int2 sg = pc.seq_group[g / pc.n_q];
-  const int q = g * pc.H + s - sg.y;   // row within the group
-  const int2 up = pc.unit_parts[sg.x + q / pc.unit_rows];
-  r.first = (int64_t)up.x * kSharedUnitRows + q % pc.unit_rows;
-  r.stride = kSharedUnitRows;
-  r.ns = up.y;
-  return r;
-}
-
-// As tc_merge_kernel, for the partials of a decode over shared prefixes.
-__global__ void __launch_bounds__(kMergeThreads)
-shared_merge_kernel(const SharedPieces pc, int rows, __nv_bfloat16 *o_lat, float *lse_out) {
-  sm100::grid_dep_launch();
-  sm100::grid_dep_wait();
-  const int64_t item = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  if (item >= (int64_t)rows * pc.H) return;
-  const PieceRows pr = piece_rows(pc, rows, (int)(item / pc.H), (int)(item % pc.H));
-  merge_row(threadIdx.x & 31, pr.ns, pc.part, pc.lse, [&](int k) { return pr.at(k); }, o_lat + item * kDc,
-            lse_out ? lse_out + item : nullptr);
-}
-
 // CTA = (head s, 512 / kTpr query rows (b, j), 8 to 64): the rows' pieces are merged by their
 // log-sum-exps straight into the B operand tile of the W_UV product (o_lat [64 rows x 512], K-major,
 // 128-byte swizzled, bf16), then out^T [d_v x 64] = W_UV^(s)T . o_lat^T on the tensor cores, with W_UV
@@ -1232,9 +1212,9 @@ constexpr uint32_t kOlBytes = kCombRows * kDc * 2;         // o_lat: [8 K-chunks
 constexpr uint32_t kWuvBytes = kDc * kDv * 2;              // W_UV^T: [8 K-chunks][2 M-chunks][64 K rows][128 B]
 static_assert(kCombThreads == 8 * kCombRows, "eight merging threads per row of the largest tile");
 
-template <typename P, int kTpr>
+template <int kTpr>
 __global__ void __launch_bounds__(kCombThreads)
-tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int rows, float *lse_out,
+tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const Pieces pc, int rows, float *lse_out,
                   __nv_bfloat16 *out, int *dev_status) {
   extern __shared__ unsigned char csm_raw[];
   unsigned char *csm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(csm_raw) + 1023) & ~uintptr_t(1023));
@@ -1310,25 +1290,16 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int row
 #pragma unroll
           for (int kk = 0; kk < kFly; ++kk)
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-              const __nv_bfloat162 *xh = reinterpret_cast<const __nv_bfloat162 *>(&x[kk][i]);
-#pragma unroll
-              for (int e2 = 0; e2 < 4; ++e2) {
-                const float2 f = __bfloat1622float2(xh[e2]);
-                acc[i][2 * e2] = fmaf(wk[kk], f.x, acc[i][2 * e2]);
-                acc[i][2 * e2 + 1] = fmaf(wk[kk], f.y, acc[i][2 * e2 + 1]);
-              }
-            }
+            for (int i = 0; i < kAtOnce; ++i) add8(x[kk][i], wk[kk], acc[i]);
         }
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
           const int cb = kTpr * (kAtOnce * hh + i) + q, kc = cb >> 3, jj = cb & 7;
-          uint4 packed;
-          packed.x = pack_bf16x2(acc[i][0], acc[i][1]);
-          packed.y = pack_bf16x2(acc[i][2], acc[i][3]);
-          packed.z = pack_bf16x2(acc[i][4], acc[i][5]);
-          packed.w = pack_bf16x2(acc[i][6], acc[i][7]);
-          *reinterpret_cast<uint4 *>(ol + kc * 8192 + (rr >> 3) * 1024 + (rr & 7) * 128 + ((jj ^ (rr & 7)) << 4)) = packed;
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(acc[i][2 * e], acc[i][2 * e + 1]);
+          unsigned char *at = ol + kc * 8192 + (rr >> 3) * 1024 + (rr & 7) * 128 + ((jj ^ (rr & 7)) << 4);
+          *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       if (q == 0 && lse_out && g < rows) lse_out[(int64_t)g * H + s] = sum > 0.f ? m + logf(sum) : -CUDART_INF_F;
@@ -1338,23 +1309,27 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const P pc, int row
     __syncthreads();
     tc_fence_after();
     tmem = tmem_slot;
-    if (tid == 0) {
-      if (!mbar_wait(smem_u32(&bar_w), 0, kWaitNs)) {
-        report(dev_status, MLA_ERR_TIMEOUT);
-        loaded = 0;
-      }
-      s_loaded = loaded;
-    }
     // Without its operands the MMA is skipped; its barrier is still completed (commit with nothing issued).
-    if (tid == 0) {
+    if (warp == 0) {
+      if (lane == 0) {
+        if (!mbar_wait(smem_u32(&bar_w), 0, kWaitNs)) {
+          report(dev_status, MLA_ERR_TIMEOUT);
+          loaded = 0;
+        }
+        s_loaded = loaded;
+      }
+      loaded = __shfl_sync(0xffffffffu, loaded, 0);
       tc_fence_after();
       const uint32_t idesc = idesc_bf16_f32(128, kCombRows, true, false);
-      for (int kc = 0; kc < kDc / 64 && loaded; ++kc)
+      const uint64_t ad = smem_desc_sw128(smem_u32(wa), 8192, 1024), bd = smem_desc_sw128(smem_u32(ol), 16, 1024);
+      if (loaded)
+#pragma unroll 1
+        for (int kc = 0; kc < kDc / 64; ++kc)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss(tmem, smem_desc_sw128(smem_u32(wa + kc * 16384) + kk * 2048, 8192, 1024),
-                 smem_desc_sw128(smem_u32(ol + kc * 8192) + kk * 32, 16, 1024), idesc, (kc | kk) ? 1u : 0u);
-      tc_commit(smem_u32(&bar_mma));
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss_warp(tmem, ad + ((kc * 16384 + kk * 2048) >> 4), bd + ((kc * 8192 + kk * 32) >> 4), idesc,
+                        (kc | kk) ? 1u : 0u);
+      tc_commit_warp(smem_u32(&bar_mma));
     }
     ok = 1;
     if (lane == 0 && !mbar_wait(smem_u32(&bar_mma), phase, kWaitNs)) {
@@ -1569,24 +1544,23 @@ int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, co
 
 namespace {
 
-// out [rows][H][128] = (pieces of each row, merged) . W_UV^(s) per head s, on the tensor cores;
-// lse (if non-null) gets the merged log-sum-exps.
-template <typename P, int kTpr>
-int launch_merge_wuv_as(const CUtensorMap &mw, int sms, const mla_dims &d, int rows, const P &pc, void *out, float *lse,
-                        int *dev_status, cudaStream_t st) {
+template <int kTpr>
+int launch_merge_wuv_as(const CUtensorMap &mw, int sms, const mla_dims &d, int rows, const Pieces &pc, void *out,
+                        float *lse, int *dev_status, cudaStream_t st) {
   const size_t smem = 1024 + kOlBytes + kWuvBytes;
   static std::atomic<int> smem_set[kSmemCacheDevs];
-  if (smem_limit(tc_combine_kernel<P, kTpr>, smem, smem_set) != cudaSuccess) return MLA_ERR_CUDA;
+  if (smem_limit(tc_combine_kernel<kTpr>, smem, smem_set) != cudaSuccess) return MLA_ERR_CUDA;
   constexpr int kR = kCombThreads / kTpr;
   const int tiles = (rows + kR - 1) / kR, per = sms / d.n_heads > 1 ? sms / d.n_heads : 1;
-  return launch_pdl(tc_combine_kernel<P, kTpr>, dim3(d.n_heads, tiles < per ? tiles : per), dim3(kCombThreads), smem, st, mw,
+  return launch_pdl(tc_combine_kernel<kTpr>, dim3(d.n_heads, tiles < per ? tiles : per), dim3(kCombThreads), smem, st, mw,
                     pc, rows, lse, static_cast<__nv_bfloat16 *>(out), dev_status) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }
 
-template <typename P>
-int launch_merge_wuv(const mla_dims &d, int rows, const P &pc, const void *w_uv, void *out, float *lse,
+// out [rows][H][128] = (pieces of each row, merged) . W_UV^(s) per head s, on the tensor cores;
+// lse (if non-null) gets the merged log-sum-exps.
+int launch_merge_wuv(const mla_dims &d, int rows, const Pieces &pc, const void *w_uv, void *out, float *lse,
                      int *dev_status, cudaStream_t st) {
   // W_UV as [H * 512 rows][128] (boxes of 64 rows x 64 columns).
   CUtensorMap mw;
@@ -1597,10 +1571,10 @@ int launch_merge_wuv(const mla_dims &d, int rows, const P &pc, const void *w_uv,
     return MLA_ERR_CUDA;
   // The fewest rows per CTA with which every CTA is resident at once.
   auto fits = [&](int r) { return (int64_t)d.n_heads * ((rows + r - 1) / r) <= sms; };
-  if (fits(8)) return launch_merge_wuv_as<P, 64>(mw, sms, d, rows, pc, out, lse, dev_status, st);
-  if (fits(16)) return launch_merge_wuv_as<P, 32>(mw, sms, d, rows, pc, out, lse, dev_status, st);
-  if (fits(32)) return launch_merge_wuv_as<P, 16>(mw, sms, d, rows, pc, out, lse, dev_status, st);
-  return launch_merge_wuv_as<P, 8>(mw, sms, d, rows, pc, out, lse, dev_status, st);
+  if (fits(8)) return launch_merge_wuv_as<64>(mw, sms, d, rows, pc, out, lse, dev_status, st);
+  if (fits(16)) return launch_merge_wuv_as<32>(mw, sms, d, rows, pc, out, lse, dev_status, st);
+  if (fits(32)) return launch_merge_wuv_as<16>(mw, sms, d, rows, pc, out, lse, dev_status, st);
+  return launch_merge_wuv_as<8>(mw, sms, d, rows, pc, out, lse, dev_status, st);
 }
 
 }  // namespace
@@ -1626,19 +1600,6 @@ int launch_tc_combine(const mla_dims &d, int B, int n_q, const int32_t *seqlens,
   return launch_pdl(tc_merge_kernel, mgrid, dim3(kMergeThreads), 0, st, B, n_q, d.n_heads, n_rb, max_segs,
                     reinterpret_cast<const int *>(w + L.seg_info), reinterpret_cast<const __nv_bfloat16 *>(w + L.o_part),
                     reinterpret_cast<const float *>(w + L.lse_part), static_cast<__nv_bfloat16 *>(out), lse) == cudaSuccess
-             ? MLA_OK
-             : MLA_ERR_CUDA;
-}
-
-int launch_tc_combine_shared(const mla_dims &d, int B, int n_q, const SharedPieces &pc, const void *w_uv, void *out,
-                             float *lse, int *dev_status, cudaStream_t st) {
-  if (w_uv && (d.d_v != kDv || (reinterpret_cast<uintptr_t>(w_uv) & 15))) return MLA_ERR_UNSUPPORTED;
-  const int rows = B * n_q;
-  if (w_uv) return launch_merge_wuv(d, rows, pc, w_uv, out, lse, dev_status, st);
-  const int64_t warps = (int64_t)rows * d.n_heads;
-  const dim3 mgrid((unsigned)((warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32)));
-  return launch_pdl(shared_merge_kernel, mgrid, dim3(kMergeThreads), 0, st, pc, rows, static_cast<__nv_bfloat16 *>(out),
-                    lse) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }

@@ -19,17 +19,6 @@ int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, co
 // Merge of the partials, and the W_UV product in the same kernel when w_uv != NULL.
 int launch_tc_combine(const mla_dims &d, int B, int n_q, const int32_t *seqlens, int max_seqlen, const void *w_uv,
                       void *out, float *lse, void *ws, int *dev_status, cudaStream_t st);
-// Where the partials of a decode over shared prefixes live (see shared_tc.cuh).
-constexpr int kSharedUnitRows = 256;   // rows of a partial
-struct SharedPieces {
-  const __nv_bfloat16 *part;   // rows of 512 bf16
-  const float *lse;
-  const int2 *unit_parts;      // first partial and number of partials of every unit
-  const int2 *seq_group;       // [B]: first unit of the sequence's group, the group's first query row
-  int n_q, H, unit_rows;       // unit_rows: query rows of a full unit
-};
-int launch_tc_combine_shared(const mla_dims &d, int B, int n_q, const SharedPieces &pc, const void *w_uv, void *out,
-                             float *lse, int *dev_status, cudaStream_t st);
 // True when stacked partials of this shape merge on the path below (bf16, d_c 512, d_v 128 with
 // W_UV, 16-byte aligned rows).
 bool tc_merge_parts_supported(const mla_dims &d, const void *o_parts, const void *w_uv, const void *out);

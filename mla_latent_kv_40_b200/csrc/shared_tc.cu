@@ -24,8 +24,8 @@
 //
 // The issuing warps run whole, and each MMA is issued by the elected lane: with warp-uniform descriptors the issue
 // keeps up with the pipe from one warp.  Reference maximum, row sums, rounding of P and of the partials as in the
-// per-sequence kernel (decode_tc.cu): lazy maximum in log2 units, sums of P in fp32 before its rounding, O / l in
-// bf16 per segment.  The (unit, tile) list is cut into equal runs, one per cluster; a unit cut between clusters
+// per-sequence kernel (decode_tc.cu): lazy maximum in log2 units, sums of P in fp32 before its rounding; but O / l of a
+// piece stays in fp32 (in bf16 it cost the merged result a rounding, 0.0034 instead of 0.0030 of its norm).  The (unit, tile) list is cut into equal runs, one per cluster; a unit cut between clusters
 // leaves one partial per piece, merged with the sequences' own partials by the combine.
 // Every wait is bounded; on expiry the kernel reports MLA_ERR_TIMEOUT, drains its copies, frees its tensor memory
 // and returns.
@@ -50,7 +50,7 @@ using namespace sm100;
 constexpr int kPage = kSharedPage;                 // keys of a page
 constexpr int kDc = 512, kDr = 64, kW = kDc + kDr;
 constexpr int kRows = 128;                         // query rows per CTA
-constexpr int kUnitRows = 256;                     // two CTAs' rows, and the rows of a partial
+constexpr int kUnitRows = kSharedPartRows;         // two CTAs' rows
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
 constexpr uint32_t kChunkBytes = kPage * 128;      // [64 keys x 64 dims] bf16, 128-byte swizzled
@@ -128,8 +128,7 @@ struct Params {
   const int *own_pages;
   int max_blocks_per_seq, num_blocks, block_size, H, n_q, max_seqlen;
   float scale_log2;
-  __nv_bfloat16 *o_part;
-  float *lse_part;
+  float *o_part, *lse_part;
   int *dev_status;
   const unsigned char *tiled;           // tiled pool, or NULL: row pool through the tensor maps
 };
@@ -843,41 +842,37 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         const int64_t prow = it.part_row() + kRows * side + r;
         const int rows = it.un.rows - kRows * (int)side;   // of this CTA
         const bool live = r < rows;
-        __nv_bfloat16 *dst = p.o_part + prow * kDc;
         // Columns 256 g .. are rank 2's dims 128 g .. 128 g + 127, then rank 3's, 256 further on.
         if ((warp & 3) * 32 >= rows) {
           // no rows of the unit here
         } else if (q.pages >= 2) {
-          // 64 columns at a time through 4 KB of a P slot whose MMAs are complete (the run's last two: one per group), so
-          // that rows leave in whole 128-byte lines: 16 lanes x 32 bytes of different rows took 5 us of LSU time a unit.
+          // 32 columns at a time through 4 KB of a P slot whose MMAs are complete (the run's last two: one per group), so
+          // that rows leave in whole 128-byte lines: stores of 32 lanes to 32 rows took 5 us of LSU time a unit.
           unsigned char *stg = tiles + kPOff + ((q.np - 2 + g) % kPSlots) * kPSlotBytes + (warp & 3) * 4096;
-          __nv_bfloat16 *out = p.o_part + (it.part_row() + kRows * (int)side + (warp & 3) * 32) * kDc + 8 * (lane & 7);
+          float *out = p.o_part + (it.part_row() + kRows * (int)side + (warp & 3) * 32) * kDc + 4 * (lane & 7);
           const int left = rows - (warp & 3) * 32 - (lane >> 3);
+          uint32_t v[32];
+          tmem_ld32(tbase + lane_off + ocol, v);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[2][32];
-            tmem_ld32(tbase + lane_off + ocol + 64 * c, v[0]);
-            tmem_ld32(tbase + lane_off + ocol + 64 * c + 32, v[1]);
+          for (int c = 0; c < 8; ++c) {
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(v[i >> 2][8 * (i & 3) + 2 * e]) * inv,
-                                   __uint_as_float(v[i >> 2][8 * (i & 3) + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4 *>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4 *>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                  make_float4(__uint_as_float(v[4 * i]) * inv, __uint_as_float(v[4 * i + 1]) * inv,
+                              __uint_as_float(v[4 * i + 2]) * inv, __uint_as_float(v[4 * i + 3]) * inv);
             __syncwarp();
-            const int dim = 256 * (c >> 1) + 128 * g + 64 * (c & 1);
+            tmem_ld32(tbase + lane_off + ocol + 32 * min(c + 1, 7), v);   // on its way while these are stored
+            const int dim = 256 * (c >> 2) + 128 * g + 32 * (c & 3);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int lr = 4 * k + (lane >> 3);
-              const uint4 y = *reinterpret_cast<const uint4 *>(stg + lr * 128 + (((lane & 7) ^ (lr & 7)) << 4));
-              if (4 * k < left) *reinterpret_cast<uint4 *>(out + (int64_t)lr * kDc + dim) = y;
+              const float4 y = *reinterpret_cast<const float4 *>(stg + lr * 128 + (((lane & 7) ^ (lr & 7)) << 4));
+              if (4 * k < left) *reinterpret_cast<float4 *>(out + (int64_t)lr * kDc + dim) = y;
             }
             __syncwarp();
           }
+          tmem_wait_ld();
           fence_proxy_async_smem();   // the slot is written by copies again
         } else {
 #pragma unroll 1
@@ -888,12 +883,12 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             const int dim = 256 * (c >> 2) + 128 * g + 32 * (c & 3);
             if (live)
 #pragma unroll
-              for (int i = 0; i < 32; i += 16) {
+              for (int i = 0; i < 32; i += 8) {
                 uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  w[e] = pack_bf16x2(__uint_as_float(v[i + 2 * e]) * inv, __uint_as_float(v[i + 2 * e + 1]) * inv);
-                st_global_v8(dst + dim + i, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(v[i + e]) * inv);
+                st_global_v8(p.o_part + prow * kDc + dim + i, make_uint4(w[0], w[1], w[2], w[3]),
+                             make_uint4(w[4], w[5], w[6], w[7]));
               }
           }
         }
@@ -982,7 +977,7 @@ int launch_shared_plan(const SharedPlanArgs &a, cudaStream_t st) {
 }
 
 int launch_shared_attention(const mla_dims &d, int n_q, int max_seqlen, const SharedPlan &pl, const void *q_abs,
-                            const CacheView &cache, const int32_t *seqlens, __nv_bfloat16 *o_part, float *lse_part,
+                            const CacheView &cache, const int32_t *seqlens, float *o_part, float *lse_part,
                             int *dev_status, cudaStream_t st) {
   const bool tiled = cache.layout == MLA_CACHE_TILED;
   CUtensorMap mc, mpe;

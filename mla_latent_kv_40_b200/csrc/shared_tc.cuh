@@ -24,6 +24,7 @@ struct SharedShare {
 };
 static_assert(sizeof(SharedShare) == 64, "read as four 16-byte words");
 constexpr int kSharedPage = 64;      // keys of a page
+constexpr int kSharedPartRows = 256; // rows of a partial
 constexpr int kSharedMembers = 32;
 // Query rows of a full unit of sequences with R rows each.
 __host__ __device__ constexpr int shared_unit_rows(int R) { return R >= 8 ? 256 : kSharedMembers * R; }
@@ -58,10 +59,14 @@ struct SharedPlanArgs {
 int launch_shared_plan(const SharedPlanArgs &a, cudaStream_t st);
 // The plan and the query absorption in one launch (absorb_tc_supported shapes).
 int launch_absorb_plan(const AbsorbArgs &ab, const SharedPlanArgs &plan, int *dev_status, cudaStream_t st);
-// Attention of every unit over its pages: partials o_part [256 (u + c) + row][512] (bf16, normalised by their own
-// sums) and lse_part of cluster c's share of unit u.
+// Attention of every unit over its pages: partials o_part [256 (u + c) + row][512] (normalised by their own sums) and
+// lse_part of cluster c's share of unit u.
 int launch_shared_attention(const mla_dims &d, int n_q, int max_seqlen, const SharedPlan &pl, const void *q_abs,
-                            const CacheView &cache, const int32_t *seqlens, __nv_bfloat16 *o_part, float *lse_part,
+                            const CacheView &cache, const int32_t *seqlens, float *o_part, float *lse_part,
                             int *dev_status, cudaStream_t st);
+// Merge of the partials, and the W_UV product when w_uv != NULL (else out is o_lat).
+int launch_shared_combine(const mla_dims &d, int B, int n_q, const SharedPlan &pl, const float *o_part,
+                          const float *lse_part, const void *w_uv, void *out, float *lse, int *dev_status,
+                          cudaStream_t st);
 
 }  // namespace mla
