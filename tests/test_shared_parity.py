@@ -250,6 +250,141 @@ def test_shared_bad_block_of_the_prefix_is_reported(lib):
         assert c.result()[2] == -6
 
 
+def _heads(h):
+    return Dims(**{**V2_LITE, "n_heads": h})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,n_q", [(1, 1), (4, 1), (7, 1), (8, 1), (9, 1), (80, 2), (96, 2), (128, 2), (255, 1), (256, 1)])
+def test_shared_head_counts(lib, heads, n_q):
+    """Units of up to 32 sequences, units that cut a sequence's rows, one sequence per unit: 70 sequences (7 at many
+    heads) in three groups, tails of one to three pages, one page shared and many."""
+    r = np.random.default_rng(heads)
+    n = 70 if heads <= 9 else 7
+    cut = sorted(r.choice(np.arange(1, n), 2, replace=False).tolist())
+    lens = r.integers(n_q, 190, n)
+    groups, at = [], 0
+    for p, end in zip((64, 1280, 192), cut + [n]):
+        groups.append((p, [int(p + x) for x in lens[at:end]]))
+        at = end
+    inp = make_shared(_heads(heads), groups, n_q, 64, seed=heads)
+    c = Call(lib, inp, heads % 2)
+    c.run()
+    check(inp, c.result(), some(inp, 12, 3, seed=heads))
+
+
+@pytest.mark.gpu
+def test_shared_many_sequences_and_groups(lib):
+    """3000 sequences in some 1200 groups (empty ones too): the plan works outside shared memory."""
+    r = np.random.default_rng(3)
+    B = 3000
+    bounds = np.concatenate(([0], np.sort(r.integers(0, B + 1, 1199)), [B]))
+    groups = [(int(r.integers(0, 3)) * 64, [int(x) for x in r.integers(1, 200, b - a)]) for a, b in zip(bounds, bounds[1:])]
+    inp = make_shared(_heads(2), groups, 1, 64, seed=4)
+    c = Call(lib, inp)
+    c.run()
+    check(inp, c.result(), some(inp, 60, 2))
+
+
+@pytest.mark.gpu
+def test_shared_long_runs_of_pages(lib):
+    """A unit per cluster and 74 pages each: the page lookups move on, and every barrier goes round many times."""
+    inp = make_shared(V3D, [(4608, [4608 + 1 + 3 * i for i in range(68)])], 1, 64, seed=21)
+    c = Call(lib, inp)
+    c.run()
+    check(inp, c.result(), some(inp, 3, 2))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(8))
+def test_shared_random_batches(lib, seed):
+    r = np.random.default_rng(100 + seed)
+    heads, bs = int(r.choice([12, 16, 20, 64, 128])), int(r.choice([64, 128, 192]))
+    n_q = int(r.integers(1, 256 // heads + 1)) if heads <= 64 else int(r.integers(1, 3))
+    n_q = min(n_q, 5)
+    groups = []
+    for _ in range(int(r.integers(1, 5))):
+        p = int(r.choice([0, r.integers(1, 300), 64 * r.integers(1, 20)]))
+        groups.append((p, [int(max(n_q, p + r.integers(-40, 400))) for _ in range(int(r.integers(1, 8)))]))
+    inp = make_shared(_heads(heads), groups, n_q, bs, seed=seed)
+    c = Call(lib, inp, seed % 2)
+    c.run()
+    check(inp, c.result(), some(inp, 6, 3, seed))
+
+
+@pytest.mark.gpu
+def test_shared_bad_lengths_are_reported(lib):
+    """A length below n_q or beyond max_seqlen is reported; the other groups' results stand."""
+    inp = make_shared(V2L, [(128, [200, 300, 150]), (64, [100, 90])], 2, 64, seed=17)
+    picks = [x for x in some(inp, 5, 3) if x[0] >= 3]
+    idx = tuple(np.array(picks).T)
+    ref, _ = reference(inp, picks)
+    for bad in (1, 0, -5, 100000):
+        c = Call(lib, inp)
+        c.dev["seqlens"][1] = bad
+        c.run()
+        out, lse, st = c.result()
+        assert st == -6
+        check_close(out[idx], ref[idx], "bf16", "other group")
+
+
+@pytest.mark.gpu
+def test_shared_two_calls_at_once(lib):
+    """Two calls on two streams with workspaces of their own, many times over: the bits of each call alone."""
+    calls = [Call(lib, make_shared(V2L, [(640, [700, 650, 900, 641]), (128, [300, 129])], 1, 64, seed=31)),
+             Call(lib, make_shared(_heads(64), [(1024, [1100, 1030, 1500])], 2, 64, seed=32))]
+    alone = []
+    for c in calls:
+        c.run()
+        alone.append(c.result())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for c, st in zip(calls, streams):
+            c.run(stream=st)
+    for c, (o, l, _) in zip(calls, alone):
+        o1, l1, st = c.result()
+        assert st == 0 and np.array_equal(o, o1) and np.array_equal(l, l1)
+
+
+@pytest.mark.gpu
+def test_shared_graphs_that_share_a_workspace(lib):
+    """Two captured graphs with one workspace, replayed in turn on one stream."""
+    a = Call(lib, make_shared(V2L, [(640, [700, 650, 900, 641]), (128, [300, 129])], 1, 64, seed=33))
+    b = Call(lib, make_shared(V2L, [(192, [200, 250]), (0, [30])], 1, 64, seed=34))
+    for c in (a, b):
+        c.run()
+    want = [a.result(), b.result()]
+    if b.ws.numel() > a.ws.numel():
+        a.ws = b.ws
+    b.ws = a.ws
+    graphs = []
+    for c in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run()
+        graphs.append(g)
+    for c in (a, b):
+        c.out.fill_(float("nan"))
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    for c, (o, l, _) in zip((a, b), want):
+        o1, l1, st = c.result()
+        assert st == 0 and np.array_equal(o, o1) and np.array_equal(l, l1)
+
+
+@pytest.mark.gpu
+def test_shared_refuses_wrong_tensors(lib):
+    inp = make_shared(V2L, [(64, [100, 90])], 1, 64, seed=41)
+    for key, bad in (("q_nope", lambda t: t.float()), ("q_pe", lambda t: t[:, :, :8]), ("seqlens", lambda t: t.long()),
+                     ("block_table", lambda t: t[:, :1]), ("w_uk", lambda t: t.transpose(1, 2)), ("prefix_lens", lambda t: t.repeat(2)),
+                     ("group_offsets", lambda t: t.cpu()), ("q_nope", lambda t: None), ("prefix_lens", lambda t: None)):
+        c = Call(lib, inp)
+        c.dev[key] = bad(c.dev[key])
+        with pytest.raises((TypeError, ValueError, AttributeError)):
+            c.run()
+
+
 def test_shared_host_refusals():
     import mla_latent_kv_40_b200 as mla
     lib = mla._lib
