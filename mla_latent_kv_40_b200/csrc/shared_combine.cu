@@ -8,8 +8,9 @@
 // goes in twice, as the bf16 of its values and the bf16 of what that rounding left; the two products are added in fp32, so
 // that the row reaches W_UV with 16 bits instead of 8 (one rounding less in the result: 0.0030 -> 0.0025 of its norm,
 // 0.0017 being the rounding of the output itself).  The tile then takes 128 KB, and W_UV (128 KB) does not fit beside
-// it: six of its eight 64-row chunks are requested before the kernel waits for the attention, the other two follow into
-// the first two slots when the MMAs have read them (and the tile after that one begins with those two).
+// it: six of its eight 64-row chunks lie in shared memory and two, transposed, in tensor memory (A operand of TS-form
+// MMAs), all of them brought in before the kernel waits for the attention.  (Sending the last two after the first two had
+// been read took 1.4 to 2.5 us more per tile.)
 // Bound by latency: a chain of dependent loads (group, unit, log-sum-exps, pieces), then the MMAs and the stores.  kTpr
 // threads per row, all of a row's blocks of two pieces in flight; the fewest rows per CTA with which every CTA is resident
 // at once (one per SM), further tiles of a head in the same CTA.
@@ -32,8 +33,11 @@ constexpr int kThreads = 256;
 constexpr int kChunks = kDc / 64;                  // K chunks of 64 latent dims
 constexpr uint32_t kOlChunk = 2 * kTile * 128;     // [64 rounded rows, 64 remainder rows][128 B]
 constexpr uint32_t kWChunk = 64 * kDv * 2;         // [2 halves of the output dims][64 latent dims][128 B]
-constexpr int kWSlots = 6;
-constexpr size_t kSmem = 1024 + kChunks * kOlChunk + kWSlots * kWChunk;
+constexpr int kWSmem = 6;                          // chunks of W_UV in shared memory; the others in tensor memory
+constexpr uint32_t kWCol = 2 * kTile;              // tensor-memory columns: the product, then 32 per chunk of W_UV^T
+constexpr uint32_t kTmemCols = 256;
+static_assert(kWCol + (kChunks - kWSmem) * 32 <= kTmemCols, "tensor memory");
+constexpr size_t kSmem = 1024 + kChunks * kOlChunk + kWSmem * kWChunk;
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -117,49 +121,66 @@ __device__ __forceinline__ float merged_lse(float m, float sum) { return sum > 0
 
 template <int kTpr>
 __global__ void __launch_bounds__(kThreads, 1)
-shared_combine_kernel(const __grid_constant__ CUtensorMap map_w, const Pieces pc, int rows, float *lse_out,
-                      __nv_bfloat16 *out, int *dev_status) {
+shared_combine_kernel(const __grid_constant__ CUtensorMap map_w, const __nv_bfloat16 *w_uv, const Pieces pc, int rows,
+                      float *lse_out, __nv_bfloat16 *out, int *dev_status) {
   extern __shared__ unsigned char raw[];
   unsigned char *ol = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   unsigned char *wa = ol + kChunks * kOlChunk;
-  __shared__ __align__(8) uint64_t bars[4];   // W_UV slots 0-1, slots 2-5, slots 0-1 read, product complete
+  __shared__ __align__(8) uint64_t bar_w, bar_mma;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_ok;
   const int s = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t bar_pair = smem_u32(&bars[0]), bar_rest = smem_u32(&bars[1]), bar_read = smem_u32(&bars[2]),
-                 bar_mma = smem_u32(&bars[3]);
   constexpr int kR = kThreads / kTpr;         // rows of a tile
   grid_dep_launch();
-  auto load_chunks = [&](int chunk, int slot, int n, uint32_t bar) {   // one thread
-    mbar_expect_tx(bar, n * kWChunk);
-    for (int i = 0; i < n; ++i)
-      for (int half = 0; half < 2; ++half)
-        tma_load_2d(smem_u32(wa + (slot + i) * kWChunk + half * (kWChunk / 2)), &map_w, 64 * half, s * kDc + 64 * (chunk + i), bar);
-  };
+  // W_UV[s] (an input: no need to wait for the attention).
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    mbar_init(smem_u32(&bar_w), 1);
+    mbar_init(smem_u32(&bar_mma), 1);
     fence_mbar_init();
     tma_prefetch_desc(&map_w);
-    load_chunks(0, 0, 2, bar_pair);           // an input: no need to wait for the attention
-    load_chunks(2, 2, 4, bar_rest);
+    mbar_expect_tx(smem_u32(&bar_w), kWSmem * kWChunk);
+    for (int kc = 0; kc < kWSmem; ++kc)
+      for (int half = 0; half < 2; ++half)
+        tma_load_2d(smem_u32(wa + kc * kWChunk + half * (kWChunk / 2)), &map_w, 64 * half, s * kDc + 64 * kc, smem_u32(&bar_w));
   }
   if (warp == 0) {
-    tmem_alloc(smem_u32(&tmem_slot), 2 * kTile);
+    tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
     tmem_relinquish();
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  // Chunk kWSmem + (warp >> 2), transposed: output dim 32 (warp & 3) + lane is this thread's tensor-memory lane, its
+  // column c holds latent dims 2 c and 2 c + 1 of the chunk.
+  {
+    const __nv_bfloat16 *src = w_uv + ((int64_t)s * kDc + 64 * (kWSmem + (warp >> 2))) * kDv + (warp & 3) * 32 + lane;
+    uint32_t w[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      w[c] = (uint32_t)__bfloat16_as_ushort(src[(2 * c) * kDv]) | ((uint32_t)__bfloat16_as_ushort(src[(2 * c + 1) * kDv]) << 16);
+    tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kWCol + 32 * (warp >> 2), w);
+    tmem_wait_st();
+  }
   grid_dep_wait();   // the plan and the partials
-  uint32_t it = 0;   // tiles done: also the loads of slots 0-1 that are behind
-  bool fine = true;  // warp 0: no wait has given up
-  uint32_t tmem = 0;
+  uint32_t it = 0;   // tiles done
+  bool fine = true;  // warp 0: W_UV has arrived
+  // This thread's row of the tile, its pieces and their weights; those of the next tile are looked up while the MMAs of
+  // this one run.
+  const int rr = tid / kTpr, q = tid % kTpr;
+  PieceRows pr;
+  float m = 0.f, sum = 0.f;
+  auto look_up = [&](int g0) {
+    pr = g0 + rr < rows ? piece_rows(pc, g0 + rr, s) : PieceRows();
+    weigh(pc, pr, m, sum);
+  };
+  look_up(blockIdx.y * kR);
   for (int g0 = blockIdx.y * kR; g0 < rows; g0 += gridDim.y * kR, ++it) {
     {
       // Row rr of the tile (rows past the end: zero; those past kR stay as they are, they touch only their own columns of
       // the product).  This thread's blocks of 8 columns: kTpr i + q.
       constexpr int kNb = 64 / kTpr, kAtOnce = kNb < 8 ? kNb : 8, kFly = kAtOnce >= 4 ? 2 : 8 / kAtOnce;
-      const int rr = tid / kTpr, q = tid % kTpr, g = g0 + rr;
-      const PieceRows pr = g < rows ? piece_rows(pc, g, s) : PieceRows();
-      float m, sum;
-      weigh(pc, pr, m, sum);
+      const int g = g0 + rr;
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
       for (int hh = 0; hh < kNb / kAtOnce; ++hh) {
@@ -189,39 +210,29 @@ shared_combine_kernel(const __grid_constant__ CUtensorMap map_w, const Pieces pc
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    tmem = tmem_slot;
     if (warp == 0) {
-      const uint32_t idesc = idesc_bf16_f32(128, 2 * kTile, true, false);
+      const uint32_t idesc = idesc_bf16_f32(128, 2 * kTile, true, false), idesc_ts = idesc_bf16_f32(128, 2 * kTile, false, false);
       const uint64_t ad = smem_desc_sw128(smem_u32(wa), kWChunk / 2, 1024), bd = smem_desc_sw128(smem_u32(ol), 16, 1024);
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (!fine) return;
-        fine = __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs));
+      if (it == 0) {
+        fine = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_w), 0, kWaitNs));
         if (!fine && lane == 0) report(dev_status, MLA_ERR_TIMEOUT);
         tc_fence_after();
-      };
-      auto product = [&](int chunk, int slot, int n, bool first) {
-        if (!fine) return;
+      }
+      if (fine) {
+#pragma unroll
+        for (int i = 0; i < 4 * (kChunks - kWSmem); ++i)   // 16 latent dims each: 8 columns of W_UV^T
+          mma_ts_warp(tmem, tmem + kWCol + 8 * i, bd + (((kWSmem + i / 4) * kOlChunk + (i & 3) * 32) >> 4), idesc_ts, i ? 1u : 0u);
 #pragma unroll 1
-        for (int i = 0; i < n; ++i)
+        for (int kc = 0; kc < kWSmem; ++kc)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss_warp(tmem, ad + (((slot + i) * kWChunk + kk * 2048) >> 4), bd + (((chunk + i) * kOlChunk + kk * 32) >> 4),
-                        idesc, (first && i == 0 && kk == 0) ? 0u : 1u);
-      };
-      const int pair = it & 1 ? kWSlots : 0, other = kWSlots - pair;   // the chunks in slots 0-1, and those still to come
-      wait(bar_pair, it & 1);
-      product(pair, 0, 2, true);
-      tc_commit_warp(bar_read);
-      wait(bar_rest, 0);
-      product(2, 2, 4, false);
-      wait(bar_read, it & 1);
-      if (fine && lane == 0) load_chunks(other, 0, 2, bar_pair);
-      wait(bar_pair, (it + 1) & 1);
-      product(other, 0, 2, false);
-      tc_commit_warp(bar_mma);   // (completes also with nothing issued)
+            mma_ss_warp(tmem, ad + ((kc * kWChunk + kk * 2048) >> 4), bd + ((kc * kOlChunk + kk * 32) >> 4), idesc, 1u);
+      }
+      tc_commit_warp(smem_u32(&bar_mma));   // (completes also with nothing issued)
       if (lane == 0) s_ok = fine;
     }
-    const bool done = __all_sync(0xffffffffu, mbar_wait(bar_mma, it & 1, kWaitNs));
+    if (g0 + gridDim.y * kR < rows) look_up(g0 + gridDim.y * kR);
+    const bool done = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_mma), it & 1, kWaitNs));
     if (!done && lane == 0) report(dev_status, MLA_ERR_TIMEOUT);
     tc_fence_after();
     // Warp w drains output dims 32 (w & 3) .. of rows 32 (w >> 2) .., the sum of both products, to a [64 x 128] bf16
@@ -253,14 +264,11 @@ shared_combine_kernel(const __grid_constant__ CUtensorMap map_w, const Pieces pc
     tc_fence_after();
   }
   if (warp == 0) {
-    // Copies that a given-up wait left in flight have landed before the shared memory goes away.
-    if (!fine && lane == 0) {
-      mbar_wait(bar_pair, it & 1, kWaitNs);
-      mbar_wait(bar_rest, 0, kWaitNs);
-    }
+    // Copies in flight (none unless the wait gave up, or the CTA had no rows) land before the shared memory goes away.
+    if (lane == 0 && (!fine || it == 0)) mbar_wait(smem_u32(&bar_w), 0, kWaitNs);
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_slot, 2 * kTile);
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -287,14 +295,14 @@ shared_merge_kernel(const Pieces pc, int rows, __nv_bfloat16 *o_lat, float *lse_
 }
 
 template <int kTpr>
-int launch_as(const CUtensorMap &mw, int sms, int rows, const Pieces &pc, void *out, float *lse, int *dev_status,
+int launch_as(const CUtensorMap &mw, const void *w_uv, int sms, int rows, const Pieces &pc, void *out, float *lse, int *dev_status,
               cudaStream_t st) {
   static std::atomic<int> smem_set[kSmemCacheDevs];
   if (smem_limit(shared_combine_kernel<kTpr>, kSmem, smem_set) != cudaSuccess) return MLA_ERR_CUDA;
   constexpr int kR = kThreads / kTpr;
   const int tiles = (rows + kR - 1) / kR, per = sms / pc.H > 1 ? sms / pc.H : 1;
-  return launch_pdl(shared_combine_kernel<kTpr>, dim3(pc.H, tiles < per ? tiles : per), dim3(kThreads), kSmem, st, mw, pc,
-                    rows, lse, static_cast<__nv_bfloat16 *>(out), dev_status) == cudaSuccess
+  return launch_pdl(shared_combine_kernel<kTpr>, dim3(pc.H, tiles < per ? tiles : per), dim3(kThreads), kSmem, st, mw,
+                    static_cast<const __nv_bfloat16 *>(w_uv), pc, rows, lse, static_cast<__nv_bfloat16 *>(out), dev_status) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }
@@ -321,10 +329,10 @@ int launch_shared_combine(const mla_dims &d, int B, int n_q, const SharedPlan &p
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MLA_ERR_CUDA;
   auto fits = [&](int r) { return (int64_t)H * ((rows + r - 1) / r) <= sms; };
-  if (fits(8)) return launch_as<32>(mw, sms, rows, pc, out, lse, dev_status, st);
-  if (fits(16)) return launch_as<16>(mw, sms, rows, pc, out, lse, dev_status, st);
-  if (fits(32)) return launch_as<8>(mw, sms, rows, pc, out, lse, dev_status, st);
-  return launch_as<4>(mw, sms, rows, pc, out, lse, dev_status, st);
+  if (fits(8)) return launch_as<32>(mw, w_uv, sms, rows, pc, out, lse, dev_status, st);
+  if (fits(16)) return launch_as<16>(mw, w_uv, sms, rows, pc, out, lse, dev_status, st);
+  if (fits(32)) return launch_as<8>(mw, w_uv, sms, rows, pc, out, lse, dev_status, st);
+  return launch_as<4>(mw, w_uv, sms, rows, pc, out, lse, dev_status, st);
 }
 
 }  // namespace mla
