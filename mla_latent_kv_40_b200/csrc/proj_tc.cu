@@ -97,7 +97,7 @@ __device__ __forceinline__ void absorb_tc_body(const CUtensorMap &map_w, const C
     if (tid - 32 < half) theta[tid - 32] = rope_theta(tid - 32, a.d_rope, a.rope_base);
     asm volatile("bar.sync 1, 96;" ::: "memory");       // warps 1-3 only
     grid_dep_wait();                                       // q_out may still be read by an earlier kernel
-    constexpr int kRowsPerWarp = 8;
+    constexpr int kRowsPerWarp = 6;                        // 16 rows a CTA (d_c = 512) as 6, 6 and 4 of the three warps
     const int nr = (kTcN - by + ny - 1) / ny;
     for (int w0 = (warp - 1) * kRowsPerWarp; w0 < nr; w0 += 3 * kRowsPerWarp) {
       int pos[kRowsPerWarp];
