@@ -414,8 +414,12 @@ MLA_API int mla_decode_sparse(const mla_dims *dims, int B, int n_q, const void *
  *   prefix length report MLA_ERR_BAD_INDEX, and then nothing is shared.
  *   block_table is required.  w_uv == NULL writes o_lat [B, n_q, H, d_c], as
  *   mla_decode_latent.  The other arguments, outputs and errors as mla_decode.
+ *   Values that are not finite in a sequence's own rows reach that sequence
+ *   alone; in shared rows, every sequence that shares them.
  *   Shapes of the tensor-core path (mla_decode_path) share; other shapes run
- *   every sequence by itself, with the same results.
+ *   every sequence by itself, with the same results.  Where they share, out and
+ *   w_uv must be 16-byte aligned (else MLA_ERR_UNSUPPORTED), and so must c_kv
+ *   and, in the row layout, k_pe (else MLA_ERR_INVALID_ARG).
  *   Workspace: >= mla_decode_shared_workspace_size bytes, 256-byte aligned.
  */
 MLA_API int mla_decode_shared_workspace_size(const mla_dims *dims, int B, int n_q, int max_seqlen, int num_groups,
@@ -470,7 +474,8 @@ MLA_API int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *
  *   seqlens may be cached_lens itself and free_count_out may be free_count
  *   itself: the state of a loop, or of a replayed graph, is updated in place.
  *   The other outputs overlap nothing.  dims: block_size and the checks of
- *   every call.  B <= 8192 (else MLA_ERR_UNSUPPORTED); one kernel, no workspace.
+ *   every call.  B <= 8192 (else MLA_ERR_UNSUPPORTED); one launch, or two where
+ *   there is much to write; no workspace.
  */
 MLA_API int mla_plan_step(const mla_dims *dims, int B, const int32_t *cached_lens, const int32_t *new_lens,
                           int num_groups, const int32_t *group_offsets, const int32_t *prefix_lens,
@@ -494,7 +499,8 @@ MLA_API int mla_plan_step(const mla_dims *dims, int B, const int32_t *cached_len
  *   negative or beyond the table row, or whose prefix is not whole blocks.
  *   Block ids outside [0, num_blocks) are reported (MLA_ERR_BAD_INDEX) and
  *   returned as they are.  seqlens_out may be seqlens and free_count_out may be
- *   free_count.  B <= 8192 (else MLA_ERR_UNSUPPORTED); one kernel, no workspace.
+ *   free_count.  B <= 8192 (else MLA_ERR_UNSUPPORTED); one launch, or two; no
+ *   workspace.
  */
 MLA_API int mla_release_blocks(const mla_dims *dims, int B, const int32_t *done, const int32_t *seqlens,
                                int num_groups, const int32_t *group_offsets, const int32_t *prefix_lens,

@@ -36,6 +36,7 @@
 #include <atomic>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "shared_plan.cuh"
 #include "shared_tc.cuh"
@@ -63,8 +64,9 @@ constexpr int kVStages = 4;                        // a page's 256 latent dims o
 constexpr uint32_t kVStageBytes = 4 * kChunkBytes;
 constexpr uint32_t kPBytes = kRows * kPage * 2;
 constexpr int kPSlots = 5;
-// A page of P travels with its rows' rescale factors: per writer warp 32 factors, a flag word, padding.
+// A page of P travels with its rows' rescale factors: per writer warp 32 factors, a word of flags, padding.
 constexpr uint32_t kPaWords = 36;
+constexpr uint32_t kMoved = 1, kOdd = 2;           // flags: some factor is not 1; some score is not finite
 constexpr uint32_t kPTxBytes = kPBytes + 4 * kPaWords * 4;
 constexpr uint32_t kPSlotBytes = ((kPTxBytes + 1023) / 1024) * 1024;
 constexpr uint32_t kQpeOff = 0;
@@ -103,8 +105,8 @@ enum Bar {
 };
 
 struct Req {
-  int kind;      // 0: before a page's MMAs, rescale O and/or zero the latent rows past the last key; 1: the epilogue
-  int rescale, slot, keys, stage;
+  int kind;      // 0: before a page's MMAs, rescale O and/or tidy the latents; 1: the epilogue
+  int rescale, slot, keys, stage, scan;
   int np, pages;   // 1: pages so far, and those of the run
 };
 
@@ -294,6 +296,26 @@ struct PageRows {
     return __shfl_sync(0xffffffffu, r0, page - base);
   }
 };
+
+// The latents of a page before its MMAs, thread t of 256: rows from `keys` on become zero and, with `scan`, so does every
+// value that is not finite.  The rows that see such a key have NaN from their scores.
+__device__ __noinline__ void tidy_page(unsigned char *vt, int keys, int scan, int t) {
+  // 4 chunks of 64 rows of 8 pieces of 16 bytes; piece t + 256 i lies in row (t >> 3) + 32 (i & 1) of chunk i >> 1.
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    uint4 *at = reinterpret_cast<uint4 *>(vt) + t + 256 * i;
+    if ((t >> 3) + 32 * (i & 1) >= keys) {
+      *at = make_uint4(0, 0, 0, 0);
+    } else if (scan) {
+      const uint4 y = *at;
+      uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] &= ((w[e] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((w[e] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
 
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_pe,
@@ -514,23 +536,23 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             if (!(ok = waitw(sm, bar(B_PFULL + pb), ppar, p.dev_status))) break;
             const uint32_t slot = smem_u32(tiles + kPOff + pb * kPSlotBytes);
             const bool first = g == 2 * it.t0;
-            // Rows past the last key may hold anything (NaN): they must be zero for 0 * row to be 0.
+            // Rows past the last key may hold anything (NaN), and one member's keys may for the others, whose P is 0 there:
+            // 0 * x is 0 for finite x only.
             int own;
             const int m = mem.owner(g, own);
             const int left = m < 0 ? kPage : __shfl_sync(0xffffffffu, mem.keys, m) - kPage * own;
-            uint32_t moved = 0;
-            if (!first) {
-              const float *pa = reinterpret_cast<const float *>(tiles + kPOff + pb * kPSlotBytes + kPBytes);
+            uint32_t flags = 0;
+            const float *pa = reinterpret_cast<const float *>(tiles + kPOff + pb * kPSlotBytes + kPBytes);
 #pragma unroll
-              for (int w = 0; w < 4; ++w) moved |= reinterpret_cast<const uint32_t *>(pa + w * kPaWords)[32];
-            }
+            for (int w = 0; w < 4; ++w) flags |= reinterpret_cast<const uint32_t *>(pa + w * kPaWords)[32];
+            const bool moved = flags & kMoved, odd = flags & kOdd;
             if (!(ok = waitw(sm, bar(B_CFULL + sv), (np / kVStages) & 1, p.dev_status))) break;
-            if (moved || left < kPage) {
+            if (flags || left < kPage) {
               // O is read back for a rescale: the previous page's MMAs must be complete.
               if (moved && !(ok = waitw(sm, bar(B_PVDONE + (np - 1) % kPSlots), ((np - 1) / kPSlots) & 1, p.dev_status)))
                 break;
               if (lane == 0) {
-                sm.req = Req{0, moved != 0, pb, left, sv, 0, 0};
+                sm.req = Req{0, moved, pb, left, sv, odd, 0, 0};
                 mbar_arrive(bar(B_REQ));
               }
               if (!(ok = waitw(sm, bar(B_REQDONE), nfix & 1, p.dev_status))) break;
@@ -558,7 +580,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
           if (!ok) break;
           run_pages = it.pages_end() - 2 * it.t0;
           if (lane == 0) {
-            sm.req = Req{1, 0, 0, 0, 0, (int)np, run_pages};
+            sm.req = Req{1, 0, 0, 0, 0, 0, (int)np, run_pages};
             mbar_arrive(bar(B_REQ));
           }
           __syncwarp();
@@ -659,11 +681,10 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
       const int vis = __shfl_sync(0xffffffffu, mem.keys, max(my_m, 0)) - p.n_q + 1 + (gr % R) / p.H;
       float m_mine = -CUDART_INF_F, l = 0.f;   // l: this group's row sum, relative to m_mine
       const uint32_t ns_end = ns + (uint32_t)(it.t1 - it.t0);
-      for (int t = it.t0; t < it.t1; ++t, ++ns) {
-        const int npg = min(2, it.un.pages - 2 * t);
-        const uint32_t pn = np;             // the tile's first page
-        np += npg;
-        if ((int)(ns & 1) != h) continue;   // the other group's
+      // One tile.  Mixed: some page of it is one member's.  A copy of its own, as the checks alone that such pages need took 4 %
+      // of a batch that is nearly all shared pages.
+      auto tile = [&](auto mixed_tag, int t, int npg, uint32_t pn) __attribute__((always_inline)) {
+        constexpr bool mixed = decltype(mixed_tag)::value;
         waitw(sm, bar(B_SFULL + h), (ns >> 1) & 1, p.dev_status);
         tc_fence_after();
         const uint32_t scol = tbase + lane_off + kSCol + 128 * h;
@@ -686,15 +707,35 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
           const int m = mem.owner(2 * t + pg, own);
           return m < 0 ? kPage : (m == my_m ? vis - kPage * own : 0);
         };
-        const int n0 = seen(0), n1 = npg == 2 ? seen(1) : 0;
+        int n0 = kPage, n1 = kPage;
+        if (mixed) {
+          n0 = seen(0);
+          if (npg == 2) n1 = seen(1);
+        }
         auto mask_page = [&](int n) {   // only pages that some row of the warp does not see whole
-          if (__all_sync(0xffffffffu, n >= kPage)) return;
+          if (!mixed || __all_sync(0xffffffffu, n >= kPage)) return;
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             v[0][k] = k < n ? v[0][k] : __float_as_uint(-CUDART_INF_F);
             v[1][k] = k + 32 < n ? v[1][k] : __float_as_uint(-CUDART_INF_F);
           }
         };
+        // A latent that is not finite leaves no row's score of its key finite (0 * x is NaN), so one warp's rows tell which of
+        // the pages have such.  It matters where a page is one member's among several: the others' P is 0 there, and the value
+        // pair must not multiply that by NaN.  (1 to 2 us of a batch of many own pages; looking at the latents themselves
+        // took 4 to 6 of 110, in shared-memory reads that the MMAs missed.)
+        uint32_t odd = 0;             // kOdd for the first page, kOdd << 8 for the second
+        if (mixed && q4 == 0 && it.un.members > 1) {
+#pragma unroll 1
+          for (int pg = 0; pg < npg; ++pg) {
+            load_page(pg);
+            tmem_wait_ld();
+            float z = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) z = fmaf(__uint_as_float(v[0][k]), 0.f, fmaf(__uint_as_float(v[1][k]), 0.f, z));
+            if (__any_sync(0xffffffffu, (__float_as_uint(z) & 0x7fffffffu) != 0u) && 2 * t + pg >= it.un.shared) odd |= kOdd << (8 * pg);
+          }
+        }
         // The second page only for its maximum (it is read again below), the first one to stay.
         if (npg == 2) {
           load_page(1);
@@ -723,7 +764,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
           l *= exp2f(m_mine - m_ref);   // m_mine = -inf: l is 0 (and m_ref, which never falls, is finite)
           m_mine = m_ref;
         }
-        const unsigned moved = __ballot_sync(0xffffffffu, need && t != it.t0);
+        const uint32_t moved = __any_sync(0xffffffffu, need && t != it.t0) ? kMoved : 0u;
         float psum0 = 0.f, psum1 = 0.f;
         uint32_t pk[32];              // this row's 64 P values of a page
         auto page_p = [&]() {
@@ -739,7 +780,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             }
         };
         // The first page of a tile carries its rows' rescale factors.
-        auto stage = [&](uint32_t page, float factor, bool flag) {
+        auto stage = [&](uint32_t page, float factor, uint32_t flags) {
           unsigned char *stg = staging(page);
           unsigned char *prow = stg + 4096 * q4 + (lane >> 3) * 1024 + (lane & 7) * 128;
 #pragma unroll
@@ -747,7 +788,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             *reinterpret_cast<uint4 *>(prow + ((c ^ (lane & 7)) << 4)) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
           float *pa = reinterpret_cast<float *>(stg + kPBytes) + q4 * kPaWords;
           pa[lane] = factor;
-          if (lane < 4) reinterpret_cast<uint32_t *>(pa + 32)[lane] = (lane == 0 && flag) ? 1u : 0u;
+          if (lane < 4) reinterpret_cast<uint32_t *>(pa + 32)[lane] = lane == 0 ? flags : 0u;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_STGFULL + page % kStgTiles));
@@ -758,13 +799,21 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_light(mapa(bar(B_SEMPTY + h), 0));   // the last read of this S is done
-        stage(pn, alpha, moved != 0);
+        stage(pn, alpha, moved | (odd & kOdd));
         if (npg == 2) {
           mask_page(n1);
           page_p();
-          stage(pn + 1, 1.f, false);
+          stage(pn + 1, 1.f, odd >> 8);
         }
         l += psum0 + psum1;
+      };
+      for (int t = it.t0; t < it.t1; ++t, ++ns) {
+        const int npg = min(2, it.un.pages - 2 * t);
+        const uint32_t pn = np;             // the tile's first page
+        np += npg;
+        if ((int)(ns & 1) != h) continue;   // the other group's
+        if (2 * t + npg > it.un.shared) tile(std::true_type{}, t, npg, pn);
+        else tile(std::false_type{}, t, npg, pn);
       }
       // Row statistics of the run: the group that did not have the last tile passes its sum on, relative to the final
       // reference; the other one sends the total.
@@ -817,13 +866,8 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             tmem_wait_st();
             tc_fence_before();
           }
-          if (q.keys < kPage) {
-            // 4 chunks of 8 pieces of 16 bytes per row; the eight warps share the rows.
-            unsigned char *vt = tiles + q.stage * kVStageBytes;
-            for (int e = threadIdx.x - 128; e < (kPage - q.keys) * 32; e += 256) {
-              const int row = q.keys + (e >> 5);
-              *reinterpret_cast<uint4 *>(vt + ((e >> 3) & 3) * kChunkBytes + row * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
+          if (q.keys < kPage || q.scan) {
+            tidy_page(tiles + q.stage * kVStageBytes, q.keys, q.scan, threadIdx.x - 128);
             fence_proxy_async_smem();
           }
           __syncwarp();

@@ -329,6 +329,34 @@ def test_shared_bad_lengths_are_reported(lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("heads,n_q", [(4, 1), (16, 2), (96, 1), (128, 1)])
+def test_shared_values_that_are_not_finite_stay_with_their_sequence(lib, heads, n_q, layout):
+    """NaN and infinities among one sequence's own keys: the other sequences of the group, whose rows meet these keys
+    with a weight of 0, keep their bits, and the sequence itself has NaN, as in a decode of its own."""
+    groups = [(192, [250, 330, 193 + n_q, 500, 196, 260]), (0, [70, 40])]
+    inp = make_shared(_heads(heads), groups, n_q, 64, seed=heads)
+    c = Call(lib, inp, layout)
+    c.run()
+    want, _, st = c.result()
+    assert st == 0
+    for seq, key, dims, value in ((1, 200, slice(0, 576), float("nan")), (3, 450, slice(300, 301), float("inf")),
+                                  (3, 200, slice(511, 512), float("nan")), (4, 193, slice(10, 12), float("-inf")),
+                                  (0, 192, slice(520, 521), float("nan")), (7, 0, slice(0, 8), float("nan"))):
+        bad = dict(inp, pool=inp["pool"].clone())
+        row = int(inp["block_table"][seq, key // 64]) * 64 + key % 64
+        bad["pool"][row, dims] = value
+        c = Call(lib, bad, layout)
+        c.run()
+        got, _, st = c.result()
+        assert st == 0
+        others = [b for b in range(8) if b != seq]
+        assert np.array_equal(got[others], want[others]), (seq, value)
+        if np.isnan(value):
+            assert np.isnan(got[seq]).all(), seq
+
+
+@pytest.mark.gpu
 def test_shared_two_calls_at_once(lib):
     """Two calls on two streams with workspaces of their own, many times over: the bits of each call alone."""
     calls = [Call(lib, make_shared(V2L, [(640, [700, 650, 900, 641]), (128, [300, 129])], 1, 64, seed=31)),
