@@ -1587,6 +1587,7 @@ int launch_tc_combine(const mla_dims &d, int B, int n_q, const int32_t *seqlens,
   const WsLayout L = ws_layout(B, n_rb);
   char *w = static_cast<char *>(ws);
   if (w_uv && (d.d_v != kDv || (reinterpret_cast<uintptr_t>(w_uv) & 15))) return MLA_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(out) & 15) return MLA_ERR_UNSUPPORTED;   // 16-byte stores
   const int rows = B * n_q;
   const int max_segs = B * n_rb + clusters_for_device();
   if (w_uv) {   // merge and W_UV product in one kernel

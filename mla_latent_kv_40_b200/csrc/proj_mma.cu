@@ -127,7 +127,8 @@ size_t append_mma_workspace(int T, int d_model, int W, int *nsplit, int *k_per_s
 
 bool append_mma_supported(const AppendArgs &a, bool bf16) {
   return bf16 && a.d_model % kBK == 0 && a.d_c % 64 == 0 && a.d_rope <= 64 && a.d_rope % 8 == 0 &&
-         a.d_c + a.d_rope <= 2 * 2 * kFinThreads;
+         a.d_c + a.d_rope <= 2 * 2 * kFinThreads && !(reinterpret_cast<uintptr_t>(a.h) & 15) &&   // 16-byte copies
+         !(reinterpret_cast<uintptr_t>(a.w_dkv) & 15) && !(reinterpret_cast<uintptr_t>(a.w_kr) & 15);
 }
 
 int launch_append_mma(const AppendArgs &a, void *ws, cudaStream_t st) {
@@ -226,7 +227,9 @@ absorb_mma_kernel(AbsorbArgs a) {
 }
 
 bool absorb_mma_supported(const AbsorbArgs &a, bool bf16) {
-  return bf16 && a.d_nope % 16 == 0 && a.d_nope <= 256 && a.d_c % 128 == 0 && a.d_rope <= 64;
+  return bf16 && a.d_nope % 16 == 0 && a.d_nope <= 256 && a.d_c % 128 == 0 && a.d_rope <= 64 && a.d_rope % 2 == 0 &&
+         !(reinterpret_cast<uintptr_t>(a.q_nope) & 15) && !(reinterpret_cast<uintptr_t>(a.w_uk) & 15) &&   // 16-byte copies
+         !(reinterpret_cast<uintptr_t>(a.q_out) & 3);
 }
 
 int launch_absorb_mma(const AbsorbArgs &a, cudaStream_t st) {

@@ -356,6 +356,43 @@ def test_shared_values_that_are_not_finite_stay_with_their_sequence(lib, heads, 
             assert np.isnan(got[seq]).all(), seq
 
 
+def _shifted(t):
+    """The same values behind an address that is no multiple of 4 bytes."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    flat[1:].copy_(t.flatten())
+    return flat[1:].view(t.shape)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d_nope,shift", [(128, True), (40, False), (96, False), (96, True)])
+def test_shared_queries_that_the_tensor_core_absorption_does_not_take(lib, d_nope, shift):
+    """Odd addresses and widths of the queries: the plan is a launch of its own, and another kernel absorbs."""
+    dims = Dims(**{**V2_LITE, "d_nope": d_nope})
+    inp = make_shared(dims, GROUPS["ragged"], 2, 64, seed=d_nope)
+    inp["seqlens"] = torch.clamp(inp["seqlens"], min=2)
+    c = Call(lib, inp)
+    if shift:
+        for k in ("q_nope", "q_pe", "w_uk"):
+            c.dev[k] = _shifted(c.dev[k])
+    c.run()
+    check(inp, c.result(), some(inp, 8, 4))
+
+
+@pytest.mark.gpu
+def test_shared_refuses_odd_addresses_of_outputs_weights_and_pools(lib):
+    inp = make_shared(V2L, [(64, [100, 90])], 1, 64, seed=43)
+    for key, groups in (("out", True), ("w_uv", True), ("c_kv", True), ("out", False), ("w_uv", False), ("c_kv", False)):
+        c = Call(lib, inp, groups=groups)
+        if key == "out":
+            c.out = _shifted(c.out)
+        elif key == "w_uv":
+            c.dev["w_uv"] = _shifted(c.dev["w_uv"])
+        else:
+            c.c_kv = _shifted(c.c_kv)
+        with pytest.raises(RuntimeError):
+            c.run()
+
+
 @pytest.mark.gpu
 def test_shared_two_calls_at_once(lib):
     """Two calls on two streams with workspaces of their own, many times over: the bits of each call alone."""

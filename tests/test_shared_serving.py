@@ -163,3 +163,26 @@ def test_serving_step_as_one_graph(lib):
         torch.cuda.synchronize()
         assert (L.state()[0] == before + k).all()
         L.check_decode(d)
+
+
+def test_append_from_odd_addresses(lib):
+    """Hidden states and weights behind addresses that no 16-byte copy can start at: the same rows but for fp32 sums of 256
+    products in another order (256 * 2^-24 = 2^-16 of the sum of magnitudes, 2^-12 of a row's norm is ample) and so a bf16
+    rounding that may fall the other way (a whole step, 2^-7 of the value at most)."""
+    a, b = Loop(lib), Loop(lib)
+    for k in ("w_dkv", "w_kr"):
+        w = getattr(b, k)
+        flat = torch.empty(w.numel() + 1, dtype=w.dtype, device="cuda")
+        flat[1:].copy_(w.flatten())
+        setattr(b, k, flat[1:].view(w.shape))
+    g = torch.Generator().manual_seed(3)
+    h = torch.randn(5, D.d_model, generator=g).to(torch.bfloat16).cuda()
+    odd = torch.empty(h.numel() + 1, dtype=h.dtype, device="cuda")
+    odd[1:].copy_(h.flatten())
+    for loop, x in ((a, h), (b, odd[1:].view(h.shape))):
+        loop.append(x, loop.i32([0, 0, 1, 1, 1]), loop.i32([0, 70, 3, 64, 191]), loop.prefix_table, 3)
+    torch.cuda.synchronize()
+    assert int(a.status.item()) == int(b.status.item()) == 0
+    want, got = a.pool.float(), b.pool.float()
+    assert ((got - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -12 * want.norm(dim=1, keepdim=True)).all()
+    assert want.abs().sum() > 0
