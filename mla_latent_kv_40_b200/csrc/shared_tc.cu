@@ -10,9 +10,9 @@
 // Shape.  A unit is at most 256 consecutive rows of a group, and a list of pages of 64 keys: the group's shared pages,
 // then the own pages of every sequence with rows in the unit, which the other rows do not see (a mask by owner and
 // length; S of such a page is computed for all rows, as an MMA with fewer rows would take the same time).  Own pages in
-// units of their own were slower by what a unit costs at its start and end: 106 us of attention for 64 sequences of
-// 128 heads behind 4096 shared tokens and up to 512 own ones.  A cluster of four CTAs works on one unit at a time, as two pairs that issue M = 256
-// MMAs (cta_group::2: each CTA holds 128 of the rows and half of the B operand, so each SM pulls half the bytes that
+// units of their own were slower by what a unit costs at its start and end: 106 against 85 us of attention for 64
+// sequences of 128 heads behind 4096 shared tokens and up to 512 own ones.  A cluster of four CTAs works on one unit at
+// a time, as two pairs that issue M = 256 MMAs (cta_group::2: each CTA holds 128 of the rows and half of the B operand, so each SM pulls half the bytes that
 // a 128-row tile of its own would need; at 128 rows the L2 -> SM path, not the tensor pipe, sets the pace):
 //   * ranks 0, 1 (score pair): Q_lat of the CTA's 128 rows in tensor memory (A operand), Q_rope in shared memory; a
 //     tile is 128 keys, and CTA r streams its page r (64 keys, contiguous in the tiled pool) as two half-page stages;
@@ -22,11 +22,15 @@
 //     dims 256 (r - 2) .. of every page (32 KB, contiguous); rank 2 issues O += P . C as two N = 256 MMAs per 16 keys.
 // Per 128 keys the score pair has 36 MMAs of 64 cycles, the value pair 16 of 128: 2304 and 2048 cycles.
 //
+// Measured: 128 sequences of 128 heads behind 32768 shared tokens (16384 rows, 1.19e12 FLOPs): 766-780 us, 1530-1550
+// TFLOP/s of the burst matrix product's 1675; 2470 cycles a tile of the 2304, on 132 of 148 SMs (33 clusters fit).
+//
 // The issuing warps run whole, and each MMA is issued by the elected lane: with warp-uniform descriptors the issue
-// keeps up with the pipe from one warp.  Reference maximum, row sums, rounding of P and of the partials as in the
-// per-sequence kernel (decode_tc.cu): lazy maximum in log2 units, sums of P in fp32 before its rounding; but O / l of a
-// piece stays in fp32 (in bf16 it cost the merged result a rounding, 0.0034 instead of 0.0030 of its norm).  The (unit, tile) list is cut into equal runs, one per cluster; a unit cut between clusters
-// leaves one partial per piece, merged with the sequences' own partials by the combine.
+// keeps up with the pipe from one warp.  Reference maximum, row sums and rounding of P as in the per-sequence kernel
+// (decode_tc.cu): lazy maximum in log2 units, sums of P in fp32 before its rounding to bf16, the type of the latents that
+// it is multiplied with; but O / l of a piece stays in fp32 (in bf16 it cost the merged result a rounding, 0.0034 instead
+// of 0.0030 of its norm).  The (unit, tile) list is cut into equal runs, one per cluster; a unit cut between clusters
+// leaves one partial per piece, merged by the combine.
 // Every wait is bounded; on expiry the kernel reports MLA_ERR_TIMEOUT, drains its copies, frees its tensor memory
 // and returns.
 #include <cuda.h>
@@ -1011,11 +1015,10 @@ int shared_clusters_for_device() {
 
 int launch_shared_plan(const SharedPlanArgs &a, cudaStream_t st) {
   const size_t bytes = shared_plan_words(a.B, a.max_units, a.num_groups) * sizeof(int);
-  const bool in_smem = bytes <= 160 * 1024;
+  const bool in_smem = bytes <= 160 * 1024;   // (some 5000 sequences in as many groups; behind that in the workspace)
   static std::atomic<int> cache[kSmemCacheDevs];
   if (in_smem && smem_limit(shared_plan_kernel, bytes, cache) != cudaSuccess) return MLA_ERR_CUDA;
-  const int threads = a.B <= 256 ? 256 : 1024;
-  return launch_pdl(shared_plan_kernel, dim3(1), dim3(threads), in_smem ? bytes : 0, st, a, (int)in_smem) == cudaSuccess
+  return launch_pdl(shared_plan_kernel, dim3(1), dim3(1024), in_smem ? bytes : 0, st, a, (int)in_smem) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }

@@ -17,7 +17,8 @@
 //   * much work: kBodyCtas CTAs that leave those outputs alone, and a second launch of one CTA that forms the sums again
 //     (while the first kernel runs) and writes them once that has finished.
 // No atomics: the result does not depend on timing.  The call is bound by latency (the dependent loads of the scan and
-// of the search), not by its bytes.
+// of the search), not by its bytes.  Measured (device): plan of 64 requests with one token each 10.7 us, of 256 with 16 to
+// 1024 tokens 12.1, of 4096 with 4 to 32 tokens 19.3 (two launches); release of 64 requests 6.0 us, of 4096 11.7.
 #include "kernels.cuh"
 #include "sm100.cuh"
 
@@ -28,7 +29,9 @@ using namespace sm100;
 
 constexpr int kCtas = 8;          // the largest portable cluster
 constexpr int kBodyCtas = 128;
-// Up to so many words that a call may have to write, one cluster takes it.
+// Up to so many words that a call may have to write, one cluster takes it (device time, one cluster against two launches:
+// plan of 256 requests with 33k tokens 10.6 and 11.6 us, 63k 13.8 and 10.8, 131k 20.7 and 10.9; release of 33k blocks 5.9
+// and 8.8, 64k 7.4 and 8.6, 131k 11.0 and 9.0; the second launch takes 3 us of the host's time).
 constexpr int64_t kWholeWords = 65536;
 // What one launch is to do.
 enum Mode { kWhole, kBody, kFinish };
