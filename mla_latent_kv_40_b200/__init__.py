@@ -423,8 +423,14 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+# torch.cuda.current_stream() builds a Stream object (3.2 us, of 14 to 20 for the small calls); this returns its handle.
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    return _current_handle(dev) if _current_handle else torch.cuda.current_stream().cuda_stream
 
 
 def mla_decode_shared(dims, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,
@@ -453,7 +459,7 @@ def mla_decode_shared(dims, q_nope, q_pe, c_kv, k_pe, block_table, max_blocks_pe
                                 _addr(k_pe), block_table.data_ptr(), max_blocks_per_seq, num_blocks, seqlens.data_ptr(),
                                 max_seqlen, G, _addr(group_offsets), _addr(prefix_lens), w_uk.data_ptr(), _addr(w_uv),
                                 out.data_ptr(), _addr(lse), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _addr(dev_status), _raw_stream(stream))
+                                workspace.numel() * workspace.element_size(), _addr(dev_status), _raw_stream(stream, dev))
     if rc:
         _check("mla_decode_shared", rc)
 
@@ -484,7 +490,7 @@ def mla_plan_step(dims, cached_lens, new_lens, group_offsets, prefix_lens, prefi
                             _addr(prefix_lens), _addr(prefix_table) if G else None, mpb, free_list.data_ptr(),
                             free_list.numel(), free_count.data_ptr(), block_table.data_ptr(), mb, num_blocks, T,
                             seqlens.data_ptr(), cu_seqlens.data_ptr(), seq_idx.data_ptr(), pos.data_ptr(), _addr(slots),
-                            free_count_out.data_ptr(), _addr(dev_status), _raw_stream(stream))
+                            free_count_out.data_ptr(), _addr(dev_status), _raw_stream(stream, dev))
     if rc:
         _check("mla_plan_step", rc)
 
@@ -508,7 +514,7 @@ def mla_release_blocks(dims, done, seqlens, group_offsets, prefix_lens, block_ta
     rc = _lib.mla_release_blocks(ctypes.byref(dims), B, done.data_ptr(), seqlens.data_ptr(), G, _addr(group_offsets),
                                  _addr(prefix_lens), block_table.data_ptr(), mb, num_blocks, free_list.data_ptr(),
                                  free_list.numel(), free_count.data_ptr(), seqlens_out.data_ptr(),
-                                 free_count_out.data_ptr(), _addr(dev_status), _raw_stream(stream))
+                                 free_count_out.data_ptr(), _addr(dev_status), _raw_stream(stream, dev))
     if rc:
         _check("mla_release_blocks", rc)
 
