@@ -8,7 +8,9 @@
 // every unit after the first kUnitCost more (its queries go to tensor memory and the finished unit's O is written out
 // while the MMAs wait; about 10 us against 1.4 us per tile).  Tile i of unit u has place cost0[u] + i in a list of length
 // W, cost0[u] = tiles before u + kUnitCost (non-empty units before u), and cluster c's share is
-// [floor(c W / C), floor((c + 1) W / C)).  Filling the clusters greedily to the least load that 33 of them manage (32 loads
+// [floor(c W / C), floor((c + 1) W / C)).  Where there are no more units than clusters and the longest is no longer than such
+// a share, every unit has a cluster to itself: no unit is cut
+// (64 sequences of 128 heads, 32 units: 97.6 us a call instead of 104.1, most of it in the merge).  Filling the clusters greedily to the least load that 33 of them manage (32 loads
 // tried at once) saved 2 us of 84 at 32 units, and took 9 us: not worth it.
 #pragma once
 
@@ -128,6 +130,7 @@ __device__ __forceinline__ void shared_plan_body(const SharedPlanArgs &a, int *w
   __syncthreads();
   // Tiles of every unit and its place; non-empty units are counted in the low word.
   int64_t list = 0;
+  int longest = 0;
   for (int u0 = 0; u0 < U; u0 += threads) {
     const int u = u0 + tid;
     int tiles = 0;
@@ -140,8 +143,18 @@ __device__ __forceinline__ void shared_plan_body(const SharedPlanArgs &a, int *w
       cost0[u] = (int)(exc >> 32) + kUnitCost * (int)(exc & 0xffffffff);
       tiles_of[u] = tiles;
     }
+    longest = max(longest, tiles);
   }
   const int W = (int)(list >> 32) + kUnitCost * max((int)(list & 0xffffffff) - 1, 0), C = min(W, a.clusters);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  __syncthreads();
+  if (lane == 0) part[warp] = longest;
+  __syncthreads();
+  longest = lane < threads / 32 ? (int)part[lane] : 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  const bool whole = (int)(list & 0xffffffff) <= a.clusters && (int64_t)longest * C <= W;
   __syncthreads();
   if (in_smem) sm100::grid_dep_wait();   // earlier calls may still read the plan that is overwritten from here on
   if ((bad && tid == 0) || wrong) report(a.dev_status, MLA_ERR_BAD_INDEX);
@@ -153,26 +166,44 @@ __device__ __forceinline__ void shared_plan_body(const SharedPlanArgs &a, int *w
     dst[1] = make_int4(row0, min(unit_rows, first_of(g + 1) * R - row0), seq0, members);
     dst[2] = make_int4(lo, 0, 0, 0);
   };
-  for (int c = tid; c < a.clusters; c += threads) {
-    int4 *sh = reinterpret_cast<int4 *>(pl.shares + c);
-    if (c >= C) {
-      sh[0] = make_int4(0, 0, 0, 0);
-      continue;
+  if (whole) {
+    int64_t n = 0;
+    for (int u0 = 0; u0 < U; u0 += threads) {
+      const int u = u0 + tid;
+      const int tiles = u < U ? tiles_of[u] : 0;
+      const int c = (int)plan_scan(tiles > 0, part, n);
+      if (u >= U) continue;
+      put(reinterpret_cast<int4 *>(pl.units + u), u);
+      pl.unit_parts[u] = tiles > 0 ? make_int2(u + c, 1) : make_int2(0, 0);
+      if (tiles > 0) {
+        int4 *sh = reinterpret_cast<int4 *>(pl.shares + c);
+        sh[0] = make_int4(cost0[u], cost0[u] + tiles, u, U);
+        put(sh + 1, u);
+      }
     }
-    const int at = (int)((int64_t)c * W / C);
-    int u = last_at(cost0, U, at);
-    while (u + 1 < U && at - cost0[u] >= tiles_of[u]) ++u;   // in the gap behind u (or u is empty): the next with tiles
-    sh[0] = make_int4(at, (int)((int64_t)(c + 1) * W / C), u, U);
-    put(sh + 1, u);
-  }
-  for (int u = tid; u < U; u += threads) {
-    put(reinterpret_cast<int4 *>(pl.units + u), u);
-    int2 parts = make_int2(0, 0);
-    if (tiles_of[u] > 0) {
-      const int c0 = cluster_of(cost0[u], W, C), c1 = cluster_of((int64_t)cost0[u] + tiles_of[u] - 1, W, C);
-      parts = make_int2(u + c0, c1 - c0 + 1);
+    for (int c = (int)n + tid; c < a.clusters; c += threads) *reinterpret_cast<int4 *>(pl.shares + c) = make_int4(0, 0, 0, 0);
+  } else {
+    for (int c = tid; c < a.clusters; c += threads) {
+      int4 *sh = reinterpret_cast<int4 *>(pl.shares + c);
+      if (c >= C) {
+        sh[0] = make_int4(0, 0, 0, 0);
+        continue;
+      }
+      const int at = (int)((int64_t)c * W / C);
+      int u = last_at(cost0, U, at);
+      while (u + 1 < U && at - cost0[u] >= tiles_of[u]) ++u;   // in the gap behind u (or u is empty): the next with tiles
+      sh[0] = make_int4(at, (int)((int64_t)(c + 1) * W / C), u, U);
+      put(sh + 1, u);
     }
-    pl.unit_parts[u] = parts;
+    for (int u = tid; u < U; u += threads) {
+      put(reinterpret_cast<int4 *>(pl.units + u), u);
+      int2 parts = make_int2(0, 0);
+      if (tiles_of[u] > 0) {
+        const int c0 = cluster_of(cost0[u], W, C), c1 = cluster_of((int64_t)cost0[u] + tiles_of[u] - 1, W, C);
+        parts = make_int2(u + c0, c1 - c0 + 1);
+      }
+      pl.unit_parts[u] = parts;
+    }
   }
   for (int b = tid; b <= B; b += threads) pl.own_pages[b] = own[b];
   for (int g = warp; g < G; g += threads / 32) {
