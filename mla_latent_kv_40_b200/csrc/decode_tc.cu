@@ -1268,7 +1268,7 @@ tc_combine_kernel(const __grid_constant__ CUtensorMap map_w, const Pieces pc, in
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
       for (int hh = 0; hh < kNb / kAtOnce; ++hh) {
-        // this round: column blocks cb = kTpr (kAtOnce hh + i) + q, i < kAtOnce (8 bf16 each)
+        // this pass: column blocks cb = kTpr (kAtOnce hh + i) + q, i < kAtOnce (8 bf16 each)
         float acc[kAtOnce][8];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i)

@@ -296,6 +296,27 @@ def test_shared_long_runs_of_pages(lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,longer", [(64, 0), (66, 0), (66, 2000), (68, 0), (7, 0)])
+def test_shared_units_that_have_a_cluster_each_or_are_cut(lib, n, longer):
+    """As many units as clusters and fewer, alike in length (none is cut) and not (they are); one unit more; a group of one
+    sequence whose length is refused leaves a unit with nothing to do."""
+    groups = [(1024, [1025 + i % 3 for i in range(n - 1)]), (0, [64 + longer])]
+    inp = make_shared(V3D, groups, 1, 64, seed=n)
+    c = Call(lib, inp)
+    c.run()
+    check(inp, c.result(), some(inp, 4, 2))
+    picks = [x for x in some(inp, 4, 2) if x[0] < n - 1]
+    ref, _ = reference(inp, picks)
+    c.dev["seqlens"][n - 1] = 0
+    c.run()
+    out, _, st = c.result()
+    assert st == -6
+    idx = tuple(np.array(picks).T)
+    check_close(out[idx], ref[idx], "bf16", "beside a refused length")
+    assert not out[n - 1].any()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("seed", range(8))
 def test_shared_random_batches(lib, seed):
     r = np.random.default_rng(100 + seed)
