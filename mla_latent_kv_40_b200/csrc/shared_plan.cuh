@@ -66,8 +66,10 @@ __device__ __forceinline__ void shared_plan_body(const SharedPlanArgs &a, int *w
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int B = a.B, R = a.R, unit_rows = shared_unit_rows(R);
   const SharedPlan &pl = a.out;
-  const bool in_smem = words != nullptr;
-  if (!in_smem) words = pl.scratch;
+  // The lengths and groups may be what the kernel before wrote (mla_plan_step, mla_release_blocks, the user's own), and
+  // earlier calls may still read the plan, or use the scratch words, that are overwritten here.
+  sm100::grid_dep_wait();
+  if (!words) words = pl.scratch;
   int *const own = words;                        // [B + 1] own pages before each sequence
   int *const seq_shared = own + B + 1;           // [B] shared pages
   int *const cost0 = seq_shared + B;             // [max_units + 1]
@@ -83,7 +85,6 @@ __device__ __forceinline__ void shared_plan_body(const SharedPlanArgs &a, int *w
   bad = __syncthreads_or(bad);
   if (bad) G = 1;    // then one group that shares nothing
   auto first_of = [&](int g) { return bad ? g * B : a.offsets[g]; };
-  if (!in_smem) sm100::grid_dep_wait();   // an earlier call may still use the scratch words
   // Units before each group.
   int64_t units = 0;
   for (int g0 = 0; g0 < G; g0 += threads) {
@@ -156,7 +157,6 @@ __device__ __forceinline__ void shared_plan_body(const SharedPlanArgs &a, int *w
   for (int o = 16; o; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
   const bool whole = (int)(list & 0xffffffff) <= a.clusters && (int64_t)longest * C <= W;
   __syncthreads();
-  if (in_smem) sm100::grid_dep_wait();   // earlier calls may still read the plan that is overwritten from here on
   if ((bad && tid == 0) || wrong) report(a.dev_status, MLA_ERR_BAD_INDEX);
   auto put = [&](int4 *dst, int u) {
     const int g = last_at(group_units, G, u);   // of groups without units, which begin where the next one does, the last
