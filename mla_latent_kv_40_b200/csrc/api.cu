@@ -83,16 +83,17 @@ int check_ws(const DecodeLayout &L, const void *workspace, size_t ws_bytes) {
 
 constexpr int kAllKeys = 0x7fffffff;   // kv_end of a decode over every cached key
 
+// lens_settled: see launch_tc_attention.
 int attention_impl(const mla_dims *dims, int B, int n_q, const void *q_abs, const void *c_kv, const void *k_pe,
                    const int32_t *block_table, int max_blocks_per_seq, int num_blocks, const int32_t *seqlens,
-                   int max_seqlen, const DecodeLayout &L, char *ws, int *dev_status, cudaStream_t st,
+                   bool lens_settled, int max_seqlen, const DecodeLayout &L, char *ws, int *dev_status, cudaStream_t st,
                    int kv_begin = 0, int kv_end = kAllKeys) {
   const bool bf16 = dims->dtype == MLA_BF16;
   CacheView cv{c_kv, k_pe, dims->ckv_stride, dims->kpe_stride, block_table, max_blocks_per_seq,
                num_blocks, dims->block_size, dims->cache_layout, dims->d_c, dims->d_c + dims->d_rope};
   if (L.use_tc)
-    return launch_tc_attention(*dims, B, n_q, q_abs, cv, seqlens, max_seqlen, ws + L.tc_off, dev_status, st,
-                               kv_begin, kv_end);
+    return launch_tc_attention(*dims, B, n_q, q_abs, cv, seqlens, lens_settled, max_seqlen, ws + L.tc_off, dev_status,
+                               st, kv_begin, kv_end);
   AttnArgs at{B, n_q, dims->n_heads, dims->d_c, dims->d_rope, q_abs, cv, seqlens, default_scale(*dims),
               kSimtChunk, L.max_chunks, reinterpret_cast<float *>(ws + L.o_off),
               reinterpret_cast<float *>(ws + L.lse_off), dev_status, kv_begin, kv_end};
@@ -133,7 +134,7 @@ int decode_impl(const mla_dims *dims, int B, int n_q, const void *q_nope, const 
                 q_nope, q_pe, w_uk, seqlens, qbuf, dims->rope_base};
   if ((rc = absorb_dispatch(ab, dims->dtype == MLA_BF16, dev_status, st))) return rc;
   if ((rc = attention_impl(dims, B, n_q, qbuf, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,
-                           max_seqlen, L, ws, dev_status, st, kv_begin, kv_end)))
+                           true, max_seqlen, L, ws, dev_status, st, kv_begin, kv_end)))
     return rc;
   return combine_impl(dims, B, n_q, seqlens, max_seqlen, w_uv, out, lse, L, ws, dev_status, st);
 }
@@ -343,7 +344,7 @@ int mla_decode_absorbed(const mla_dims *dims, int d_cq, int B, int n_q, const vo
   }
   // (4) split-KV attention and the merge of its partials into o_lat.
   if ((rc = attention_impl(dims, B, n_q, q_abs, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,
-                           max_seqlen, L.dec, ws, dev_status, st)))
+                           true, max_seqlen, L.dec, ws, dev_status, st)))
     return rc;
   if ((rc = combine_impl(dims, B, n_q, seqlens, max_seqlen, nullptr, o_lat, lse, L.dec, ws, dev_status, st))) return rc;
   // (5) u = sum_s o_lat^(s) W_UVO^(s).
@@ -394,7 +395,7 @@ int mla_decode_sparse(const mla_dims *dims, int B, int n_q, const void *q_nope, 
   const mla_dims *in = &L.inner;
   const int W = dims->d_c + dims->d_rope;
   if ((rc = attention_impl(in, L.units, 1, qbuf, pool, pool + (size_t)dims->d_c * elem(dims), nullptr, L.pages,
-                           L.units * L.pages, counts, L.pages * 64, L.dec, dws, dev_status, st)))
+                           L.units * L.pages, counts, false, L.pages * 64, L.dec, dws, dev_status, st)))
     return rc;
   (void)W;
   return combine_impl(in, L.units, 1, counts, L.pages * 64, w_uv, out, lse, L.dec, dws, dev_status, st);
@@ -615,7 +616,7 @@ int mla_decode_step(const mla_dims *dims, int B, int n_q, const void *h_new, con
     if ((rc = absorb_dispatch(ab, bf16, dev_status, st))) return rc;
   }
   if ((rc = attention_impl(dims, B, n_q, qbuf, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,
-                           max_seqlen, L.dec, dws, dev_status, st)))
+                           true, max_seqlen, L.dec, dws, dev_status, st)))
     return rc;
   return combine_impl(dims, B, n_q, seqlens, max_seqlen, w_uv, out, lse, L.dec, dws, dev_status, st);
 }
@@ -668,7 +669,7 @@ int mla_decode_attention(const mla_dims *dims, int B, int n_q, const void *q_abs
   const DecodeLayout L = decode_layout(dims, B, n_q, max_seqlen);
   if ((rc = check_ws(L, workspace, ws_bytes))) return rc;
   return attention_impl(dims, B, n_q, q_abs, c_kv, k_pe, block_table, max_blocks_per_seq, num_blocks, seqlens,
-                        max_seqlen, L, static_cast<char *>(workspace), dev_status,
+                        false, max_seqlen, L, static_cast<char *>(workspace), dev_status,
                         reinterpret_cast<cudaStream_t>(stream));
 }
 

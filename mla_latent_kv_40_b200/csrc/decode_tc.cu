@@ -163,6 +163,7 @@ struct TcParams {
   const unsigned char *tiled;        // tiled page pool (pages move by bulk copy), or NULL: row pool via TMA maps
   const unsigned char *row_pool;     // row pool base (c_kv) for L2 prefetch
   int rows_contig;                   // row pool with fused 576-wide rows: a page is 73728 contiguous bytes
+  int lens_settled;                  // the lengths are older than the kernel ahead, which starts no dependent before its own wait
 };
 
 __device__ __forceinline__ int seq_len_clamped(const TcParams &p, int b) {
@@ -437,8 +438,10 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
   const uint32_t peer = rank ^ 1u;
 
   // The next kernel on the stream may start its prologue now.  Roles that read what an earlier
-  // kernel of this library writes (queries, pool pages) or that write global memory call
-  // grid_dep_wait() first; the prologue below touches inputs only.
+  // kernel writes (queries, pool pages) or that write global memory call grid_dep_wait() first.
+  // The plan reads the lengths: behind an absorption of this library, which starts this kernel only
+  // once everything ahead of itself is complete, at once; else behind the wait too (always waiting
+  // took 3 us of a decode at V3 batch 64 and 2 of 28 at two sequences).
   grid_dep_launch();
   if (threadIdx.x < 8) sb.prog[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
@@ -463,6 +466,7 @@ mla_decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
     tmem_alloc(smem_u32(&sb.tmem_base), 512);
     tmem_relinquish();
   }
+  if (!p.lens_settled) grid_dep_wait();
   if (warp == 0) make_plan(p, sb, cid, C);
   if (threadIdx.x == 32 && !p.tiled) {
     tma_prefetch_desc(&map_c);
@@ -1482,8 +1486,8 @@ size_t tc_decode_workspace_bytes(const mla_dims &d, int B, int n_q) {
 }
 
 int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
-                        const int32_t *seqlens, int max_seqlen, void *ws, int *dev_status, cudaStream_t st,
-                        int kv_begin, int kv_end) {
+                        const int32_t *seqlens, bool lens_settled, int max_seqlen, void *ws, int *dev_status,
+                        cudaStream_t st, int kv_begin, int kv_end) {
   if (kv_begin < 0 || kv_begin % kTileKeys) return MLA_ERR_INVALID_ARG;
   const bool tiled = cache.layout == MLA_CACHE_TILED;
   if ((reinterpret_cast<uintptr_t>(cache.c_kv) & 15) || (!tiled && (reinterpret_cast<uintptr_t>(cache.k_pe) & 15)) ||
@@ -1512,6 +1516,7 @@ int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, co
   p.max_seqlen = max_seqlen;
   p.q = static_cast<const __nv_bfloat16 *>(q_abs);
   p.seqlens = seqlens;
+  p.lens_settled = lens_settled;
   p.block_table = cache.block_table;
   p.max_blocks_per_seq = cache.max_blocks_per_seq;
   p.num_blocks = cache.num_blocks;

@@ -13,9 +13,11 @@ int tc_decode_kernel_launches();
 size_t tc_decode_workspace_bytes(const mla_dims &d, int B, int n_q);
 // Split-KV attention from an absorbed query buffer; partials stay in ws.  Only keys in
 // [kv_begin, kv_end) are read (kv_begin a multiple of 64); the full decode passes 0, INT_MAX.
+// lens_settled: the kernel ahead on the stream neither writes the lengths nor lets this one start
+// before all that is ahead of itself is complete.
 int launch_tc_attention(const mla_dims &d, int B, int n_q, const void *q_abs, const CacheView &cache,
-                        const int32_t *seqlens, int max_seqlen, void *ws, int *dev_status, cudaStream_t st,
-                        int kv_begin, int kv_end);
+                        const int32_t *seqlens, bool lens_settled, int max_seqlen, void *ws, int *dev_status,
+                        cudaStream_t st, int kv_begin, int kv_end);
 // Merge of the partials, and the W_UV product in the same kernel when w_uv != NULL.
 int launch_tc_combine(const mla_dims &d, int B, int n_q, const int32_t *seqlens, int max_seqlen, const void *w_uv,
                       void *out, float *lse, void *ws, int *dev_status, cudaStream_t st);

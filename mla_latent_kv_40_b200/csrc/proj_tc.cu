@@ -60,7 +60,6 @@ __device__ __forceinline__ void absorb_tc_body(const CUtensorMap &map_w, const C
   const int m0 = by * 128, r0 = bz * kTcN;
   const int R = a.B * a.n_q, W = a.d_c + a.d_rope;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  grid_dep_launch();   // reads below touch inputs only; q_out is written after grid_dep_wait()
 
   if (tid == 0) {
     mbar_init(smem_u32(&bar_full), 1);
@@ -96,7 +95,9 @@ __device__ __forceinline__ void absorb_tc_body(const CUtensorMap &map_w, const C
     const int half = a.d_rope / 2;
     if (tid - 32 < half) theta[tid - 32] = rope_theta(tid - 32, a.d_rope, a.rope_base);
     asm volatile("bar.sync 1, 96;" ::: "memory");       // warps 1-3 only
-    grid_dep_wait();                                       // q_out may still be read by an earlier kernel
+    grid_dep_wait();                                       // the lengths may be new; q_out may still be read by an earlier kernel
+    // Only now may the attention start: it reads the lengths at once, and whatever wrote them is complete here.
+    if (warp == 1) grid_dep_launch();
     constexpr int kRowsPerWarp = 6;                        // 16 rows a CTA (d_c = 512) as 6, 6 and 4 of the three warps
     const int nr = (kTcN - by + ny - 1) / ny;
     for (int w0 = (warp - 1) * kRowsPerWarp; w0 < nr; w0 += 3 * kRowsPerWarp) {

@@ -12,8 +12,9 @@ import numpy as np
 import pytest
 import torch
 
-from workloads import Dims, V2_LITE
+from helpers import device_pool, dims_of
 from test_shared_parity import Call, make_shared
+from workloads import DecodeCase, Dims, V2_LITE, make_decode_step_inputs
 
 PRODUCER = r"""
 #include <cuda_runtime.h>
@@ -78,3 +79,94 @@ def test_shared_decode_behind_a_producer_of_lengths_and_groups(lib, produce, hea
     before = dict(seqlens=torch.full_like(c.dev["seqlens"], 70), prefix_lens=torch.zeros_like(c.dev["prefix_lens"]),
                   group_offsets=torch.tensor([0, 1, 6], dtype=torch.int32, device="cuda"))
     late(produce, sorted(before), c.run, c.result, c.dev, before)
+
+
+class Step:
+    """One decode step's inputs on the device, and a call of each entry point that takes lengths or positions."""
+
+    def __init__(self, mla, n_q):
+        d = Dims(**{**V2_LITE, "d_model": 256})
+        case = DecodeCase("late", d, 7, n_q, ("list", (63, 64, 165, 511, 1500, 700, 901)), 64, True, 77)
+        self.inp = inp = make_decode_step_inputs(case)
+        self.mla, self.d, self.n_q, self.B, self.H = mla, d, n_q, 7, d.n_heads
+        self.dims = dims_of(mla, d, 64, 1)
+        self.dev = {k: inp[k].cuda() for k in ("q_nope", "q_pe", "block_table", "seqlens", "w_uk", "w_uv", "h_new", "w_dkv", "w_kr",
+                                               "gamma", "seq_idx", "pos")}
+        # The pool's unused rows hold NaN; any finite rows will do here.
+        self.pool0, _, _ = device_pool(mla, d, 64, torch.nan_to_num(inp["pool"].float()).to(torch.bfloat16), 1)
+        self.pool = self.pool0.clone()
+        self.S, B, H = int(inp["seqlens"].max()), 7, d.n_heads
+        bf = lambda *shape: torch.empty(*shape, dtype=torch.bfloat16, device="cuda")   # noqa: E731
+        self.out, self.o_lat, self.q_abs = bf(B, n_q, H, 128), bf(B, n_q, H, 512), bf(B, n_q, H, 576)
+        self.lse = torch.empty(B, n_q, H, device="cuda")
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.dev["topk"] = torch.tensor(np.random.default_rng(1).integers(0, 60, (B, n_q, 100)), dtype=torch.int32).cuda()
+        size = max(mla.mla_decode_step_workspace_size(self.dims, B, n_q, self.S),
+                   mla.mla_decode_sparse_workspace_size(self.dims, B, n_q, 100))
+        self.ws = mla.alloc_workspace(size)
+        self.append_ws = mla.alloc_workspace(mla.mla_append_workspace_size(self.dims, B * n_q))
+
+    def call(self, entry):
+        m, v, i = self.mla, self.dev, self.inp
+        pool = (self.pool, self.pool, v["block_table"], i["max_blocks_per_seq"], i["num_blocks"])
+        q, cache = (v["q_nope"], v["q_pe"]), (*pool, v["seqlens"], self.S)
+        if entry == "decode":
+            m.mla_decode(self.dims, *q, *cache, v["w_uk"], v["w_uv"], self.out, self.lse, self.ws, self.status)
+        elif entry == "latent":
+            m.mla_decode_latent(self.dims, *q, *cache, v["w_uk"], self.o_lat, self.lse, self.ws, self.status)
+        elif entry == "partial":
+            m.mla_decode_partial(self.dims, *q, *cache, 64, 640, v["w_uk"], self.o_lat, self.lse, self.ws, self.status)
+        elif entry == "attention":
+            m.mla_decode_attention(self.dims, self.q_abs, *cache, self.ws, self.status)
+            m.mla_decode_combine(self.dims, self.B, self.n_q, v["seqlens"], self.S, v["w_uv"], self.out, self.lse, self.ws)
+        elif entry == "sparse":
+            m.mla_decode_sparse(self.dims, *q, *cache, v["topk"], v["w_uk"], v["w_uv"], self.out, self.lse, self.ws, self.status)
+        elif entry == "step":
+            m.mla_decode_step(self.dims, v["h_new"].view(self.B, self.n_q, -1), v["w_dkv"], v["w_kr"], v["gamma"], *q, *cache,
+                              v["w_uk"], v["w_uv"], self.out, self.lse, self.ws, self.status)
+        elif entry == "append":
+            m.mla_append_latent(self.dims, v["h_new"], v["w_dkv"], v["w_kr"], v["gamma"], v["seq_idx"], v["pos"], self.pool, self.pool,
+                                v["block_table"], self.B, i["max_blocks_per_seq"], i["num_blocks"], self.status,
+                                workspace=self.append_ws)
+        else:
+            m.mla_absorb_q(self.dims, *q, v["w_uk"], v["seqlens"], self.q_abs)
+
+    def reset(self):
+        self.pool.copy_(self.pool0)
+        for t in (self.out, self.o_lat, self.lse, self.q_abs):
+            t.zero_()
+        if self.entry == "attention":   # (its queries are an input)
+            self.q_abs.copy_(self.keep_q)
+
+    def check(self, entry, produce, before):
+        self.entry = entry
+        self.call("absorb")
+        self.keep_q = self.q_abs.clone()
+
+        def run():
+            self.call(entry)
+
+        def result():
+            torch.cuda.synchronize()
+            assert int(self.status.item()) == 0
+            got = [t.view(torch.int16).cpu().numpy() for t in (self.out, self.o_lat, self.q_abs, self.pool)]
+            got.append(self.lse.view(torch.int32).cpu().numpy())
+            self.reset()
+            return got
+
+        self.reset()
+        late(produce, sorted(before), run, result, self.dev, before)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n_q", [1, 3])
+@pytest.mark.parametrize("entry", ["decode", "latent", "partial", "attention", "sparse", "step", "append", "absorb"])
+def test_entry_points_behind_a_producer_of_lengths_tables_and_positions(lib, produce, entry, n_q):
+    s = Step(lib, n_q)
+    if entry == "append":
+        before = dict(seq_idx=torch.zeros_like(s.dev["seq_idx"]), pos=torch.zeros_like(s.dev["pos"]))
+    else:
+        before = dict(seqlens=torch.full_like(s.dev["seqlens"], 40))
+        if entry != "absorb":
+            before["block_table"] = torch.zeros_like(s.dev["block_table"])
+    s.check(entry, produce, before)
