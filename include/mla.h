@@ -25,6 +25,12 @@
  *    bounded wait that timed out) are written to *dev_status (if non-NULL) with
  *    an atomic compare-and-swap from 0, so the first error wins; the caller
  *    zeroes it beforehand and reads it after synchronising.
+ *  - A call's kernels may start while the work ahead on the stream still runs,
+ *    and then read its weights (w_dkv, w_kr, w_uk, w_uv).  They read everything
+ *    else (lengths, tables, positions, queries, hidden states, the cache) when
+ *    all of that work is complete, also where its last kernel lets dependents
+ *    start early (programmatic dependent launch).  Weights that a kernel of that
+ *    kind has just written are not read safely.
  *  - Concurrent calls on different streams with disjoint outputs and
  *    workspaces are safe, with one exception: mla_decode_noalloc, whose calls
  *    share one library-owned scratch buffer per GPU (see there).  Besides that

@@ -155,9 +155,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
 // ---------------------------------------------------------------- programmatic dependent launch
 // A kernel launched with programmatic stream serialisation may start before the previous kernel
 // on its stream has finished.  grid_dep_wait() blocks until every prerequisite grid has completed
-// and its memory is visible; each kernel calls it before it reads anything an earlier kernel of
-// this library writes and before its first global write.  grid_dep_launch() lets the next kernel
-// start its own prologue.  Both are no-ops for a kernel launched without the attribute.
+// and its memory is visible; each kernel calls it before it reads anything but weights and before
+// its first global write.  (The attention of a decode reads the lengths for its plan earlier, where
+// the kernel ahead called grid_dep_launch() behind its own grid_dep_wait() and does not write them.)
+// grid_dep_launch() lets the next kernel start its own prologue.  Both are no-ops for a kernel
+// launched without the attribute.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -66,7 +66,7 @@ def late(produce, keys, run, result, dev, before):
             produce(final, dev[k])
             run()
             got = result()
-            assert torch.equal(dev[k], final)
+            assert torch.equal(dev[k].view(torch.uint8), final.view(torch.uint8))
             for a, b in zip(got, want):
                 assert np.array_equal(a, b), k
 
@@ -170,3 +170,52 @@ def test_entry_points_behind_a_producer_of_lengths_tables_and_positions(lib, pro
         if entry != "absorb":
             before["block_table"] = torch.zeros_like(s.dev["block_table"])
     s.check(entry, produce, before)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n_q", [1, 3])
+@pytest.mark.parametrize("entry", ["decode", "partial", "sparse", "step", "append", "absorb"])
+def test_entry_points_behind_a_producer_of_queries_and_hidden_states(lib, produce, entry, n_q):
+    s = Step(lib, n_q)
+    names = {"append": ["h_new"], "step": ["h_new", "q_nope", "q_pe"]}.get(entry, ["q_nope", "q_pe"])
+    s.check(entry, produce, {k: torch.flip(s.dev[k], [-1]) for k in names})
+
+
+@pytest.mark.gpu
+def test_shared_decode_behind_a_producer_of_queries_tables_and_keys(lib, produce):
+    inp = make_shared(Dims(**V2_LITE), [(640, [700, 650, 900, 641]), (128, [300, 129])], 1, 64, seed=52)
+    c = Call(lib, inp)
+    c.dev["pool"] = c.c_kv
+    before = {k: torch.flip(c.dev[k], [-1]) for k in ("q_nope", "q_pe")}
+    before.update(block_table=torch.zeros_like(c.dev["block_table"]), pool=torch.zeros_like(c.c_kv))
+    late(produce, sorted(before), c.run, c.result, c.dev, before)
+
+
+@pytest.mark.gpu
+def test_a_decode_that_takes_what_the_call_ahead_wrote(lib):
+    """The output of one call as the hidden states of the append behind it, and these rows decoded by the next: the bits of
+    the same calls with the device at rest between them."""
+    s = Step(lib, 1)
+    dims = s.dims
+    dims.d_model = 16 * 128   # a token's heads side by side
+    g = torch.Generator(device="cuda").manual_seed(5)
+    s.dev["w_dkv"] = (torch.randn(2048, 512, generator=g, device="cuda") * 0.02).to(torch.bfloat16)
+    s.dev["w_kr"] = (torch.randn(2048, 64, generator=g, device="cuda") * 0.02).to(torch.bfloat16)
+    s.dev["h_new"] = s.out.view(s.B, 2048)
+    s.append_ws = lib.alloc_workspace(lib.mla_append_workspace_size(dims, s.B))
+    s.entry = "decode"
+
+    def chain(pause):
+        s.reset()
+        for entry in ("decode", "append", "decode", "append", "decode"):
+            s.call(entry)
+            if pause:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert int(s.status.item()) == 0
+        return s.out.view(torch.int16).clone(), s.pool.view(torch.int16).clone()
+
+    want = chain(True)
+    for _ in range(20):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
