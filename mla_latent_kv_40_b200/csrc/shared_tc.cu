@@ -419,7 +419,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         uint32_t n = 0, ns = 0, uc = 0;
         bool ok = true;
         while (ok && it.next(p)) {
-          ok = waitw(sm, bar(B_QREADY), uc & 1, p.dev_status);
+          ok = waitw(sm, bar(B_QREADY), uc & 1, p.dev_status, true);
           ++uc;
           for (int t = it.t0; ok && t < it.t1; ++t, ++ns) {
             const uint32_t sbuf = ns & 1, dcol = tbase + kSCol + 128 * sbuf;
@@ -471,7 +471,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
           for (int g = 2 * it.t0; g < it.pages_end(); ++g, ++pn) {
             const uint32_t pb = pn % kPSlots, sg = pn % kStgTiles;
             ok = wait1(sm, bar(B_STGFULL + sg), (pn / kStgTiles) & 1, p.dev_status) &&
-                 (pn < kPSlots || wait1(sm, bar(B_PEMPTY + pb), (pn / kPSlots - 1) & 1, p.dev_status));
+                 (pn < kPSlots || wait1(sm, bar(B_PEMPTY + pb), (pn / kPSlots - 1) & 1, p.dev_status, true));
             if (!ok) break;
             bulk_copy_to_peer(pslot_remote + pb * kPSlotBytes, smem_u32(tiles + kStgOff + sg * kPSlotBytes), kPTxBytes,
                               pfull_remote + 8 * pb);
@@ -530,7 +530,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             if (lane < 2 && run_pages >= 2) {
               const int pb = (np - 2 + lane) % kPSlots;
               mbar_expect_tx(bar(B_PFULL + pb), kPTxBytes);
-              mbar_arrive_cluster_light(mapa(bar(B_PEMPTY + pb), side));
+              mbar_arrive_cluster(mapa(bar(B_PEMPTY + pb), side));   // (it stored there)
             }
             __syncwarp();
           }
@@ -550,7 +550,8 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
 #pragma unroll
             for (int w = 0; w < 4; ++w) flags |= reinterpret_cast<const uint32_t *>(pa + w * kPaWords)[32];
             const bool moved = flags & kMoved, odd = flags & kOdd;
-            if (!(ok = waitw(sm, bar(B_CFULL + sv), (np / kVStages) & 1, p.dev_status))) break;
+            // At rank 2 the phase holds rank 3's arrival, which passes on what its epilogue warps stored in an own page.
+            if (!(ok = waitw(sm, bar(B_CFULL + sv), (np / kVStages) & 1, p.dev_status, lead && m >= 0))) break;
             if (flags || left < kPage) {
               // O is read back for a rescale: the previous page's MMAs must be complete.
               if (moved && !(ok = waitw(sm, bar(B_PVDONE + (np - 1) % kPSlots), ((np - 1) / kPSlots) & 1, p.dev_status)))
@@ -566,7 +567,10 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             if (!lead) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_light(ready + 8 * sv);
+              if (lane == 0) {
+                if (odd || left < kPage) mbar_arrive_cluster(ready + 8 * sv);   // the page was tidied: by stores that rank 2's MMAs read
+                else mbar_arrive_cluster_light(ready + 8 * sv);
+              }
               continue;
             }
             tc_fence_after();
@@ -675,7 +679,8 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_light(mapa(bar(B_QREADY), 0));   // read by the async proxy only, which the fences order
+        // A release for the cluster: rank 0's MMAs read the RoPE rows that these warps stored in either CTA.
+        if (lane == 0) mbar_arrive_cluster(mapa(bar(B_QREADY), 0));
       }
       // This row's member and how many of that member's own keys it sees; rows past the unit's end see none.
       Members mem;

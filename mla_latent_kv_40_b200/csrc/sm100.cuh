@@ -109,8 +109,10 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
 }
 
 // The same arrival without ordering this thread's writes for the other CTA.  The cluster-scope release costs a few
-// hundred cycles where the thread has writes in flight; arrivals that only pass on tensor-memory reads (ordered by
-// tcgen05.fence) or copies of the async proxy (ordered by their own barrier) do without it.
+// hundred cycles where the thread has writes in flight; arrivals that only pass on reads that are over, of tensor memory
+// (ordered by tcgen05.fence) or of a buffer that may be filled again, or copies of the async proxy (ordered by their own
+// barrier) do without it.  Where ordinary stores of this CTA are read or written over by another CTA's MMAs or copies, the
+// release above is needed, with a wait that acquires for the cluster.
 __device__ __forceinline__ void mbar_arrive_cluster_light(uint32_t remote_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
