@@ -45,7 +45,9 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int *dev
 //   D[m][r] = sum_k W_UK[s][m0 + m][k] q_nope[r0 + r][s][k]   (A and B both K-major)
 // The CTAs with blockIdx.y == 0 .. 3 share the RoPE of their 64 rows.
 // (s, by, bz) play the roles of (blockIdx.x, blockIdx.y, blockIdx.z) of a grid (H, d_c / 128, rows / 64)
-// whose y extent is ny; sm is the CTA's 1024-byte aligned dynamic shared memory.
+// whose y extent is ny; sm is the CTA's 1024-byte aligned dynamic shared memory.  kSettled: the kernel behind this one
+// reads lengths ahead of its own wait, so it may start only when what wrote them is complete, behind this one's wait.
+template <bool kSettled>
 __device__ __forceinline__ void absorb_tc_body(const CUtensorMap &map_w, const CUtensorMap &map_q, const AbsorbArgs &a,
                                                int *dev_status, int s, int by, int bz, int ny, unsigned char *sm) {
   __shared__ __align__(8) uint64_t bar_full, bar_mma;
@@ -60,6 +62,7 @@ __device__ __forceinline__ void absorb_tc_body(const CUtensorMap &map_w, const C
   const int m0 = by * 128, r0 = bz * kTcN;
   const int R = a.B * a.n_q, W = a.d_c + a.d_rope;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!kSettled) grid_dep_launch();
 
   if (tid == 0) {
     mbar_init(smem_u32(&bar_full), 1);
@@ -96,8 +99,7 @@ __device__ __forceinline__ void absorb_tc_body(const CUtensorMap &map_w, const C
     if (tid - 32 < half) theta[tid - 32] = rope_theta(tid - 32, a.d_rope, a.rope_base);
     asm volatile("bar.sync 1, 96;" ::: "memory");       // warps 1-3 only
     grid_dep_wait();                                       // the lengths may be new; q_out may still be read by an earlier kernel
-    // Only now may the attention start: it reads the lengths at once, and whatever wrote them is complete here.
-    if (warp == 1) grid_dep_launch();
+    if (kSettled && warp == 1) grid_dep_launch();
     constexpr int kRowsPerWarp = 6;                        // 16 rows a CTA (d_c = 512) as 6, 6 and 4 of the three warps
     const int nr = (kTcN - by + ny - 1) / ny;
     for (int w0 = (warp - 1) * kRowsPerWarp; w0 < nr; w0 += 3 * kRowsPerWarp) {
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kTcThreads)
 absorb_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_q, AbsorbArgs a,
                  int *dev_status) {
   extern __shared__ unsigned char smem_raw[];
-  absorb_tc_body(map_w, map_q, a, dev_status, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.y, align1024(smem_raw));
+  absorb_tc_body<true>(map_w, map_q, a, dev_status, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.y, align1024(smem_raw));
 }
 
 // The absorption and, in block 0, the plan of a decode over shared prefixes: neither needs the other, and as launches of
@@ -198,7 +200,7 @@ absorb_plan_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     return;
   }
   const int id = blockIdx.x - 1, s = id % a.H, by = (id / a.H) % ny, bz = id / (a.H * ny);
-  absorb_tc_body(map_w, map_q, a, dev_status, s, by, bz, ny, align1024(smem_raw));
+  absorb_tc_body<false>(map_w, map_q, a, dev_status, s, by, bz, ny, align1024(smem_raw));
 }
 
 // ------------------------------------------------------------------ append projection
@@ -365,7 +367,7 @@ decode_prep_kernel(const __grid_constant__ CUtensorMap map_wd, const __grid_cons
   id -= pp.nA;
   if (id < pp.nB) {
     const int s = id % pp.ab.H, by = (id / pp.ab.H) % pp.b_ny, bz = id / (pp.ab.H * pp.b_ny);
-    absorb_tc_body(map_w, map_q, pp.ab, pp.ap.dev_status, s, by, bz, pp.b_ny, sm);
+    absorb_tc_body<true>(map_w, map_q, pp.ab, pp.ap.dev_status, s, by, bz, pp.b_ny, sm);
     return;
   }
   const int tok = id - pp.nB;

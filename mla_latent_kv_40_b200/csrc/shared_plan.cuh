@@ -61,15 +61,20 @@ __device__ __forceinline__ int last_at(const int *a, int n, int v) {
 __device__ __forceinline__ int cluster_of(int64_t at, int W, int C) { return (int)(((at + 1) * C + W - 1) / W - 1); }
 
 // `words`: shared_plan_words() words of shared memory, or NULL to use a.out.scratch.
+//
+// The lengths and groups may be what the kernel ahead still writes, and only grid_dep_wait() makes that visible.  The plan is
+// formed ahead of the wait all the same, from copies, and again behind it if a copy differs from what is there then: a
+// plan behind the wait alone took 5 us of a call of 28.  Any words that are read ahead give a plan within bounds.
 __device__ __forceinline__ void shared_plan_body(const SharedPlanArgs &a, int *words) {
   __shared__ int64_t part[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int B = a.B, R = a.R, unit_rows = shared_unit_rows(R);
   const SharedPlan &pl = a.out;
-  // The lengths and groups may be what the kernel before wrote (mla_plan_step, mla_release_blocks, the user's own), and
-  // earlier calls may still read the plan, or use the scratch words, that are overwritten here.
-  sm100::grid_dep_wait();
-  if (!words) words = pl.scratch;
+  bool waited = !words;
+  if (!words) {
+    sm100::grid_dep_wait();   // an earlier call may still use the scratch words
+    words = pl.scratch;
+  }
   int *const own = words;                        // [B + 1] own pages before each sequence
   int *const seq_shared = own + B + 1;           // [B] shared pages
   int *const cost0 = seq_shared + B;             // [max_units + 1]
@@ -77,84 +82,109 @@ __device__ __forceinline__ void shared_plan_body(const SharedPlanArgs &a, int *w
   int *const shared_of = tiles_of + a.max_units;
   int *const span_of = shared_of + a.max_units;  // first sequence * 64 + members
   int *const group_units = span_of + a.max_units;   // [num_groups + 1] first unit
-  int G = a.num_groups, bad = 0;
-  for (int g = tid; g < G; g += threads) {
-    const int lo = a.offsets[g], hi = a.offsets[g + 1];
-    bad |= lo < 0 || lo > hi || hi > B || (g == 0 && lo != 0) || (g == G - 1 && hi != B) || a.prefix_lens[g] < 0;
-  }
-  bad = __syncthreads_or(bad);
-  if (bad) G = 1;    // then one group that shares nothing
-  auto first_of = [&](int g) { return bad ? g * B : a.offsets[g]; };
-  // Units before each group.
-  int64_t units = 0;
-  for (int g0 = 0; g0 < G; g0 += threads) {
-    const int g = g0 + tid;
-    const int64_t rows = g < G ? (int64_t)(first_of(g + 1) - first_of(g)) * R : 0;
-    const int64_t exc = plan_scan((rows + unit_rows - 1) / unit_rows, part, units);
-    if (g < G) group_units[g] = (int)exc;
-  }
-  if (tid == 0) group_units[G] = (int)units;
-  __syncthreads();
-  const int U = (int)units;
-  // Shared pages of every group.
-  int wrong = 0;
-  for (int g = warp; g < G; g += threads / 32) {
-    const int lo = first_of(g), hi = first_of(g + 1), u0 = group_units[g], n = group_units[g + 1] - u0;
-    int common = bad ? 0 : a.prefix_lens[g];
-    for (int b = lo + lane; b < hi; b += 32) {
-      const int S = a.seqlens[b];
-      wrong |= S < a.n_q || S > a.max_seqlen;
-      common = min(common, max(min(S, a.max_seqlen) - a.n_q + 1, 0));
+  int *const lens = group_units + a.num_groups + 1;   // [B], [num_groups + 1], [num_groups] copies of the inputs
+  int *const offs = lens + B;
+  int *const prefs = offs + a.num_groups + 1;
+  // Every input word and its copy, past L1, which may hold what was there ahead of the wait (one load's latency up to as many
+  // words as threads).
+  auto inputs = [&](auto &&f) {
+    for (int i = tid; i < B + 2 * a.num_groups + 1; i += threads) {
+      const int g = i - B, p = g - a.num_groups - 1;
+      f(lens[i], __ldcg(g < 0 ? a.seqlens + i : p < 0 ? a.offsets + g : a.prefix_lens + p));
     }
+  };
+  int G, bad, wrong, U, longest, W, C;
+  int64_t list;
+  auto first_of = [&](int g) { return bad ? g * B : offs[g]; };
+  for (;;) {
+    inputs([](int &copy, int word) { copy = word; });
+    __syncthreads();
+    G = a.num_groups;
+    bad = 0;
+    for (int g = tid; g < G; g += threads) {
+      const int lo = offs[g], hi = offs[g + 1];
+      bad |= lo < 0 || lo > hi || hi > B || (g == 0 && lo != 0) || (g == G - 1 && hi != B) || prefs[g] < 0;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) G = 1;    // then one group that shares nothing
+    // Units before each group.
+    int64_t units = 0;
+    for (int g0 = 0; g0 < G; g0 += threads) {
+      const int g = g0 + tid;
+      const int64_t rows = g < G ? (int64_t)(first_of(g + 1) - first_of(g)) * R : 0;
+      const int64_t exc = plan_scan((rows + unit_rows - 1) / unit_rows, part, units);
+      if (g < G) group_units[g] = (int)exc;
+    }
+    if (tid == 0) group_units[G] = (int)units;
+    __syncthreads();
+    U = (int)units;
+    // Shared pages of every group.
+    wrong = 0;
+    for (int g = warp; g < G; g += threads / 32) {
+      const int lo = first_of(g), hi = first_of(g + 1), u0 = group_units[g], n = group_units[g + 1] - u0;
+      int common = bad ? 0 : prefs[g];
+      for (int b = lo + lane; b < hi; b += 32) {
+        const int S = lens[b];
+        wrong |= S < a.n_q || S > a.max_seqlen;
+        common = min(common, max(min(S, a.max_seqlen) - a.n_q + 1, 0));
+      }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) common = min(common, __shfl_xor_sync(0xffffffffu, common, o));
-    const int shared = common / a.block_size * (a.block_size / kSharedPage);
-    for (int b = lo + lane; b < hi; b += 32) seq_shared[b] = shared;
-    for (int i = lane; i < n; i += 32) {
-      const int row0 = lo * R + i * unit_rows, rows = min(unit_rows, hi * R - row0);
-      const int seq0 = row0 / R, last = (row0 + rows - 1) / R;
-      shared_of[u0 + i] = shared;
-      span_of[u0 + i] = seq0 * 64 + last - seq0 + 1;
+      for (int o = 16; o; o >>= 1) common = min(common, __shfl_xor_sync(0xffffffffu, common, o));
+      const int shared = common / a.block_size * (a.block_size / kSharedPage);
+      for (int b = lo + lane; b < hi; b += 32) seq_shared[b] = shared;
+      for (int i = lane; i < n; i += 32) {
+        const int row0 = lo * R + i * unit_rows, rows = min(unit_rows, hi * R - row0);
+        const int seq0 = row0 / R, last = (row0 + rows - 1) / R;
+        shared_of[u0 + i] = shared;
+        span_of[u0 + i] = seq0 * 64 + last - seq0 + 1;
+      }
     }
-  }
-  __syncthreads();
-  // Own pages before each sequence.
-  int64_t pages_all = 0;
-  for (int b0 = 0; b0 < B; b0 += threads) {
-    const int b = b0 + tid;
-    int n = 0;
-    if (b < B) n = (max(min(a.seqlens[b], a.max_seqlen) - kSharedPage * seq_shared[b], 0) + kSharedPage - 1) / kSharedPage;
-    const int64_t exc = plan_scan(n, part, pages_all);
-    if (b < B) own[b] = (int)exc;
-  }
-  if (tid == 0) own[B] = (int)pages_all;
-  __syncthreads();
-  // Tiles of every unit and its place; non-empty units are counted in the low word.
-  int64_t list = 0;
-  int longest = 0;
-  for (int u0 = 0; u0 < U; u0 += threads) {
-    const int u = u0 + tid;
-    int tiles = 0;
-    if (u < U) {
-      const int seq0 = span_of[u] >> 6;
-      tiles = (shared_of[u] + own[seq0 + (span_of[u] & 63)] - own[seq0] + 1) / 2;
+    __syncthreads();
+    // Own pages before each sequence.
+    int64_t pages_all = 0;
+    for (int b0 = 0; b0 < B; b0 += threads) {
+      const int b = b0 + tid;
+      int n = 0;
+      if (b < B) n = (max(min(lens[b], a.max_seqlen) - kSharedPage * seq_shared[b], 0) + kSharedPage - 1) / kSharedPage;
+      const int64_t exc = plan_scan(n, part, pages_all);
+      if (b < B) own[b] = (int)exc;
     }
-    const int64_t exc = plan_scan((int64_t)(tiles > 0) | ((int64_t)tiles << 32), part, list);
-    if (u < U) {
-      cost0[u] = (int)(exc >> 32) + kUnitCost * (int)(exc & 0xffffffff);
-      tiles_of[u] = tiles;
+    if (tid == 0) own[B] = (int)pages_all;
+    __syncthreads();
+    // Tiles of every unit and its place; non-empty units are counted in the low word.
+    list = 0;
+    longest = 0;
+    for (int u0 = 0; u0 < U; u0 += threads) {
+      const int u = u0 + tid;
+      int tiles = 0;
+      if (u < U) {
+        const int seq0 = span_of[u] >> 6;
+        tiles = (shared_of[u] + own[seq0 + (span_of[u] & 63)] - own[seq0] + 1) / 2;
+      }
+      const int64_t exc = plan_scan((int64_t)(tiles > 0) | ((int64_t)tiles << 32), part, list);
+      if (u < U) {
+        cost0[u] = (int)(exc >> 32) + kUnitCost * (int)(exc & 0xffffffff);
+        tiles_of[u] = tiles;
+      }
+      longest = max(longest, tiles);
     }
-    longest = max(longest, tiles);
-  }
-  const int W = (int)(list >> 32) + kUnitCost * max((int)(list & 0xffffffff) - 1, 0), C = min(W, a.clusters);
+    W = (int)(list >> 32) + kUnitCost * max((int)(list & 0xffffffff) - 1, 0);
+    C = min(W, a.clusters);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-  __syncthreads();
-  if (lane == 0) part[warp] = longest;
-  __syncthreads();
-  longest = lane < threads / 32 ? (int)part[lane] : 0;
+    for (int o = 16; o; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    __syncthreads();
+    if (lane == 0) part[warp] = longest;
+    __syncthreads();
+    longest = lane < threads / 32 ? (int)part[lane] : 0;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    for (int o = 16; o; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    if (waited) break;
+    sm100::grid_dep_wait();   // (earlier calls may also still read the plan that is overwritten from here on)
+    waited = true;
+    int news = 0;
+    inputs([&](int &copy, int word) { news |= copy != word; });
+    if (!__syncthreads_or(news)) break;
+  }
   const bool whole = (int)(list & 0xffffffff) <= a.clusters && (int64_t)longest * C <= W;
   __syncthreads();
   if ((bad && tid == 0) || wrong) report(a.dev_status, MLA_ERR_BAD_INDEX);

@@ -40,7 +40,7 @@ struct SharedPlan {
 };
 // Words that the plan works on (in shared memory while they fit there).
 inline size_t shared_plan_words(int B, int units, int num_groups) {
-  return 2 * (size_t)B + 1 + 4 * (size_t)units + 1 + (size_t)num_groups + 1;
+  return 3 * (size_t)B + 1 + 4 * (size_t)units + 1 + 3 * (size_t)num_groups + 2;
 }
 
 constexpr int kSharedMaxClusters = 64;
