@@ -126,7 +126,7 @@ __device__ __forceinline__ void shared_plan_body(const SharedPlanArgs &a, int *w
       for (int b = lo + lane; b < hi; b += 32) {
         const int S = lens[b];
         wrong |= S < a.n_q || S > a.max_seqlen;
-        common = min(common, max(min(S, a.max_seqlen) - a.n_q + 1, 0));
+        common = min(common, max(min(max(S, 0), a.max_seqlen) - a.n_q + 1, 0));
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) common = min(common, __shfl_xor_sync(0xffffffffu, common, o));
@@ -145,7 +145,7 @@ __device__ __forceinline__ void shared_plan_body(const SharedPlanArgs &a, int *w
     for (int b0 = 0; b0 < B; b0 += threads) {
       const int b = b0 + tid;
       int n = 0;
-      if (b < B) n = (max(min(lens[b], a.max_seqlen) - kSharedPage * seq_shared[b], 0) + kSharedPage - 1) / kSharedPage;
+      if (b < B) n = (max(min(max(lens[b], 0), a.max_seqlen) - kSharedPage * seq_shared[b], 0) + kSharedPage - 1) / kSharedPage;
       const int64_t exc = plan_scan(n, part, pages_all);
       if (b < B) own[b] = (int)exc;
     }
