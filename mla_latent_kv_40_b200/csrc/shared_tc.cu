@@ -105,7 +105,8 @@ enum Bar {
   B_REQDONE = B_REQ + 1,
   B_STATSFULL = B_REQDONE + 1,          // value: row statistics of a finished unit
   B_OFREE = B_STATSFULL + 1,            // value: both CTAs' O has been read (both CTAs)
-  B_COUNT = B_OFREE + 1
+  B_RUNSEEN = B_OFREE + 1,              // value: the slots' thread has seen the MMAs of the run's last pages
+  B_COUNT = B_RUNSEEN + 1
 };
 
 struct Req {
@@ -525,7 +526,9 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
           Members mem;
           mem.load(p, it.un);
           if (uc > 0) {
-            if (!(ok = waitw(sm, bar(B_OFREE), (uc - 1) & 1, p.dev_status))) break;
+            // Warp 2 must have seen the phases of the run's last slots before these go round again, or it would wait for the
+            // other parity: no phase of this barrier completes before the one ahead of it has been waited for here.
+            if (!(ok = waitw(sm, bar(B_OFREE), (uc - 1) & 1, p.dev_status) && waitw(sm, bar(B_RUNSEEN), (uc - 1) & 1, p.dev_status))) break;
             // The epilogue is through with the P slots of the finished run's last two pages, which it borrowed.
             if (lane < 2 && run_pages >= 2) {
               const int pb = (np - 2 + lane) % kPSlots;
@@ -609,6 +612,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             mbar_expect_tx(bar(B_PFULL + pb), kPTxBytes);
             mbar_arrive_cluster_light(pempty + 8 * pb);
           }
+          if (ok) mbar_arrive(bar(B_RUNSEEN));
         }
       }
     }
