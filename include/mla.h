@@ -421,7 +421,9 @@ MLA_API int mla_decode_sparse(const mla_dims *dims, int B, int n_q, const void *
  *   block_table is required.  w_uv == NULL writes o_lat [B, n_q, H, d_c], as
  *   mla_decode_latent.  The other arguments, outputs and errors as mla_decode.
  *   Values that are not finite in a sequence's own rows reach that sequence
- *   alone; in shared rows, every sequence that shares them.
+ *   alone; in shared rows, every sequence that shares them.  out is NaN for
+ *   query rows that see such a latent, also under a score of -inf (lse of such
+ *   rows means nothing).
  *   Shapes of the tensor-core path (mla_decode_path) share; other shapes run
  *   every sequence by itself, with the same results.  Where they share, out and
  *   w_uv must be 16-byte aligned (else MLA_ERR_UNSUPPORTED), and so must c_kv

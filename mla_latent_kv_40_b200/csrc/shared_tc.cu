@@ -119,6 +119,7 @@ struct Small {                          // behind the tiles
   float stat_l[kRows], stat_m[kRows];
   float m_sh[2][kRows];                 // score: reference maximum after a tile, per group
   float xl[kRows];
+  int odd_seen[2];                      // score: own pages of the run with scores that are not finite, per group
   uint64_t bars[B_COUNT];
   Req req;
   uint32_t tmem_base;
@@ -138,6 +139,8 @@ struct Params {
   float *o_part, *lse_part;
   int *dev_status;
   const unsigned char *tiled;           // tiled pool, or NULL: row pool through the tensor maps
+  const unsigned char *rows;            // the row pool's latents
+  int64_t row_bytes;
 };
 
 // ------------------------------------------------------------ cta_group::2 forms
@@ -303,7 +306,8 @@ struct PageRows {
 };
 
 // The latents of a page before its MMAs, thread t of 256: rows from `keys` on become zero and, with `scan`, so does every
-// value that is not finite.  The rows that see such a key have NaN from their scores.
+// value that is not finite.  The rows that see such a key have NaN from their scores, or from a sum that is made NaN at the
+// end of the run.
 __device__ __noinline__ void tidy_page(unsigned char *vt, int keys, int scan, int t) {
   // 4 chunks of 64 rows of 8 pieces of 16 bytes; piece t + 256 i lies in row (t >> 3) + 32 (i & 1) of chunk i >> 1.
 #pragma unroll 1
@@ -320,6 +324,42 @@ __device__ __noinline__ void tidy_page(unsigned char *vt, int keys, int scan, in
       *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+}
+
+// Whether this lane's row sees a key of member `mine` whose latents are not all finite among the own pages of a run: `vis` own
+// keys of that member are seen.  Warp-collective, and slow: for runs that have scores which are not finite.
+__device__ __noinline__ bool sees_lost_key(const Params &p, const SharedUnit un, const Members mem, int page0, int page1, int mine,
+                                           int vis) {
+  const int lane = threadIdx.x & 31;
+  bool sees = false;
+#pragma unroll 1
+  for (int v = max(page0, un.shared); v < page1; ++v) {
+    int own;
+    const int m = mem.owner(v, own);
+    if (!__any_sync(0xffffffffu, m == mine)) continue;
+    const int left = __shfl_sync(0xffffffffu, mem.keys, m) - kPage * own;
+    const int64_t row = max(mem.row(p, un, v), (int64_t)0);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const int key = lane + 32 * half;
+      bool bad = false;
+#pragma unroll 1
+      for (int c = 0; c < kDc / 64 && key < left; ++c) {
+        const unsigned char *src = p.tiled ? p.tiled + (row / kPage) * (9 * kChunkBytes) + c * kChunkBytes + key * 128
+                                           : p.rows + (row + key) * p.row_bytes + c * 128;
+        for (int g = 0; g < 8; ++g) {
+          const uint4 y = *reinterpret_cast<const uint4 *>(src + 16 * g);
+          const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bad |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+        }
+      }
+      const uint32_t lost = __ballot_sync(0xffffffffu, bad);
+      const int first = lost ? __ffs(lost) - 1 + 32 * half : kPage;
+      sees |= m == mine && kPage * own + first < vis && first < kPage;
+    }
+  }
+  return sees;
 }
 
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
@@ -692,6 +732,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
       const int gr = it.un.row0 + kRows * (int)side + r, R = p.n_q * p.H;
       const int my_m = kRows * (int)side + r < it.un.rows ? gr / R - it.un.seq0 : -2;
       const int vis = __shfl_sync(0xffffffffu, mem.keys, max(my_m, 0)) - p.n_q + 1 + (gr % R) / p.H;
+      if (q4 == 0 && lane == 0) sm.odd_seen[h] = 0;
       float m_mine = -CUDART_INF_F, l = 0.f;   // l: this group's row sum, relative to m_mine
       const uint32_t ns_end = ns + (uint32_t)(it.t1 - it.t0);
       // One tile.  Mixed: some page of it is one member's.  A copy of its own, as the checks alone that such pages need took 4 %
@@ -714,16 +755,17 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
             mx = max3f(mx, __uint_as_float(v[1][k]), __uint_as_float(v[1][k + 1]));
           }
         };
-        // Visible keys of both pages: 64 or more of a shared page, none of another member's page.
-        auto seen = [&](int pg) {
+        // Visible keys of both pages: 64 or more of a shared page, none of another member's page.  left: keys of the owner there.
+        int n0 = kPage, n1 = kPage, left0 = -1, left1 = -1;
+        auto seen = [&](int pg, int &left) {
           int own;
           const int m = mem.owner(2 * t + pg, own);
+          left = m < 0 ? -1 : __shfl_sync(0xffffffffu, mem.keys, m) - kPage * own;
           return m < 0 ? kPage : (m == my_m ? vis - kPage * own : 0);
         };
-        int n0 = kPage, n1 = kPage;
         if (mixed) {
-          n0 = seen(0);
-          if (npg == 2) n1 = seen(1);
+          n0 = seen(0, left0);
+          if (npg == 2) n1 = seen(1, left1);
         }
         auto mask_page = [&](int n) {   // only pages that some row of the warp does not see whole
           if (!mixed || __all_sync(0xffffffffu, n >= kPage)) return;
@@ -736,17 +778,26 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         // A latent that is not finite leaves no row's score of its key finite (0 * x is NaN), so one warp's rows tell which of
         // the pages have such.  It matters where a page is one member's among several: the others' P is 0 there, and the value
         // pair must not multiply that by NaN.  (1 to 2 us of a batch of many own pages; looking at the latents themselves
-        // took 4 to 6 of 110, in shared-memory reads that the MMAs missed.)
+        // took 4 to 6 of 110, in shared-memory reads that the MMAs missed.)  What lies behind a member's last key is zero there
+        // anyhow.
         uint32_t odd = 0;             // kOdd for the first page, kOdd << 8 for the second
         if (mixed && q4 == 0 && it.un.members > 1) {
 #pragma unroll 1
           for (int pg = 0; pg < npg; ++pg) {
+            const int left = pg ? left1 : left0;
+            if (left < 0) continue;   // a shared page
             load_page(pg);
             tmem_wait_ld();
             float z = 0.f;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) z = fmaf(__uint_as_float(v[0][k]), 0.f, fmaf(__uint_as_float(v[1][k]), 0.f, z));
-            if (__any_sync(0xffffffffu, (__float_as_uint(z) & 0x7fffffffu) != 0u) && 2 * t + pg >= it.un.shared) odd |= kOdd << (8 * pg);
+            for (int k = 0; k < 32; ++k) {
+              z = fmaf(k < left ? __uint_as_float(v[0][k]) : 0.f, 0.f, z);
+              z = fmaf(k + 32 < left ? __uint_as_float(v[1][k]) : 0.f, 0.f, z);
+            }
+            if (__any_sync(0xffffffffu, (__float_as_uint(z) & 0x7fffffffu) != 0u)) {
+              odd |= kOdd << (8 * pg);
+              if (lane == 0) sm.odd_seen[h] = 1;
+            }
           }
         }
         // The second page only for its maximum (it is read again below), the first one to stay.
@@ -839,6 +890,9 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (last) {
         l += sm.xl[r];
+        // An infinite latent may leave a score of -inf, so a weight of 0, and is taken out of the page for the other members'
+        // sake; but 0 * inf is NaN.
+        if ((sm.odd_seen[0] | sm.odd_seen[1]) && sees_lost_key(p, it.un, mem, 2 * it.t0, it.pages_end(), my_m, vis)) l = CUDART_NAN_F;
         if (uc > 0) waitw(sm, bar(B_STATSEMPTY), (uc - 1) & 1, p.dev_status);
         const uint32_t mate = 2 + side;   // the value CTA of these rows
         st_cluster_f32(mapa(smem_u32(&sm.stat_l[r]), mate), l);
@@ -895,7 +949,7 @@ shared_attn_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_const
         const float l = sm.stat_l[r], m = sm.stat_m[r];
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(statsempty_remote);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // (NaN stays NaN)
         const int64_t prow = it.part_row() + kRows * side + r;
         const int rows = it.un.rows - kRows * (int)side;   // of this CTA
         const bool live = r < rows;
@@ -1065,6 +1119,8 @@ int launch_shared_attention(const mla_dims &d, int n_q, int max_seqlen, const Sh
   p.lse_part = lse_part;
   p.dev_status = dev_status;
   p.tiled = tiled ? static_cast<const unsigned char *>(cache.c_kv) : nullptr;
+  p.rows = static_cast<const unsigned char *>(cache.c_kv);
+  p.row_bytes = 2 * (int64_t)cache.ckv_stride;
   return launch_pdl(shared_attn_kernel, dim3(4 * C), dim3(kThreads), kSmemBytes, st, mc, mpe, p) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from helpers import check_close
-from test_shared_parity import Call, V2L, make_shared, reference, some
+from test_shared_parity import Call, V2L, _heads, make_shared, reference, some
 
 INT_MIN, INT_MAX = -2**31, 2**31 - 1
 
@@ -26,3 +26,38 @@ def test_shared_lengths_at_the_ends_of_their_type(lib, bad, n_q):
     out, lse, st = c.result()
     assert st == -6
     check_close(out[idx], ref[idx], "bf16", "other group")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("heads,n_q", [(4, 1), (16, 2), (96, 1), (128, 1)])
+def test_shared_infinite_latents_leave_their_sequence_no_finite_row(lib, heads, n_q, layout):
+    """0 * inf is NaN also where the infinite latent makes the score -inf: every row that sees such a key has NaN, as in a
+    decode of its own and whoever shares its unit; the other sequences keep their bits."""
+    groups = [(192, [250, 330, 193 + n_q, 500, 196, 260]), (0, [70, 40])]
+    inp = make_shared(_heads(heads), groups, n_q, 64, seed=heads)
+    c = Call(lib, inp, layout)
+    c.run()
+    want, _, st = c.result()
+    assert st == 0
+    inf = float("inf")
+    for seq, key, dim, value in ((3, 450, 300, inf), (3, 450, 300, -inf), (1, 200, 0, -inf), (1, 329, 511, inf), (4, 192, 10, -inf),
+                                 (7, 0, 255, inf), (5, 256, 256, -inf), (0, 249, 575, inf)):
+        bad = dict(inp, pool=inp["pool"].clone())
+        row = int(inp["block_table"][seq, key // 64]) * 64 + key % 64
+        bad["pool"][row, dim] = value
+        c, plain = Call(lib, bad, layout), Call(lib, bad, layout, groups=False)
+        c.run()
+        plain.run()
+        (got, _, st), (alone, _, _) = c.result(), plain.result()
+        assert st == 0
+        others = [b for b in range(8) if b != seq]
+        assert np.array_equal(got[others], want[others]), (seq, value)
+        S = int(inp["seqlens"][seq])
+        for j in range(n_q):
+            if key > S - n_q + j:   # (a row that does not see the key: mla_decode multiplies it by 0)
+                continue
+            # (a RoPE key of -inf is a key of no weight: nothing of it is in the values)
+            if dim < 512:
+                assert np.isnan(got[seq, j]).all(), (seq, key, dim, j)
+            assert np.array_equal(np.isnan(got[seq, j]), np.isnan(alone[seq, j])), (seq, key, dim, j)
