@@ -217,12 +217,12 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanArgs 
 
   if (kMode != kFinish) {
     // New table entries.
-    for (int k0 = gtid * kPer; k0 < taken; k0 += threads * kPer) {
-      int b = last_le(cum, B, k0);
+    for (uint32_t k0 = gtid * kPer; k0 < (uint32_t)taken; k0 += threads * kPer) {   // (unsigned: the last step may pass 2^31)
+      int b = last_le(cum, B, (int)k0);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int k = k0 + i;
-        if (k >= taken) break;
+        if (k0 + i >= (uint32_t)taken) break;
+        const int k = (int)(k0 + i);
         while (b + 1 < B && cum[b + 1] <= k) ++b;
         int id = a.free_list[free - 1 - k];
         if (id < 0 || id >= a.num_blocks) {
@@ -243,18 +243,18 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanArgs 
     }
     // Tokens: request, position and pool row.
     const int T = cu[B];
-    for (int t0 = gtid * kPer; t0 < T; t0 += threads * kPer) {
-      int b = last_le(cu, B, t0);
+    for (uint32_t t0 = gtid * kPer; t0 < (uint32_t)T; t0 += threads * kPer) {
+      int b = last_le(cu, B, (int)t0);
       int32_t sq[kPer], ps[kPer];
       int64_t sl[kPer];
       int at_b = -1, at_l = -1;
       int32_t blk = -1;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int t = t0 + i;
         sq[i] = ps[i] = -1;
         sl[i] = -1;
-        if (t < T) {
+        if (t0 + i < (uint32_t)T) {
+          const int t = (int)(t0 + i);
           while (b + 1 < B && cu[b + 1] <= t) ++b;
           const int c = held[b];
           if (c >= 0) {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanArgs 
           }
         }
       }
-      if (a.vec && t0 + kPer <= T) {
+      if (a.vec && t0 + kPer <= (uint32_t)T) {
         *reinterpret_cast<int4 *>(a.seq_idx + t0) = make_int4(sq[0], sq[1], sq[2], sq[3]);
         *reinterpret_cast<int4 *>(a.pos + t0) = make_int4(ps[0], ps[1], ps[2], ps[3]);
         if (a.slots) {
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanArgs 
       } else {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-          if (t0 + i < T) {
+          if (t0 + i < (uint32_t)T) {
             a.seq_idx[t0 + i] = sq[i];
             a.pos[t0 + i] = ps[i];
             if (a.slots) a.slots[t0 + i] = sl[i];
@@ -392,12 +392,12 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) 
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   if (kMode != kFinish) {
-    for (int k0 = gtid * kPer; k0 < put; k0 += threads * kPer) {
-      int b = last_le(cum, B, k0);
+    for (uint32_t k0 = gtid * kPer; k0 < (uint32_t)put; k0 += threads * kPer) {
+      int b = last_le(cum, B, (int)k0);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int k = k0 + i;
-        if (k >= put) break;
+        if (k0 + i >= (uint32_t)put) break;
+        const int k = (int)(k0 + i);
         while (b + 1 < B && cum[b + 1] <= k) ++b;
         const int id = a.block_table[(int64_t)b * a.max_blocks_per_seq + first[b] + (k - cum[b])];
         if (id < 0 || id >= a.num_blocks) report(status, MLA_ERR_BAD_INDEX);

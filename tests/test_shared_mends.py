@@ -61,3 +61,36 @@ def test_shared_infinite_latents_leave_their_sequence_no_finite_row(lib, heads, 
             if dim < 512:
                 assert np.isnan(got[seq, j]).all(), (seq, key, dim, j)
             assert np.array_equal(np.isnan(got[seq, j]), np.isnan(alone[seq, j])), (seq, key, dim, j)
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.gpu
+def test_plan_and_release_of_nearly_2_to_31_tokens_and_blocks(lib):
+    """Four requests of 2^29 - 1 tokens in blocks of one token: 2^31 - 4 tokens, table entries and free ids, so that the last
+    step of every thread's walk passes 2^31."""
+    n, B = 2**29 - 1, 4
+    total = n * B
+    dims = lib.make_dims(16, 512, 64, 128, 128, 7168, 1, "bf16")
+    free_list = torch.arange(total, dtype=torch.int32, device="cuda")
+    free, lens, cu, st = _i32([total]), _i32([0] * B), _i32([0] * (B + 1)), _i32([0])
+    table = torch.full((B, n), -1, dtype=torch.int32, device="cuda")
+    seq_idx = torch.full((total,), -7, dtype=torch.int32, device="cuda")
+    pos = torch.full((total,), -7, dtype=torch.int32, device="cuda")
+    lib.mla_plan_step(dims, lens, _i32([n] * B), None, None, None, free_list, free, table, total, lens, cu, seq_idx, pos, None, free, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and int(free.item()) == 0
+    assert lens.tolist() == [n] * B and cu.tolist() == [b * n for b in range(B + 1)]
+    steps = torch.arange(n, dtype=torch.int32, device="cuda")
+    for b in range(B):   # the k-th new block is free_list[total - 1 - k] = total - 1 - k
+        assert torch.equal(table[b], total - 1 - b * n - steps)
+        assert torch.equal(pos[b * n:(b + 1) * n], steps)
+        assert bool((seq_idx[b * n:(b + 1) * n] == b).all())
+    del seq_idx, pos, steps
+    free_list.fill_(-1)
+    lib.mla_release_blocks(dims, _i32([1] * B), lens, None, None, table, total, free_list, free, lens, free, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and int(free.item()) == total and lens.tolist() == [0] * B
+    assert torch.equal(free_list, table.view(-1))
