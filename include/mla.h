@@ -418,6 +418,12 @@ MLA_API int mla_decode_sparse(const mla_dims *dims, int B, int n_q, const void *
  *   shortest sequence.  num_groups == 0: nothing is shared, and both arrays may
  *   be NULL.  On the device, offsets that do not rise from 0 to B or a negative
  *   prefix length report MLA_ERR_BAD_INDEX, and then nothing is shared.
+ *   An idle slot of a group: as everywhere, a length below n_q is reported, and
+ *   as the shortest member it would also end the sharing of its group.  Give it
+ *   the length of the group's prefix (at least n_q; the prefix is read through
+ *   the first sequence's row, which has to name it) and ignore its output: it
+ *   then costs its rows only.  One without a prefix needs n_q tokens of some
+ *   block in its table row.
  *   block_table is required.  w_uv == NULL writes o_lat [B, n_q, H, d_c], as
  *   mla_decode_latent.  The other arguments, outputs and errors as mla_decode.
  *   Values that are not finite in a sequence's own rows reach that sequence
@@ -475,8 +481,10 @@ MLA_API int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *
  *     MLA_ERR_BAD_INDEX: a negative length, new_lens[b] > max_tokens (these two
  *     have no tokens in cu_seqlens), a total beyond the table row or 2^31 - 1,
  *     tokens that do not all fit max_tokens, cached_lens[b] below the group's
- *     prefix, and a prefix that is negative, not whole blocks, or longer than
- *     prefix_table.  Free ids outside [0, num_blocks) report MLA_ERR_BAD_INDEX;
+ *     prefix (but cached_lens[b] == new_lens[b] == 0 is an idle slot, as
+ *     mla_release_blocks leaves it: nothing is written for it but its length,
+ *     and nothing reported), and a prefix that is negative, not whole blocks, or
+ *     longer than prefix_table.  Free ids outside [0, num_blocks) report MLA_ERR_BAD_INDEX;
  *     the table gets -1 there, and so do the tokens.  Group offsets that do not
  *     rise from 0 to B report MLA_ERR_BAD_INDEX, and no request has a prefix.
  *   seqlens may be cached_lens itself and free_count_out may be free_count

@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanArgs 
     const int P = g >= 0 ? a.prefix_lens[g] : 0;
     bool bad = n < 0 || n > a.max_tokens;
     if (bad) n = 0;
-    bad |= c < 0 || (int64_t)c + n > room || P < 0 || P % bs != 0 || P / bs > a.max_prefix_blocks || c < P;
+    const bool idle = c == 0 && n == 0 && !bad;   // a slot without a request, as a release leaves it: nothing to refuse
+    bad |= c < 0 || (int64_t)c + n > room || P < 0 || P % bs != 0 || P / bs > a.max_prefix_blocks || (c < P && !idle);
     cu[b] = n;
     held[b] = bad ? ~max(c, 0) : c;
     if (bad || P <= 0 || c != P) gid[b] = -1;

@@ -6,6 +6,7 @@ import torch
 
 from helpers import check_close
 from test_shared_parity import Call, V2L, _heads, make_shared, reference, some
+from test_shared_serving import D as loop_dims, Loop
 
 INT_MIN, INT_MAX = -2**31, 2**31 - 1
 
@@ -94,3 +95,54 @@ def test_plan_and_release_of_nearly_2_to_31_tokens_and_blocks(lib):
     torch.cuda.synchronize()
     assert int(st.item()) == 0 and int(free.item()) == total and lens.tolist() == [0] * B
     assert torch.equal(free_list, table.view(-1))
+
+
+@pytest.mark.gpu
+def test_a_serving_loop_with_idle_slots_reports_nothing(lib):
+    """Requests finish and their slots stay free for some steps: the plan passes over them (length 0, no token), the decode is
+    given the prefix's length for them, and dev_status stays 0 at every step; later others join in their places."""
+    loop = Loop(lib)
+    new = [5, 64, 3, 130, 1, 70, 63, 90]
+    b = loop.plan(new, sum(new))
+    loop.append(loop.rnd(sum(new), loop_dims.d_model), b["seq_idx"], b["pos"], loop.table, loop.mb)
+    done = [0, 1, 0, 0, 0, 0, 1, 0]          # (not the groups' first, whose rows name the prompts)
+    lib.mla_release_blocks(loop.dims, _i32(done), loop.lens, loop.offsets, loop.prefixes, loop.table, 40, loop.free_list,
+                           loop.free_count, loop.lens, loop.free_count, loop.status)
+    assert loop.lens.tolist()[1] == loop.lens.tolist()[6] == 0
+    prefix = torch.repeat_interleave(loop.prefixes, (loop.offsets[1:] - loop.offsets[:-1]).long())
+    d, lens = loop.decode_buffers(), loop.lens
+    for step in range(3):
+        b = loop.plan([1 - x for x in done], 6)
+        loop.append(loop.rnd(6, loop_dims.d_model), b["seq_idx"], b["pos"], loop.table, loop.mb)
+        loop.lens = torch.where(lens == 0, prefix, lens)     # what the decode sees
+        loop.call_decode(d)
+        loop.check_decode(d)                                 # (the idle slots' rows are those of the prompt alone)
+        loop.lens = lens
+        torch.cuda.synchronize()
+        assert int(loop.status.item()) == 0 and lens.tolist()[1] == lens.tolist()[6] == 0
+        assert b["cu"].tolist() == [0, 1, 1, 2, 3, 4, 5, 5, 6]
+    lens[1], lens[6] = 128, 192                              # new requests behind the same prompts
+    b = loop.plan([1, 7, 1, 1, 1, 1, 2, 1], 15)
+    loop.append(loop.rnd(15, loop_dims.d_model), b["seq_idx"], b["pos"], loop.table, loop.mb)
+    loop.call_decode(d)
+    loop.check_decode(d)
+
+
+@pytest.mark.gpu
+def test_plan_idle_slots_beside_what_is_refused(lib):
+    """Length 0 without tokens behind a prefix is idle; with a token, or with tokens short of the prefix, refused."""
+    lens, new = _i32([0, 0, 64, 128, 0]), _i32([0, 1, 0, 1, 0])
+    for rows, status in (([0, 4], 0), ([0, 1], -6), ([2, 4], -6), ([3], 0)):
+        B = len(rows)
+        pick = torch.tensor(rows, device="cuda")
+        c, n, st = lens[pick].contiguous(), new[pick].contiguous(), _i32([0])
+        table, cu, free = torch.full((B, 4), -1, dtype=torch.int32, device="cuda"), _i32([0] * (B + 1)), _i32([4])
+        seq_idx, pos, out = _i32([-7] * 4), _i32([-7] * 4), torch.full_like(c, -9)
+        dims = lib.make_dims(16, 512, 64, 128, 128, 7168, 64, "bf16")
+        lib.mla_plan_step(dims, c, n, _i32([0, B]), _i32([128]), _i32([[5, 6]]), _i32([0, 1, 2, 3]), free, table, 7, out, cu, seq_idx,
+                          pos, None, free, st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == status, rows
+        if rows == [0, 4]:
+            assert out.tolist() == [0, 0] and cu.tolist() == [0, 0, 0] and (table == -1).all() and int(free.item()) == 4
+            assert (seq_idx == -7).all()
