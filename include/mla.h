@@ -430,8 +430,9 @@ MLA_API int mla_decode_sparse(const mla_dims *dims, int B, int n_q, const void *
  *   alone; in shared rows, every sequence that shares them.  out is NaN for
  *   query rows that see such a latent, also under a score of -inf (lse of such
  *   rows means nothing).
- *   Shapes of the tensor-core path (mla_decode_path) share; other shapes run
- *   every sequence by itself, with the same results.  Where they share, out and
+ *   Shapes of the tensor-core path (mla_decode_path) share; other shapes, such
+ *   as blocks that are not whole 64-token pages, run every sequence by itself,
+ *   with the same results.  Where they share, out and
  *   w_uv must be 16-byte aligned (else MLA_ERR_UNSUPPORTED), and so must c_kv
  *   and, in the row layout, k_pe (else MLA_ERR_INVALID_ARG).
  *   Workspace: >= mla_decode_shared_workspace_size bytes, 256-byte aligned.
@@ -449,8 +450,11 @@ MLA_API int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *
  * mla_plan_step — the bookkeeping of one step over the paged cache, on the GPU:
  *   block tables, sequence lengths and slot maps from the requests' lengths.
  *   The source pages have no counterpart (they do not page the cache); its
- *   outputs are the index arguments of mla_append_latent, mla_decode,
- *   mla_decode_shared and mla_prefill.
+ *   outputs are the index arguments of mla_append_latent, mla_decode and
+ *   mla_decode_shared.  mla_prefill takes cu_seqlens only where cached_lens is 0
+ *   for every request with tokens: it places a sequence's first query token at
+ *   position 0.  No call attends from more than 256 / n_heads tokens of a
+ *   request behind tokens that are cached already (such as a shared prefix).
  *   Request b holds cached_lens[b] tokens and receives new_lens[b] >= 0 more.
  *   All arrays are int32 device memory unless said otherwise.
  *   - cu_seqlens [B + 1]: prefix sums of new_lens; token t of the step belongs
@@ -538,7 +542,7 @@ MLA_API int mla_prefill_workspace_size(const mla_dims *dims, int B, int total_to
  *   o_t = softmax_{i<=t}(scale * q_t . k_i) v.
  *   cu_seqlens [B+1] (int32, device): sequence b owns query rows
  *   cu_seqlens[b] .. cu_seqlens[b+1]-1, its token t at position t; its cache
- *   (already appended) holds tokens 0 .. len-1.  q_nope [total, H, d_nope],
+ *   (already appended) holds tokens 0 .. len-1 and no earlier ones.  q_nope [total, H, d_nope],
  *   q_pe [total, H, d_R] (not rotated).  Writes out [total, H, d_v] and, if
  *   non-NULL, lse [total, H].
  */
