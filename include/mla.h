@@ -41,6 +41,10 @@
  *    dynamic shared-memory size already requested from the driver.  Each is
  *    guarded (a mutex or atomics), so first calls from several host threads
  *    are safe.
+ *  - Decodes on the tensor-core path (mla_decode_path) copy 16 bytes at a time:
+ *    c_kv and, in the row layout, k_pe at other addresses than multiples of 16
+ *    return MLA_ERR_INVALID_ARG, out, o_lat and w_uv MLA_ERR_UNSUPPORTED
+ *    (mla_decode_sparse: MLA_ERR_UNSUPPORTED for each of them).
  *  - There is no CPU fallback: a shape the CUDA kernels do not handle returns
  *    MLA_ERR_UNSUPPORTED.
  *

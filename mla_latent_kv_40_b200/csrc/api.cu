@@ -81,6 +81,15 @@ int check_ws(const DecodeLayout &L, const void *workspace, size_t ws_bytes) {
   return MLA_OK;
 }
 
+// Addresses at which the tensor-core decode copies 16 bytes at a time, where the shape takes it: asked for ahead of a call's
+// first launch.  w_uv may be NULL, and so may out where the merged rows go to the workspace.
+int check_tc_addresses(const mla_dims *dims, int n_q, const void *c_kv, const void *k_pe, const void *w_uv, const void *out) {
+  if (!tc_decode_supported(*dims, n_q)) return MLA_OK;
+  auto odd = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; };
+  if (odd(c_kv) || (dims->cache_layout != MLA_CACHE_TILED && odd(k_pe))) return MLA_ERR_INVALID_ARG;
+  return odd(w_uv) || odd(out) ? MLA_ERR_UNSUPPORTED : MLA_OK;
+}
+
 constexpr int kAllKeys = 0x7fffffff;   // kv_end of a decode over every cached key
 
 // lens_settled: see launch_tc_attention.
@@ -127,7 +136,7 @@ int decode_impl(const mla_dims *dims, int B, int n_q, const void *q_nope, const 
   if (rc) return rc;
   if (!q_nope || (!q_pe && dims->d_rope) || !w_uk || !out) return MLA_ERR_INVALID_ARG;
   const DecodeLayout L = decode_layout(dims, B, n_q, max_seqlen);
-  if ((rc = check_ws(L, workspace, ws_bytes))) return rc;
+  if ((rc = check_ws(L, workspace, ws_bytes)) || (rc = check_tc_addresses(dims, n_q, c_kv, k_pe, w_uv, out))) return rc;
   char *ws = static_cast<char *>(workspace);
   void *qbuf = ws + L.q_off;
   AbsorbArgs ab{B, n_q, dims->n_heads, dims->d_c, dims->d_rope, dims->d_nope,
@@ -323,6 +332,7 @@ int mla_decode_absorbed(const mla_dims *dims, int d_cq, int B, int n_q, const vo
     return MLA_ERR_INVALID_ARG;
   AbsorbedLayout L = absorbed_layout(dims, d_cq, B, n_q, max_seqlen);
   if (!workspace || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MLA_ERR_WORKSPACE;
+  if ((rc = check_tc_addresses(dims, n_q, c_kv, k_pe, nullptr, nullptr))) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = dims->dtype == MLA_BF16;
   char *ws = static_cast<char *>(workspace);
@@ -379,17 +389,19 @@ int mla_decode_sparse(const mla_dims *dims, int B, int n_q, const void *q_nope, 
   int32_t *counts = reinterpret_cast<int32_t *>(ws + L.counts_off);
   char *pool = ws + L.pool_off;
   char *dws = ws + L.dec_off;
+  const CacheView src{c_kv, k_pe, dims->ckv_stride, dims->kpe_stride, block_table, max_blocks_per_seq, num_blocks,
+                      dims->block_size, dims->cache_layout, dims->d_c, dims->d_c + dims->d_rope};
+  const bool tiled = L.inner.cache_layout == MLA_CACHE_TILED;
+  if (!sparse_gather_supported(src, pool, tiled, (int)elem(dims))) return MLA_ERR_UNSUPPORTED;
+  int rc = check_tc_addresses(&L.inner, 1, pool, pool, w_uv, out);
+  if (rc) return rc;
   // (1) Query absorption at each token's own position (the real sequence lengths).
   void *qbuf = dws + L.dec.q_off;
   AbsorbArgs ab{B, n_q, dims->n_heads, dims->d_c, dims->d_rope, dims->d_nope,
                 q_nope, q_pe, w_uk, seqlens, qbuf, dims->rope_base};
-  int rc = absorb_dispatch(ab, dims->dtype == MLA_BF16, dev_status, st);
-  if (rc) return rc;
+  if ((rc = absorb_dispatch(ab, dims->dtype == MLA_BF16, dev_status, st))) return rc;
   // (2) The listed rows of every query token into its own pages of the gathered pool.
-  CacheView src{c_kv, k_pe, dims->ckv_stride, dims->kpe_stride, block_table, max_blocks_per_seq, num_blocks,
-                dims->block_size, dims->cache_layout, dims->d_c, dims->d_c + dims->d_rope};
-  if ((rc = launch_sparse_gather(B, n_q, topk, topk_idx, seqlens, max_seqlen, src, pool,
-                                 L.inner.cache_layout == MLA_CACHE_TILED, (int)elem(dims), counts, dev_status, st)))
+  if ((rc = launch_sparse_gather(B, n_q, topk, topk_idx, seqlens, max_seqlen, src, pool, tiled, (int)elem(dims), counts, dev_status, st)))
     return rc;
   // (3) + (4) Attention over the gathered pool (every listed key visible to its own query) and combine.
   const mla_dims *in = &L.inner;
@@ -444,10 +456,7 @@ int mla_decode_shared(const mla_dims *dims, int B, int n_q, const void *q_nope, 
   if (!q_nope || (!q_pe && dims->d_rope) || !w_uk || !out) return MLA_ERR_INVALID_ARG;
   const SharedLayout L = shared_layout(dims, B, n_q, num_groups);
   if (!workspace || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MLA_ERR_WORKSPACE;
-  const bool tiled = dims->cache_layout == MLA_CACHE_TILED;
-  if ((reinterpret_cast<uintptr_t>(c_kv) & 15) || (!tiled && (reinterpret_cast<uintptr_t>(k_pe) & 15)))
-    return MLA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(out) & 15) || (reinterpret_cast<uintptr_t>(w_uv) & 15)) return MLA_ERR_UNSUPPORTED;
+  if ((rc = check_tc_addresses(dims, n_q, c_kv, k_pe, w_uv, out))) return rc;
   char *ws = static_cast<char *>(workspace);
   void *qbuf = ws + L.q_off;
   const SharedPlan pl{reinterpret_cast<SharedShare *>(ws + L.shares_off), reinterpret_cast<SharedUnit *>(ws + L.units_off),
@@ -590,6 +599,7 @@ int mla_decode_step(const mla_dims *dims, int B, int n_q, const void *h_new, con
     return MLA_ERR_INVALID_ARG;
   const StepLayout L = step_layout(dims, B, n_q, max_seqlen);
   if (!workspace || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MLA_ERR_WORKSPACE;
+  if ((rc = check_tc_addresses(dims, n_q, c_kv, k_pe, w_uv, out))) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   const int T = B * n_q;

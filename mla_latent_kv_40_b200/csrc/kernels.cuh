@@ -225,6 +225,7 @@ int launch_gemm(const GemmArgs &g, bool bf16, cudaStream_t st);
 int launch_rope_into_query(int B, int n_q, int H, int d_c, int d_rope, const void *q_pe_raw, const int32_t *seqlens,
                            void *q_abs, float rope_base, bool bf16, cudaStream_t st);
 // Sparse decode: compact each query token's listed cache rows into its own run of 64-token pages.
+bool sparse_gather_supported(const CacheView &src, const void *pool, bool dst_tiled, int elem);
 int launch_sparse_gather(int B, int n_q, int topk, const int32_t *idx, const int32_t *seqlens, int max_seqlen,
                          const CacheView &src, void *pool, bool dst_tiled, int elem, int32_t *counts,
                          int *dev_status, cudaStream_t st);

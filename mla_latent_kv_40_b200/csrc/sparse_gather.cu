@@ -91,18 +91,31 @@ sparse_gather_kernel(int n_q, int topk, int pages, const int32_t *idx, const int
 
 }  // namespace
 
+namespace {
+
+// 16-byte items need every 16-byte group of a row to lie inside one contiguous, aligned piece.
+bool whole_groups(const CacheView &src, const void *pool, int elem) {
+  const int per = 16 / elem;
+  const bool vec16 = src.W % per == 0 && (src.d_c % per == 0) && !(reinterpret_cast<uintptr_t>(pool) & 15) &&
+                     !(reinterpret_cast<uintptr_t>(src.c_kv) & 15);
+  return vec16 && (src.layout != MLA_CACHE_ROWS ||
+                   ((src.ckv_stride * elem) % 16 == 0 && (src.kpe_stride * elem) % 16 == 0 &&
+                    !(reinterpret_cast<uintptr_t>(src.k_pe) & 15)));
+}
+
+}  // namespace
+
+// (The tiled layout moves whole 16-byte groups.)
+bool sparse_gather_supported(const CacheView &src, const void *pool, bool dst_tiled, int elem) {
+  return !dst_tiled || whole_groups(src, pool, elem);
+}
+
 int launch_sparse_gather(int B, int n_q, int topk, const int32_t *idx, const int32_t *seqlens, int max_seqlen,
                          const CacheView &src, void *pool, bool dst_tiled, int elem, int32_t *counts,
                          int *dev_status, cudaStream_t st) {
   const int pages = (topk + kPage - 1) / kPage;
-  // 16-byte items need every 16-byte group of a row to lie inside one contiguous, aligned piece.
-  const int per = 16 / elem;
-  bool vec16 = src.W % per == 0 && (src.d_c % per == 0) &&
-               !(reinterpret_cast<uintptr_t>(pool) & 15) && !(reinterpret_cast<uintptr_t>(src.c_kv) & 15);
-  if (src.layout == MLA_CACHE_ROWS)
-    vec16 = vec16 && (src.ckv_stride * elem) % 16 == 0 && (src.kpe_stride * elem) % 16 == 0 &&
-            !(reinterpret_cast<uintptr_t>(src.k_pe) & 15);
-  if (dst_tiled && !vec16) return MLA_ERR_UNSUPPORTED;   // the tiled layout moves whole 16-byte groups
+  if (!sparse_gather_supported(src, pool, dst_tiled, elem)) return MLA_ERR_UNSUPPORTED;
+  const bool vec16 = whole_groups(src, pool, elem);
   sparse_gather_kernel<<<dim3(B * n_q, pages), kThreads, 0, st>>>(n_q, topk, pages, idx, seqlens, max_seqlen, src,
                                                                   static_cast<unsigned char *>(pool), dst_tiled,
                                                                   vec16, elem, counts, dev_status);
