@@ -146,3 +146,35 @@ def test_plan_idle_slots_beside_what_is_refused(lib):
         if rows == [0, 4]:
             assert out.tolist() == [0, 0] and cu.tolist() == [0, 0, 0] and (table == -1).all() and int(free.item()) == 4
             assert (seq_idx == -7).all()
+
+
+@pytest.mark.gpu
+def test_the_current_stream_with_and_without_torch_s_private_handle(lib, monkeypatch):
+    """The small calls ask for the current stream's handle directly, or, where this torch has no such call, as the others do:
+    the same stream, by default, in a stream context and where one is given."""
+    side = torch.cuda.Stream()
+    dev = torch.cuda.current_device()
+
+    def handles():
+        default = lib._raw_stream(None, dev)
+        with torch.cuda.stream(side):
+            inside = lib._raw_stream(None, dev)
+        return default, inside, lib._raw_stream(side, dev)
+
+    want = (torch.cuda.current_stream().cuda_stream, side.cuda_stream, side.cuda_stream)
+    assert handles() == want
+    monkeypatch.setattr(lib, "_current_handle", None)
+    assert handles() == want
+    inp = make_shared(V2L, [(128, [200, 300, 150])], 1, 64, seed=19)
+    c = Call(lib, inp)
+    with torch.cuda.stream(side):
+        c.run()
+    side.synchronize()
+    first = c.out.clone()
+    monkeypatch.undo()
+    c.out.zero_()
+    with torch.cuda.stream(side):
+        side.wait_stream(torch.cuda.default_stream())
+        c.run()
+    side.synchronize()
+    assert torch.equal(first, c.out)
