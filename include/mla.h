@@ -434,6 +434,8 @@ MLA_API int mla_decode_sparse(const mla_dims *dims, int B, int n_q, const void *
  *   alone; in shared rows, every sequence that shares them.  out is NaN for
  *   query rows that see such a latent, also under a score of -inf (lse of such
  *   rows means nothing).
+ *   It pays where a group's shared tokens are several times its sequences' own
+ *   ones and groups are few; otherwise mla_decode is the faster call.
  *   Shapes of the tensor-core path (mla_decode_path) share; other shapes, such
  *   as blocks that are not whole 64-token pages, run every sequence by itself,
  *   with the same results.  Where they share, out and

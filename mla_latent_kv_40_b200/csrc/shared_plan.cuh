@@ -9,9 +9,9 @@
 // while the MMAs wait; about 10 us against 1.4 us per tile).  Tile i of unit u has place cost0[u] + i in a list of length
 // W, cost0[u] = tiles before u + kUnitCost (non-empty units before u), and cluster c's share is
 // [floor(c W / C), floor((c + 1) W / C)).  Where there are no more units than clusters and the longest is no longer than such
-// a share, every unit has a cluster to itself: no unit is cut (64 sequences of 128 heads, 32 units: 97.6 us a call instead
-// of 104.1, most of it in the merge).  Filling the clusters greedily to the least load that 33 of them manage (32 loads
-// tried at once) took 9 us: not worth it.
+// a share, every unit has a cluster to itself: no unit is cut (64 sequences of 128 heads, 32 units: 106.8 us a call instead
+// of 109.0, or 99.6 instead of 106.2 with the buffers placed otherwise; most of it in the merge).  Filling the clusters
+// greedily to the least load that 33 of them manage (32 loads tried at once) took 9 us: not worth it.
 #pragma once
 
 #include "shared_tc.cuh"

@@ -17,8 +17,9 @@
 //   * much work: kBodyCtas CTAs that leave those outputs alone, and a second launch of one CTA that forms the sums again
 //     (while the first kernel runs) and writes them once that has finished.
 // No atomics: the result does not depend on timing.  The call is bound by latency (the dependent loads of the scan and
-// of the search), not by its bytes.  Measured (device): plan of 64 requests with one token each 10.7 us, of 256 with 16 to
-// 1024 tokens 12.1, of 4096 with 4 to 32 tokens 19.3 (two launches); release of 64 requests 6.0 us, of 4096 11.7.
+// of the search), not by its bytes.  Measured (device, several boxes): plan of 64 requests with one token each 10.6 to 13.6 us,
+// of 256 with 16 to 1024 tokens 11.9 to 13.5, of 4096 with 4 to 32 tokens 19.3 to 20.4 (two launches); release of 64 requests
+// 6.2 us, of 4096 11.5.
 #include "kernels.cuh"
 #include "sm100.cuh"
 

@@ -4,6 +4,8 @@ The result is that of an ordinary decode of every sequence through its own block
 the reference.  Bars: those of the other decode tests (tests/helpers.py): queries, P, partial outputs and the merged
 o_lat are each rounded to bf16 once (2^-8 relative at most each, fp32 between), four independent roundings of random
 sign: 2 * 2^-8 / sqrt(3) = 4.5e-3 of the output's norm, below the 1e-2 bar; fp32 paths keep 1e-4.
+(Partials are in fp32 by now and the merged row meets W_UV in two bf16 parts: queries, P and the output remain, some 2.5e-3.
+The bar counts more than is rounded; tests/test_shared_rows.py has bounds of every row by its own arithmetic.)
 """
 import ctypes
 
