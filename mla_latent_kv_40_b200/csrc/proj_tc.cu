@@ -272,8 +272,9 @@ __device__ __forceinline__ void append_tc_body(const CUtensorMap &map_wd, const 
       load_h(i);
     }
   } else if (tid == 32) {
-    // MMA issuer.
+    // MMA issuer.  (The limit of its waits begins when the hidden states may be loaded.)
     const uint32_t idesc = idesc_bf16_f32(128, kTcN, true, false);
+    grid_dep_wait();
     for (int i = 0; i < nst; ++i) {
       const int st = i % kApStages;
       if (!wait_bar(smem_u32(&bar_full[st]), (i / kApStages) & 1, dev_status)) { ok = 0; break; }

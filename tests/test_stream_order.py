@@ -36,7 +36,7 @@ extern "C" int produce(const void *src, void *dst, int n, unsigned long long ns,
 
 @pytest.fixture(scope="module")
 def produce(tmp_path_factory):
-    """produce(src, dst): dst = src, 50 us later, from a kernel that lets its dependents start at once."""
+    """produce(src, dst): dst = src, 50 us (or `ns`) later, from a kernel that lets its dependents start at once."""
     d = tmp_path_factory.mktemp("producer")
     src, out = d / "producer.cu", d / "producer.so"
     src.write_text(PRODUCER)
@@ -46,9 +46,9 @@ def produce(tmp_path_factory):
     so = ctypes.CDLL(str(out))
     so.produce.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_ulonglong, ctypes.c_void_p]
 
-    def run(a, b):
+    def run(a, b, ns=50000):
         assert a.is_contiguous() and b.is_contiguous() and a.numel() * a.element_size() % 4 == 0 and a.shape == b.shape
-        assert so.produce(a.data_ptr(), b.data_ptr(), a.numel() * a.element_size() // 4, 50000,
+        assert so.produce(a.data_ptr(), b.data_ptr(), a.numel() * a.element_size() // 4, ns,
                           torch.cuda.current_stream().cuda_stream) == 0
 
     return run
@@ -219,3 +219,40 @@ def test_a_decode_that_takes_what_the_call_ahead_wrote(lib):
     for _ in range(20):
         for a, b in zip(chain(False), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("entry", ["append", "step", "decode", "attention", "shared"])
+def test_a_producer_that_takes_longer_than_a_bounded_wait(lib, produce, entry):
+    """The waits inside the kernels give up after 2 s; what is ahead on the stream may take longer."""
+    if entry == "shared":
+        inp = make_shared(Dims(**V2_LITE), [(640, [700, 650, 900, 641]), (128, [300, 129])], 1, 64, seed=53)
+        c = Call(lib, inp)
+        run, lens = c.run, c.dev["seqlens"]
+
+        def result():
+            return c.result()
+    else:
+        s = Step(lib, 1)
+        s.entry = entry
+        s.call("absorb")
+        s.keep_q = s.q_abs.clone()
+        s.reset()
+        lens = s.dev["h_new"] if entry in ("append", "step") else s.dev["seqlens"]
+
+        def run():
+            s.call(entry)
+
+        def result():
+            torch.cuda.synchronize()
+            got = s.out.float().cpu().numpy(), s.pool.view(torch.int16).cpu().numpy(), int(s.status.item())
+            s.reset()
+            return got
+
+    run()
+    want = result()
+    produce(lens.clone(), lens, 2300000000)
+    run()
+    got = result()
+    assert got[2] == want[2] == 0
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
