@@ -424,10 +424,10 @@ MLA_API int mla_decode_sparse(const mla_dims *dims, int B, int n_q, const void *
  *   prefix length report MLA_ERR_BAD_INDEX, and then nothing is shared.
  *   An idle slot of a group: as everywhere, a length below n_q is reported, and
  *   as the shortest member it would also end the sharing of its group.  Give it
- *   the length of the group's prefix (at least n_q; the prefix is read through
- *   the first sequence's row, which has to name it) and ignore its output: it
- *   then costs its rows only.  One without a prefix needs n_q tokens of some
- *   block in its table row.
+ *   the length of the group's prefix plus n_q - 1 and ignore its output: it then
+ *   costs its rows only.  (Its table row names the prefix's blocks where it is
+ *   the group's first sequence, and with n_q > 1 any one block behind them.)
+ *   One without a prefix needs n_q tokens of some block in its table row.
  *   block_table is required.  w_uv == NULL writes o_lat [B, n_q, H, d_c], as
  *   mla_decode_latent.  The other arguments, outputs and errors as mla_decode.
  *   Values that are not finite in a sequence's own rows reach that sequence

@@ -178,3 +178,25 @@ def test_the_current_stream_with_and_without_torch_s_private_handle(lib, monkeyp
         c.run()
     side.synchronize()
     assert torch.equal(first, c.out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n_q", [1, 2, 4])
+def test_shared_idle_slots_as_the_header_says(lib, n_q):
+    """A slot given the prefix's length plus n_q - 1, with a table row that names nothing of the prefix (it is not the first) and
+    for n_q > 1 one block behind it: nothing is reported, and the others have the bits that they have beside a real
+    member of that length."""
+    P = 256
+    inp = make_shared(V2L, [(P, [300, P + n_q - 1, 320, 500])], n_q, 64, seed=23)
+    full = Call(lib, inp)
+    full.run()
+    want, want_lse, st = full.result()
+    assert st == 0
+    table = inp["block_table"].clone()
+    table[1] = -1
+    table[1, P // 64 if n_q > 1 else 0] = 0
+    idle = Call(lib, dict(inp, block_table=table))
+    idle.run()
+    got, lse, st = idle.result()
+    others = [0, 2, 3]
+    assert st == 0 and np.array_equal(got[others], want[others]) and np.array_equal(lse[others], want_lse[others])
